@@ -455,6 +455,125 @@ nosa_status nosa_sparse_attention_noalloc(const nosa_config* cfg, const void* un
                                           int32_t n_blocks, const void* tail, int32_t tail_len,
                                           const void* q, void* out, float* lse, void* stream);
 
+/*
+ * 8-bit block cache: a caller-owned KV cache whose full blocks are held in 8 bits
+ * with one scale for the keys and one for the values of each block and head, the
+ * attention that reads it, and eviction by accumulated attention weight. (The NOSA
+ * pages have no counterpart: it serves callers whose cache stays on the GPU and
+ * either must hold more tokens in the same memory or must not grow at all.)
+ *
+ * State, all of it device memory that the caller allocates; U = batch * n_kv_heads,
+ * and only the shape fields of cfg are used:
+ *   units     : n_units 8-bit block units of nosa_quant_unit_bytes(cfg) bytes
+ *   block_tab : int32 [U][max_blocks], the unit of each block of a (request, KV
+ *               head), oldest first. The entries past the full blocks name the units
+ *               that appended tokens fill next. No unit that is appended to may be
+ *               named twice.
+ *   tail      : one block unit of cfg's dtype (layout above) per (request, KV head):
+ *               its newest lens % 64 tokens, not quantised
+ *   lens      : int32 [U], tokens held: lens / 64 full blocks, then the tail.
+ *               0 <= lens <= 64 * max_blocks; units differ freely.
+ *   mass      : fp32 [U][max_blocks], the attention weight that each block has
+ *               accumulated; entry lens / 64 is the tail's. Zeros at the start.
+ *
+ * 8-bit unit (d = head_dim; 8480 bytes for d = 64, 16672 for d = 128):
+ *   bytes [0, 128 d)      : four slices of 16 tokens, each 16 d key codes, then 16 d
+ *                           value codes, in the order in which a warp's lanes feed
+ *                           them to the tensor cores. With tt = t % 16 the code of
+ *                           token t, dim x is at  32 d (t / 16)  +
+ *     key   : 16 (32 (x / 32) + 4 (2 (tt / 4) + tt % 2) + x % 16 / 4)
+ *                + 4 (2 (x % 32 / 16) + tt % 4 / 2) + x % 4
+ *     value : 16 d + 16 (32 (x / 32) + 4 (x % 8) + tt / 4) + 4 (x % 32 / 8) + tt % 4
+ *   bytes [128 d, +256)   : fp32 eviction logits of the 64 tokens
+ *   then fp32 key scale, fp32 value scale, zeros to a multiple of 32 bytes.
+ * A code is an e4m3 number (4 exponent bits, 3 mantissa bits, largest 448) and
+ * stands for code * scale.
+ *
+ * Device status: calls take `status`, a device int32 word or NULL, and OR bits into
+ * it (they never clear it): NOSA_QUANT_WAIT a bounded wait in a kernel gave up,
+ * NOSA_QUANT_INDEX a table entry, length or count out of range, NOSA_QUANT_CAPACITY
+ * tokens that did not fit. A table entry out of range is skipped, a length out of
+ * range makes the unit empty for attention and leaves it as it was elsewhere, a count
+ * is clamped.
+ *
+ * Strides: k_strides, v_strides, q_strides are NULL (contiguous) or three host
+ * values: elements between requests, tokens and heads of the array, each >= 0 and a
+ * multiple of 16 bytes; the head_dim elements of a row are consecutive.
+ *
+ * All calls are async and can be captured; none allocates. max_blocks <= 16384.
+ */
+#define NOSA_QUANT_WAIT 1
+#define NOSA_QUANT_INDEX 2
+#define NOSA_QUANT_CAPACITY 4
+
+/* Bytes of an 8-bit block unit (0 if cfg is invalid). */
+size_t nosa_quant_unit_bytes(const nosa_config* cfg);
+
+/*
+ * Appends n_tokens tokens per request (n_new[b] <= n_tokens of them where n_new is
+ * not NULL: the first ones). Tokens enter the tail; a block that fills up is
+ * quantised and stored in the unit that block_tab names for it:
+ *   scale = max |x| / 448 over the elements of its tokens whose logit is not -inf,
+ *   code  = e4m3(x * (448 / max |x|)), to nearest, ties to even;
+ * tokens with logit -inf (masked) become zeros. A maximum below 2^-100 gives scale 0
+ * and zeros; a NaN or infinity in a token that is not masked gives scale NaN (the
+ * block's keys or values are then NaN, and so is what attends to it).
+ *   k, v     : device [batch][n_tokens][n_kv_heads][head_dim] of cfg dtype
+ *   e        : device fp32 [batch][n_tokens][n_kv_heads], or NULL: zeros
+ *   lens_out : int32 [U], receives the new lengths; may be lens
+ * A unit that the tokens would take past 64 * max_blocks is left as it was
+ * (NOSA_QUANT_CAPACITY). Tail rows at and past the new lens % 64 keep their bytes.
+ */
+nosa_status nosa_quant_append(const nosa_config* cfg, int32_t max_blocks, int32_t n_tokens,
+                              const void* k, const int64_t* k_strides, const void* v,
+                              const int64_t* v_strides, const float* e, const int32_t* n_new,
+                              void* units, int64_t n_units, const int32_t* block_tab, void* tail,
+                              const int32_t* lens, int32_t* lens_out, int32_t* status,
+                              void* stream);
+
+/*
+ * Attention of the newest n_queries tokens of every request (1 <= n_queries <= 128;
+ * q_len[b] <= n_queries of them where q_len is not NULL: the first rows) over the
+ * cache, which holds them already: query t of request b sees the first
+ * lens - q_len[b] + t + 1 tokens of its unit. Logits are q.k / sqrt(d) + e; a token
+ * with e = -inf is masked and contributes nothing whatever its key and value hold.
+ * A row that sees no token gives out = 0, lse = -inf. Sums and the softmax are held
+ * in fp32, the products take 11-bit (bf16) or 22-bit (fp32) operands.
+ *   q    : device [batch][n_queries][n_q_heads][head_dim] of cfg dtype
+ *   out  : the same shape, contiguous (written; rows past q_len[b] are left)
+ *   lse  : device fp32 [batch][n_queries][n_q_heads] or NULL
+ *   mass : fp32 [U][max_blocks] or NULL. Every entry becomes decay * mass plus, where
+ *          it has tokens, their softmax weights, summed over the request's queries and
+ *          the query heads of the KV head; 0 <= decay <= 1 (0 overwrites).
+ *   workspace : device, nosa_quant_attention_workspace_bytes(...) bytes, 256-byte
+ *          aligned; scratch that calls on one stream (or graphs that do not overlap)
+ *          may share. The size is that of cfg's device.
+ */
+size_t nosa_quant_attention_workspace_bytes(const nosa_config* cfg, int32_t max_blocks,
+                                            int32_t n_queries, int32_t with_mass);
+nosa_status nosa_quant_attention(const nosa_config* cfg, int32_t max_blocks, int32_t n_queries,
+                                 const void* units, int64_t n_units, const int32_t* block_tab,
+                                 const void* tail, const int32_t* lens, const void* q,
+                                 const int64_t* q_strides, const int32_t* q_len, void* out,
+                                 float* lse, float* mass, float decay, void* workspace,
+                                 size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * Eviction: every unit with more than `budget` full blocks keeps its newest n_recent
+ * (0 <= n_recent <= budget) and, of the others, the budget - n_recent of the largest
+ * mass (ties keep the lower index; NaN ranks above every number). The table row
+ * becomes the kept blocks in their order, then the evicted ones (the next
+ * destinations of appended blocks), then the rest as it was; mass moves along, the
+ * evicted blocks' becomes 0, and lens shrinks by 64 per evicted block. The tail and
+ * the units are not touched.
+ *   tab_out, mass_out, lens_out : as block_tab, mass, lens; each may be the input
+ *   order : int32 [U][max_blocks] or NULL: the table index that each entry had
+ */
+nosa_status nosa_quant_evict(const nosa_config* cfg, int32_t max_blocks, int32_t budget,
+                             int32_t n_recent, const int32_t* block_tab, const float* mass,
+                             const int32_t* lens, int32_t* tab_out, float* mass_out,
+                             int32_t* lens_out, int32_t* order, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

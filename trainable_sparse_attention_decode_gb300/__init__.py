@@ -25,12 +25,15 @@ __all__ = [
     "nosa_selftest_bounded_wait", "nosa_frontend_rows", "nosa_decode_step_hidden",
     "nosa_frontend_packed_bytes", "nosa_frontend_pack", "nosa_prefill_workspace_bytes",
     "nosa_prefill_forward", "nosa_prefill_device_error", "nosa_prefill_timing",
-    "nosa_numa_choose",
+    "nosa_numa_choose", "NOSA_QUANT_WAIT", "NOSA_QUANT_INDEX", "NOSA_QUANT_CAPACITY",
+    "nosa_quant_unit_bytes", "nosa_quant_append", "nosa_quant_attention_workspace_bytes",
+    "nosa_quant_attention", "nosa_quant_evict",
 ]
 
 NOSA_F32, NOSA_BF16 = 0, 1
 NOSA_FLAG_TIMING = 1
 NOSA_FLAG_POOLED_BF16 = 2
+NOSA_QUANT_WAIT, NOSA_QUANT_INDEX, NOSA_QUANT_CAPACITY = 1, 2, 4
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "OOM", 3: "HOST_OOM", 4: "CAPACITY", 5: "CUDA",
           6: "STATE", 7: "UNSUPPORTED"}
 DBG = {name: i for i, name in enumerate(
@@ -101,6 +104,14 @@ def _load():
         "nosa_prefill_device_error": (C.c_int, [P(NosaConfig), I32, VP, P(I32)]),
         "nosa_prefill_timing": (C.c_int, [P(C.c_float), P(C.c_float)]),
         "nosa_numa_choose": (I32, [I32, P(I32), I32, P(I32), I32]),
+        "nosa_quant_unit_bytes": (SZ, [P(NosaConfig)]),
+        "nosa_quant_append": (C.c_int, [P(NosaConfig), I32, I32, VP, VP, VP, VP, VP, VP, VP,
+                                        C.c_int64, VP, VP, VP, VP, VP, VP]),
+        "nosa_quant_attention_workspace_bytes": (SZ, [P(NosaConfig), I32, I32, I32]),
+        "nosa_quant_attention": (C.c_int, [P(NosaConfig), I32, I32, VP, C.c_int64, VP, VP, VP, VP,
+                                           VP, VP, VP, VP, VP, C.c_float, VP, SZ, VP, VP]),
+        "nosa_quant_evict": (C.c_int, [P(NosaConfig), I32, I32, I32, VP, VP, VP, VP, VP, VP, VP,
+                                       VP, VP]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(L, name)
@@ -390,3 +401,127 @@ def nosa_sparse_attention_noalloc(cfg: NosaConfig, units, block_tab, tail, tail_
         _ptr(tail, None, torch.uint8, "tail", allow_none=True), int(tail_len),
         _ptr(q, qs, dt, "q"), _ptr(out, qs, dt, "out"),
         _ptr(lse, qs[:2], torch.float32, "lse", 4, allow_none=True), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit block cache (state and layouts: include/nosa.h)
+# ---------------------------------------------------------------------------
+def _on(cfg: NosaConfig, t, shape, dtype, what, align=4, allow_none=False):
+    """_ptr for a tensor that must live on cfg's device."""
+    if t is not None and t.is_cuda and t.get_device() != cfg.device:
+        raise ValueError(f"{what} is on cuda:{t.get_device()}, the configuration's device is "
+                         f"cuda:{cfg.device}")
+    return _ptr(t, shape, dtype, what, align, allow_none)
+
+
+def _rows(cfg: NosaConfig, t, shape, dtype, what):
+    """Pointer and strides (None where contiguous) of [batch][n][heads][d] rows."""
+    if t is None or t.is_contiguous():
+        return _on(cfg, t, shape, dtype, what, 16), None
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"{what}: the elements of a row must be consecutive")
+    row = t[0, 0, 0] if t.numel() else t.reshape(-1)
+    return _on(cfg, row, None, dtype, what, 16), (C.c_int64 * 3)(*st[:3])
+
+
+def _units(cfg: NosaConfig, t):
+    """Pointer and number of the 8-bit units in t."""
+    size = nosa_quant_unit_bytes(cfg)
+    n, rest = divmod(t.numel(), size) if size else (0, 0)
+    if rest:
+        raise ValueError(f"units must hold whole units of {size} bytes")
+    return _on(cfg, t, None, _torch().uint8, "units", 16), n
+
+
+def _device_stream(cfg: NosaConfig, stream):
+    """The given stream, or the current one of cfg's device."""
+    return _stream(_torch().cuda.current_stream(cfg.device) if stream is None else stream)
+
+
+def nosa_quant_unit_bytes(cfg: NosaConfig) -> int:
+    return int(lib.nosa_quant_unit_bytes(C.byref(cfg)))
+
+
+def nosa_quant_append(cfg: NosaConfig, k, v, e, units, block_tab, tail, lens, lens_out=None,
+                      n_new=None, status=None, stream=None):
+    """Appends tokens k, v [batch][n][Hkv][d] (rows may be strided), e [batch][n][Hkv] fp32 or
+    None to the cache (units, block_tab, tail, lens), quantising the blocks that fill up.
+    The new lengths go to lens_out (lens itself by default); n_new [batch] int32 gives the
+    valid tokens of each request."""
+    torch = _torch()
+    U = cfg.batch * cfg.n_kv_heads
+    dt, i32 = _dtype_of(cfg), torch.int32
+    n, blocks = k.shape[1], block_tab.shape[1]
+    shp = (cfg.batch, n, cfg.n_kv_heads, cfg.head_dim)
+    kp, ks = _rows(cfg, k, shp, dt, "k")
+    vp, vs = _rows(cfg, v, shp, dt, "v")
+    up, nu = _units(cfg, units)
+    lp = _on(cfg, lens, (U,), i32, "lens")
+    if tail.numel() != U * nosa_payload_bytes(cfg):
+        raise ValueError("tail must hold one block unit per request and KV head")
+    _check(lib.nosa_quant_append(
+        C.byref(cfg), blocks, n, kp, ks, vp, vs,
+        _on(cfg, e, shp[:3], torch.float32, "e", allow_none=True),
+        _on(cfg, n_new, (cfg.batch,), i32, "n_new", allow_none=True), up, nu,
+        _on(cfg, block_tab, (U, blocks), i32, "block_tab"),
+        _on(cfg, tail, None, torch.uint8, "tail", 16), lp,
+        lp if lens_out is None else _on(cfg, lens_out, (U,), i32, "lens_out"),
+        _on(cfg, status, (1,), i32, "status", allow_none=True), _device_stream(cfg, stream)))
+
+
+def nosa_quant_attention_workspace_bytes(cfg: NosaConfig, max_blocks: int, n_queries: int = 1,
+                                         with_mass: bool = False) -> int:
+    return int(lib.nosa_quant_attention_workspace_bytes(C.byref(cfg), max_blocks, n_queries,
+                                                        1 if with_mass else 0))
+
+
+def nosa_quant_attention(cfg: NosaConfig, units, block_tab, tail, lens, q, out, lse=None, mass=None,
+                         decay=1.0, q_len=None, workspace=None, status=None, stream=None):
+    """Attention of the newest tokens' queries q [batch][n][Hq][d] (rows may be strided) over the
+    cache; writes out (and lse [batch][n][Hq]) and, given mass [U][max_blocks], accumulates the
+    blocks' attention weight. Returns the workspace (allocated here when not passed)."""
+    torch = _torch()
+    U = cfg.batch * cfg.n_kv_heads
+    dt, i32, f32 = _dtype_of(cfg), torch.int32, torch.float32
+    n, blocks = q.shape[1], block_tab.shape[1]
+    shp = (cfg.batch, n, cfg.n_q_heads, cfg.head_dim)
+    qp, qs = _rows(cfg, q, shp, dt, "q")
+    up, nu = _units(cfg, units)
+    if tail.numel() != U * nosa_payload_bytes(cfg):
+        raise ValueError("tail must hold one block unit per request and KV head")
+    if workspace is None:
+        workspace = torch.empty(
+            nosa_quant_attention_workspace_bytes(cfg, blocks, n, mass is not None),
+            dtype=torch.uint8, device=q.device)
+    _check(lib.nosa_quant_attention(
+        C.byref(cfg), blocks, n, up, nu, _on(cfg, block_tab, (U, blocks), i32, "block_tab"),
+        _on(cfg, tail, None, torch.uint8, "tail", 16), _on(cfg, lens, (U,), i32, "lens"), qp, qs,
+        _on(cfg, q_len, (cfg.batch,), i32, "q_len", allow_none=True),
+        _on(cfg, out, shp, dt, "out", 16),
+        _on(cfg, lse, shp[:3], f32, "lse", allow_none=True),
+        _on(cfg, mass, (U, blocks), f32, "mass", allow_none=True), decay,
+        _on(cfg, workspace, None, torch.uint8, "workspace", 256), workspace.numel(),
+        _on(cfg, status, (1,), i32, "status", allow_none=True), _device_stream(cfg, stream)))
+    return workspace
+
+
+def nosa_quant_evict(cfg: NosaConfig, budget, n_recent, block_tab, mass, lens, tab_out=None,
+                     mass_out=None, lens_out=None, order=None, status=None, stream=None):
+    """Evicts the blocks of least accumulated weight from every unit with more than `budget` full
+    blocks (its newest n_recent stay). Works in place unless outputs are given."""
+    torch = _torch()
+    U, blocks = cfg.batch * cfg.n_kv_heads, block_tab.shape[1]
+    i32, f32 = torch.int32, torch.float32
+    tp = _on(cfg, block_tab, (U, blocks), i32, "block_tab")
+    mp = _on(cfg, mass, (U, blocks), f32, "mass")
+    lp = _on(cfg, lens, (U,), i32, "lens")
+    _check(lib.nosa_quant_evict(
+        C.byref(cfg), blocks, int(budget), int(n_recent), tp, mp, lp,
+        tp if tab_out is None else _on(cfg, tab_out, (U, blocks), i32, "tab_out"),
+        mp if mass_out is None else _on(cfg, mass_out, (U, blocks), f32, "mass_out"),
+        lp if lens_out is None else _on(cfg, lens_out, (U,), i32, "lens_out"),
+        _on(cfg, order, (U, blocks), i32, "order", allow_none=True),
+        _on(cfg, status, (1,), i32, "status", allow_none=True), _device_stream(cfg, stream)))

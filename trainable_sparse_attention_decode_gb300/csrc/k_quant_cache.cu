@@ -1,0 +1,380 @@
+// Write side of the 8-bit block cache: appending tokens and evicting blocks.
+#include "k_quant.cuh"
+
+#include <algorithm>
+
+namespace nosa {
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+// Eight consecutive elements as fp32.
+template <typename T> struct Row8;
+template <> struct Row8<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const void* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x); f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
+    f[4] = bf16_lo(r.z); f[5] = bf16_hi(r.z); f[6] = bf16_lo(r.w); f[7] = bf16_hi(r.w);
+  }
+};
+template <> struct Row8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
+
+// Four fp32 values as four e4m3 codes (round to nearest even), the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// Quantises block j of the unit's new blocks (0: the one that the tail began) and
+// stores it: x -> e4m3(x * (448 / max |x|)), the maximum over the block's tokens
+// whose logit is not -inf; the others become zeros. A thread owns patches of 4
+// tokens x 8 dims, the smallest piece whose key and value words are whole, so the
+// block stays in registers between the maximum and the conversion and the input
+// is read once; the image is put together in shared memory and leaves in 16-byte
+// stores.
+template <typename T, int D>
+__device__ void quant_block(const QAppendArgs& p, int Hkv, int u, int j, int n0, const uint8_t* tail,
+                            uint8_t* img, uint32_t* red) {
+  constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NT = kAppendThreads;
+  constexpr int NP = 16 * (D / 8);  // patches of K (and of V)
+  constexpr int PPT = 2 * NP / NT;  // patches per thread: 2 (d = 128) or 1
+  static_assert(PPT * NT == 2 * NP, "patches must divide over the threads");
+  const int tid = threadIdx.x, b = u / Hkv, h = u % Hkv;
+  const int old = n0 % kQB, blk = n0 / kQB + j;
+  float* e_s = reinterpret_cast<float*>(img + quant_e_off(D));
+
+  Row8<T> row[PPT][4];
+#pragma unroll
+  for (int i = 0; i < PPT; ++i) {
+    const int id = tid + i * NT, isv = id / NP, pt = id % NP, c8 = pt % (D / 8), tg = pt / (D / 8);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 4 * tg + r, pos = j * kQB + t;
+      if (pos < old) {  // from the tail: keys in 16-byte chunks, values in rows
+        if (isv) {
+          row[i][r].load(tail + ((size_t)kQB * D + (size_t)t * D + c8 * 8) * ELT);
+        } else if constexpr (CE == 8) {
+          row[i][r].load(tail + ((size_t)c8 * kQB + t) * 16);
+        } else {
+          Row8<float>& f = row[i][r];
+          f.a = *reinterpret_cast<const float4*>(tail + ((size_t)(2 * c8) * kQB + t) * 16);
+          f.b = *reinterpret_cast<const float4*>(tail + ((size_t)(2 * c8 + 1) * kQB + t) * 16);
+        }
+      } else {
+        const QStrides& st = isv ? p.vs : p.ks;
+        row[i][r].load(reinterpret_cast<const T*>(isv ? p.v : p.k) + b * st.b + (pos - old) * st.t + h * st.h + c8 * 8);
+      }
+    }
+  }
+  if (tid < kQB) {
+    const int pos = j * kQB + tid;
+    float ev = 0.f;
+    if (pos < old)
+      ev = reinterpret_cast<const float*>(tail + 2 * (size_t)kQB * D * ELT)[tid];
+    else if (p.e != nullptr)
+      ev = p.e[((long long)b * p.n + (pos - old)) * Hkv + h];
+    e_s[tid] = ev;
+  }
+  if (tid < 2) red[tid] = 0;
+  __syncthreads();
+
+  // Maximum of the magnitudes' bit patterns: a NaN or an infinity comes out on top.
+#pragma unroll
+  for (int i = 0; i < PPT; ++i) {
+    const int id = tid + i * NT, isv = id / NP, tg = id % NP / (D / 8);
+    uint32_t mx = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (e_s[4 * tg + r] == -INFINITY) row[i][r].zero();
+      float f[8];
+      row[i][r].get(f);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) mx = max(mx, __float_as_uint(f[x]) & 0x7FFFFFFFu);
+    }
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if ((tid & 31) == 0) atomicMax(red + isv, mx);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PPT; ++i) {
+    const int id = tid + i * NT, isv = id / NP, pt = id % NP, c8 = pt % (D / 8), tg = pt / (D / 8);
+    const float amax = __uint_as_float(red[isv]);
+    const bool finite = red[isv] < 0x7F800000u;
+    const float inv = (finite && amax >= 0x1p-100f) ? 448.f / amax : 0.f;
+    float f[4][8];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      row[i][r].get(f[r]);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) f[r][x] = inv > 0.f ? f[r][x] * inv : 0.f;
+    }
+    if (isv) {  // one word: the patch's four tokens of one dim
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        *reinterpret_cast<uint32_t*>(img + quant_v_off(4 * tg, c8 * 8 + x, D)) =
+            e4m3x4(f[0][x], f[1][x], f[2][x], f[3][x]);
+    } else {  // one word: four dims of one token
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int x = 0; x < 8; x += 4)
+          *reinterpret_cast<uint32_t*>(img + quant_k_off(4 * tg + r, c8 * 8 + x, D)) =
+              e4m3x4(f[r][x], f[r][x + 1], f[r][x + 2], f[r][x + 3]);
+    }
+  }
+  if (tid < 2) {
+    const float amax = __uint_as_float(red[tid]);
+    const float sc = red[tid] >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : amax >= 0x1p-100f ? amax / 448.f : 0.f;
+    reinterpret_cast<float*>(img + quant_scale_off(D))[tid] = sc;
+  }
+  constexpr int kUsed = quant_scale_off(D) + 8;
+  for (int o = kUsed + tid * 4; o < quant_unit_bytes(D); o += NT * 4) *reinterpret_cast<uint32_t*>(img + o) = 0;
+  __syncthreads();
+  const int idx = p.tab[(long long)u * p.max_blocks + blk];
+  if (idx < 0 || (long long)idx >= p.n_units) {
+    if (tid == 0) quant_flag(p.status, kQErrIndex);
+    return;
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.units + (long long)idx * quant_unit_bytes(D));
+  for (int o = tid; o < quant_unit_bytes(D) / 16; o += NT) dst[o] = reinterpret_cast<const uint4*>(img)[o];
+}
+
+// What the call does to unit u: tokens before it, new ones (0 where the unit is left as it was).
+struct UnitAppend {
+  int n0, add;
+};
+__device__ __forceinline__ UnitAppend unit_append(const QAppendArgs& p, int Hkv, int u, bool flag) {
+  UnitAppend r;
+  r.n0 = quant_len(p.lens, u, p.max_blocks, p.status, flag);
+  r.add = quant_count(p.n_new, u / Hkv, p.n, p.status, flag);
+  if (r.n0 < 0) {
+    r.n0 = r.add = 0;
+  } else if (r.n0 > kQB * p.max_blocks - r.add) {
+    if (flag) quant_flag(p.status, kQErrCapacity);
+    r.add = 0;
+  }
+  return r;
+}
+
+// Blocks that the call completes: grid (units, most blocks), so that neighbouring
+// CTAs read the heads of the same tokens.
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendThreads) quant_blocks_kernel(QAppendArgs p, int Hkv, long long payload) {
+  __shared__ __align__(16) uint8_t img[quant_unit_bytes(D)];
+  __shared__ uint32_t red[2];
+  const int u = blockIdx.x, j = blockIdx.y;
+  const UnitAppend a = unit_append(p, Hkv, u, false);
+  if (j >= (a.n0 % kQB + a.add) / kQB) return;
+  quant_block<T, D>(p, Hkv, u, j, a.n0, p.tail + u * payload, img, red);
+}
+
+// The unit's tail and length; with BLOCK also the one block that at most 64 new
+// tokens can complete (single tokens: one launch).
+template <typename T, int D, bool BLOCK>
+__global__ void __launch_bounds__(kAppendThreads) quant_tail_kernel(QAppendArgs p, int Hkv, long long payload) {
+  __shared__ __align__(16) uint8_t img[BLOCK ? quant_unit_bytes(D) : 16];
+  __shared__ uint32_t red[2];
+  constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE;
+  const int u = blockIdx.x, b = u / Hkv, h = u % Hkv, tid = threadIdx.x;
+  const UnitAppend a = unit_append(p, Hkv, u, tid == 0);
+  uint8_t* tail = p.tail + u * payload;
+  const int old = a.n0 % kQB, done = (old + a.add) / kQB;
+  if (BLOCK && done > 0) {
+    quant_block<T, D>(p, Hkv, u, 0, a.n0, tail, img, red);
+  }
+  __syncthreads();  // the old tail and length have been read
+  const int first = done > 0 ? 0 : old, left = old + a.add - done * kQB;
+  for (int i = tid; i < (left - first) * NCH; i += kAppendThreads) {
+    const int r = first + i / NCH, c = i % NCH;
+    const long long tok = (long long)done * kQB + r - old;
+    const T* ksrc = reinterpret_cast<const T*>(p.k) + b * p.ks.b + tok * p.ks.t + h * p.ks.h + c * CE;
+    const T* vsrc = reinterpret_cast<const T*>(p.v) + b * p.vs.b + tok * p.vs.t + h * p.vs.h + c * CE;
+    *reinterpret_cast<uint4*>(tail + ((size_t)c * kQB + r) * 16) = *reinterpret_cast<const uint4*>(ksrc);
+    *reinterpret_cast<uint4*>(tail + (size_t)kQB * D * ELT + (size_t)r * D * ELT + c * 16) =
+        *reinterpret_cast<const uint4*>(vsrc);
+  }
+  float* te = reinterpret_cast<float*>(tail + 2 * (size_t)kQB * D * ELT);
+  for (int r = first + tid; r < left; r += kAppendThreads)
+    te[r] = p.e != nullptr ? p.e[((long long)b * p.n + (long long)done * kQB + r - old) * Hkv + h] : 0.f;
+  if (tid == 0) p.lens_out[u] = p.lens[u] + a.add;
+}
+
+template <typename T, int D>
+cudaError_t append_variant(const Shape& s, const QAppendArgs& a, cudaStream_t stream) {
+  if (a.n <= kQB) {
+    quant_tail_kernel<T, D, true><<<s.U, kAppendThreads, 0, stream>>>(a, s.Hkv, s.payload);
+  } else {
+    const int most = std::min((a.n + kQB - 1) / kQB, a.max_blocks);
+    quant_blocks_kernel<T, D><<<dim3(s.U, most), kAppendThreads, 0, stream>>>(a, s.Hkv, s.payload);
+    quant_tail_kernel<T, D, false><<<s.U, kAppendThreads, 0, stream>>>(a, s.Hkv, s.payload);
+  }
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Eviction. One CTA per unit: the table row and the weights' bit patterns go to
+// shared memory once, a radix selection (8 bits at a time over the order-preserving
+// keys) finds the largest weight that still leaves, and a stable partition writes
+// the row back: kept blocks in order, then the evicted ones, which are the next
+// destinations of appended blocks.
+// ---------------------------------------------------------------------------
+constexpr int kEvictThreads = 256;
+
+// Order-preserving key of a weight; NaN ranks above every number.
+__device__ __forceinline__ uint32_t weight_key(uint32_t bits) {
+  const float f = __uint_as_float(bits);
+  return isnan(f) ? 0xFFFFFFFFu : ordered_key(f);
+}
+
+// Exclusive prefix sum over the block's threads; *total receives the sum.
+__device__ __forceinline__ int block_scan(int v, int* warp_s, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();  // warp_s is free
+  if (lane == 31) warp_s[warp] = inc;
+  __syncthreads();
+  int base = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kEvictThreads / 32; ++w) {
+    const int x = warp_s[w];
+    if (w < warp) base += x;
+    sum += x;
+  }
+  *total = sum;
+  return base + inc - v;
+}
+
+__global__ void __launch_bounds__(kEvictThreads) quant_evict_kernel(QEvictArgs p) {
+  extern __shared__ uint32_t evict_smem[];
+  __shared__ int hist[256];
+  __shared__ int warp_s[kEvictThreads / 32];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_rank;
+  const int u = blockIdx.x, tid = threadIdx.x;
+  const long long row = (long long)u * p.max_blocks;
+  const int n0 = quant_len(p.lens, u, p.max_blocks, p.status, tid == 0);
+  const int full = n0 < 0 ? 0 : n0 / kQB, over = max(0, full - p.budget);
+  if (over == 0) {  // nothing to evict: the row as it is
+    for (int i = tid; i < p.max_blocks; i += kEvictThreads) {
+      if (p.tab_out != p.tab) p.tab_out[row + i] = p.tab[row + i];
+      if (p.mass_out != p.mass) p.mass_out[row + i] = p.mass[row + i];
+      if (p.order != nullptr) p.order[row + i] = i;
+    }
+    if (tid == 0 && p.lens_out != p.lens) p.lens_out[u] = p.lens[u];
+    return;
+  }
+  uint32_t* w = evict_smem;                                  // [full] weights (bit patterns)
+  int32_t* tb = reinterpret_cast<int32_t*>(evict_smem + full);  // [full] table entries
+  for (int i = tid; i < full; i += kEvictThreads) {
+    w[i] = __float_as_uint(p.mass[row + i]);
+    tb[i] = p.tab[row + i];
+  }
+  const float tail_mass = full < p.max_blocks ? p.mass[row + full] : 0.f;
+  const int old = full - p.n_recent;  // >= over: n_recent <= budget
+  if (tid == 0) {
+    s_prefix = 0;
+    s_rank = over;  // the over-th smallest key among those with the prefix
+  }
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
+    __syncthreads();
+    const uint32_t prefix = s_prefix;
+    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    const int rank = s_rank;
+    for (int i = tid; i < old; i += kEvictThreads) {
+      const uint32_t k = weight_key(w[i]);
+      if ((k & mask) == prefix) atomicAdd(hist + ((k >> shift) & 255), 1);
+    }
+    __syncthreads();
+    int total;
+    const int c = hist[tid];
+    const int before = block_scan(c, warp_s, &total);
+    if (before < rank && rank <= before + c) {  // exactly one thread
+      s_prefix = prefix | ((uint32_t)tid << shift);
+      s_rank = rank - before;
+    }
+    __syncthreads();
+  }
+  const uint32_t cut = s_prefix;
+  // Blocks below the cut leave; of those at the cut, the s_rank of the highest indices.
+  const int per = (old + kEvictThreads - 1) / kEvictThreads, i0 = min(old, tid * per), i1 = min(old, i0 + per);
+  int eq = 0;
+  for (int i = i0; i < i1; ++i) eq += weight_key(w[i]) == cut;
+  int eq_total;
+  int eq_at = block_scan(eq, warp_s, &eq_total);
+  const int eq_keep = eq_total - s_rank;
+  int kept = 0;
+  {
+    int x = eq_at;
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t k = weight_key(w[i]);
+      kept += k > cut || (k == cut && x++ < eq_keep);
+    }
+  }
+  int kept_total;
+  int at = block_scan(kept, warp_s, &kept_total);
+  int gone = full - over + (i0 - at);
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t k = weight_key(w[i]);
+    const bool keep = k > cut || (k == cut && eq_at++ < eq_keep);
+    const int to = keep ? at++ : gone++;
+    p.tab_out[row + to] = tb[i];
+    if (keep) p.mass_out[row + to] = __uint_as_float(w[i]);
+    if (p.order != nullptr) p.order[row + to] = i;
+  }
+  for (int i = old + tid; i < full; i += kEvictThreads) {  // the newest blocks move up
+    p.tab_out[row + i - over] = tb[i];
+    p.mass_out[row + i - over] = __uint_as_float(w[i]);
+    if (p.order != nullptr) p.order[row + i - over] = i;
+  }
+  // behind the kept blocks: the tail's weight, then zeros
+  for (int i = full - over + tid; i <= full && i < p.max_blocks; i += kEvictThreads)
+    p.mass_out[row + i] = i == full - over ? tail_mass : 0.f;
+  for (int i = full + tid; i < p.max_blocks; i += kEvictThreads) {
+    if (p.tab_out != p.tab) p.tab_out[row + i] = p.tab[row + i];
+    if (p.mass_out != p.mass && i > full) p.mass_out[row + i] = p.mass[row + i];
+    if (p.order != nullptr) p.order[row + i] = i;
+  }
+  if (tid == 0) p.lens_out[u] = n0 - kQB * over;
+}
+
+}  // namespace
+
+cudaError_t launch_quant_append(const Shape& s, const QAppendArgs& a, cudaStream_t stream) {
+  if (s.dtype == 0)
+    return s.d == 64 ? append_variant<float, 64>(s, a, stream) : append_variant<float, 128>(s, a, stream);
+  return s.d == 64 ? append_variant<__nv_bfloat16, 64>(s, a, stream) : append_variant<__nv_bfloat16, 128>(s, a, stream);
+}
+
+cudaError_t launch_quant_evict(const Shape& s, const QEvictArgs& a, cudaStream_t stream) {
+  const size_t smem = (size_t)a.max_blocks * 8;
+  static std::atomic<int> lim[64];
+  if (smem > 40000) {
+    const cudaError_t e = raise_smem_limit((const void*)quant_evict_kernel, smem, lim);
+    if (e != cudaSuccess) return e;
+  }
+  quant_evict_kernel<<<s.U, kEvictThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace nosa

@@ -30,18 +30,6 @@ constexpr int kScoreCap = 32; // a step graph's score grid covers this many more
 
 thread_local std::string g_thread_err;
 
-struct DeviceGuard {
-  int prev = -1;
-  int want;
-  explicit DeviceGuard(int dev) : want(dev) {
-    cudaGetDevice(&prev);
-    if (prev != dev) cudaSetDevice(dev);
-  }
-  ~DeviceGuard() {
-    if (prev >= 0 && prev != want) cudaSetDevice(prev);
-  }
-};
-
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Host-only validation. Returns NOSA_OK, NOSA_ERR_INVALID_ARG or NOSA_ERR_UNSUPPORTED.

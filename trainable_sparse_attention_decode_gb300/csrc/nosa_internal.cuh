@@ -306,6 +306,19 @@ int attention_pick_nsplit(const Shape& s, int n_blocks, int has_tail);
 cudaError_t launch_attention(const Shape& s, const AttnArgs& a, cudaStream_t stream);
 bool attention_supported(int dtype, int d, int G);
 
+// Makes device `dev` current for the scope of a call.
+struct DeviceGuard {
+  int prev = -1;
+  int want;
+  explicit DeviceGuard(int dev) : want(dev) {
+    cudaGetDevice(&prev);
+    if (prev != dev) cudaSetDevice(dev);
+  }
+  ~DeviceGuard() {
+    if (prev >= 0 && prev != want) cudaSetDevice(prev);
+  }
+};
+
 // Raises a kernel's dynamic shared-memory limit to at least `bytes` on the
 // current device, calling the driver only when the limit must grow (the caller
 // passes one cache array of 64 per kernel).
