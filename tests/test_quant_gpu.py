@@ -365,6 +365,33 @@ def test_attention_matches_oracle(dtype, batch, hq, hkv, d, lens, T, with_mass):
     assert torch.equal(out, out2) and torch.equal(lse, lse2) and (mass is None or torch.equal(mass, m1))
 
 
+@pytest.mark.parametrize("dtype,hq,hkv,d,T", [
+    ("bf16", 6, 3, 128, 1), ("bf16", 6, 3, 64, 1), ("f32", 6, 3, 128, 1), ("f32", 6, 3, 64, 1), ("bf16", 8, 2, 128, 4),
+    ("bf16", 8, 2, 64, 4), ("bf16", 8, 2, 128, 8), ("f32", 8, 2, 64, 8), ("f32", 8, 2, 128, 7)])
+def test_attention_long_rings(dtype, hq, hkv, d, T):
+    """Enough blocks that every CTA goes round its ring several times and crosses units; the
+    tables name the units of a small pool many times."""
+    rng = np.random.default_rng(T * d)
+    batch = 4
+    c = Cache(rng, dtype, batch, hq, hkv, d, [64 * 70 + 5] * (batch * hkv))
+    lens = np.array([64 * 1500 + 40, 64 * 900, 70, 64 * 2100 + 1, 64 * 30, 64 * 1200 + 63, 1, 64 * 800, 64 * 999 + 2,
+                     64 * 640, 64 * 333 + 33, 64 * 1024][:batch * hkv], np.int32)
+    c.cap = 2101
+    c.lens = lens
+    c.tab = rng.integers(0, len(c.images), size=(len(lens), c.cap)).astype(np.int32)
+    c.upload()
+    q = query(rng, batch, T, hq, d, dtype)
+    m0 = rng.random(size=c.tab.shape).astype(np.float32)
+    mass = dev(m0)
+    out, lse, status = c.run(q, mass=mass, decay=0.5)
+    assert status == 0
+    c.check(q, out, lse, mass0=m0, mass=f64(mass), decay=0.5)
+    for _ in range(20):  # and again, many times, with the same result
+        m1 = dev(m0)
+        out2, lse2, status = c.run(q, mass=m1, decay=0.5, workspace=c.workspace)
+        assert status == 0 and torch.equal(out, out2) and torch.equal(lse, lse2) and torch.equal(mass, m1)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_query_counts_and_strides(dtype):
     rng = np.random.default_rng(9)

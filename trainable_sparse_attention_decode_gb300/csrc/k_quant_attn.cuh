@@ -7,11 +7,15 @@
 //
 // The cache is read once, so HBM bounds a call with few rows. Three launches:
 //   stream  : the full blocks of all units, one after another, are one list of items
-//             that one wave of CTAs shares equally (units differ in length, so the
-//             shares are cut from the lengths on the device). A producer warp keeps a
-//             ring of whole units in flight with bulk copies; four warps each own one
-//             16-token slice of every unit with a running maximum, sum and output of
-//             their own, and join when the CTA leaves a unit.
+//             that one wave of CTAs (one per SM) shares equally: units differ in
+//             length, so the shares are cut from the lengths on the device. A producer
+//             warp keeps a ring of whole units in flight with bulk copies; the consumer
+//             warps take the units in turn, each with a running maximum, sum and
+//             output of its own. A warp that has a whole block to itself pays its
+//             reductions and the output's rescaling once per 64 tokens and has four
+//             independent chains of products. Where the CTA leaves a unit the warps
+//             leave their parts to a helper warp, which joins them and has the next
+//             unit's queries ready, and go on.
 //   combine : one CTA per unit (and row tile) attends to the tail in fp32 while the
 //             stream still runs, then joins the unit's parts.
 //   weights : with accumulated weights, a warp per block adds up what the stream
@@ -40,7 +44,6 @@
 
 namespace nosa {
 
-constexpr int kQaThreads = 160;   // four consumer warps and a producer warp
 constexpr int kQaMinItems = 2;    // blocks of a CTA's share, at least
 constexpr int kQcThreads = 256;   // combine
 constexpr float kQLog2e = 1.4426950408889634f;
@@ -71,7 +74,7 @@ struct QStreamParams {
   float* part_acc;    // ... [rows][d] its output (not normalised)
   float2* rowstat;    // [units x tiles][rows] final maximum and 1 / sum
   float* tail_w;      // [units x tiles] weight of the tail
-  float2* blk;        // [units x tiles][max_blocks][4][rows] maximum and sum of a slice, or null
+  float2* blk;        // [units x tiles][max_blocks][rows] maximum and sum of a block, or null
 };
 
 // 1 / sqrt(d)
@@ -110,6 +113,17 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // CTAs that share `total` items, and the CTA that holds item x.
 __device__ __forceinline__ int qa_active(long long total, int ctas) {
   const long long want = (total + kQaMinItems - 1) / kQaMinItems;
@@ -131,56 +145,161 @@ __device__ __forceinline__ QRow qa_row(int r, int G, int n, int qn) {
   return w;
 }
 
-template <int D, int NT, bool F32>
+// Shape of a stream CTA. A warp has 8 NT rows; RG warps share a unit, each with its own
+// rows, and IS units are worked on at once. Item i of the CTA goes to the warps of slot
+// i % IS and to stage i % STAGES, and STAGES is a multiple of IS: a stage always has the
+// same readers. Copies may land out of order, and a barrier's parity tells a phase only
+// from its neighbours, so a warp may wait for a stage's next fill only after it has seen
+// the fill before.
+template <int D, int NT, int RG, bool F32>
 struct QGeom {
-  static constexpr int ROWS = 8 * NT, KS = D / 16, UB = quant_unit_bytes(D);
-  // ring depth: three CTAs per SM for 8 rows, two for more (their outputs need the registers)
-  static constexpr int PER_SM = NT == 1 ? 3 : 2;
-  static constexpr int STAGES = NT == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
-  static constexpr int RP = D + 4;  // padded row of the joining buffer
+  static constexpr int ROWS = 8 * NT * RG, KS = D / 16, UB = quant_unit_bytes(D);
+  static constexpr int IS = NT == 1 ? (D == 128 ? 4 : 8) : RG == 1 ? (D == 128 ? 5 : 6) : 8 / RG;
+  static constexpr int W = IS * RG;             // consumer warps; a producer and a helper come on top
+  static constexpr int THREADS = 32 * (W + 2);
+  static constexpr int STAGES = D == 64 ? 2 * 8 / IS * IS : RG == 1 ? 2 * IS : RG == 4 && F32 ? 6 : 8;
+  static constexpr int SL = NT == 1 ? 4 : 2;    // slices of a block that a warp takes at once
+  static constexpr int NB = NT == 1 ? 2 : 1;    // buffers for queries and for parts
+  static constexpr int RP = D + 4;              // padded row of a part
+  static constexpr int Q_BYTES = NT * RG * KS * 32 * (F32 ? 16 : 8);
+  static constexpr int RED_BYTES = W * 8 * NT * RP * 4, ML_BYTES = W * 8 * NT * 8;
   static constexpr int Q_OFF = STAGES * UB;
-  static constexpr int RED_OFF = Q_OFF + NT * KS * 32 * (F32 ? 16 : 8);
-  static constexpr int ML_OFF = RED_OFF + 4 * 8 * RP * 4;
-  static constexpr int ROW_OFF = ML_OFF + 4 * 8 * 8;
-  static constexpr int DESC_OFF = ROW_OFF + ROWS * 8;
-  static constexpr int BAR_OFF = DESC_OFF + STAGES * 16;
-  static constexpr int SMEM = BAR_OFF + (2 * STAGES + 1) * 8;
-  static_assert(UB % 16 == 0 && Q_OFF % 16 == 0 && RED_OFF % 16 == 0 && DESC_OFF % 16 == 0, "alignment");
+  static constexpr int RED_OFF = Q_OFF + NB * Q_BYTES;
+  static constexpr int ML_OFF = RED_OFF + NB * RED_BYTES;
+  static constexpr int ROW_OFF = ML_OFF + NB * ML_BYTES;
+  static constexpr int NULL_OFF = ROW_OFF + NB * ROWS * 8;
+  static constexpr int BAR_OFF = NULL_OFF + (STAGES * 4 + 7) / 8 * 8;
+  static constexpr int SMEM = BAR_OFF + (2 * STAGES + 3 * NB) * 8;
+  static_assert(STAGES % IS == 0 && STAGES <= 32, "a stage has one slot and one producer lane");
+  static_assert(UB % 16 == 0 && Q_OFF % 16 == 0 && RED_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
+  static_assert(SMEM <= 227 * 1024 - 256, "shared memory");
 };
 
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(kQaThreads, QGeom<D, NT, F32>::PER_SM) quant_stream_kernel(QStreamParams p) {
-  using Gm = QGeom<D, NT, F32>;
-  constexpr int KS = Gm::KS, ROWS = Gm::ROWS, STAGES = Gm::STAGES, UB = Gm::UB;
+// A CTA's share as segments: consecutive blocks of one (unit, tile).
+struct QWalk {
+  const QStreamParams& p;
+  int u, tile, j0, cnt, left, lane, have, len, tokens;
+  // from the unit that holds the first item, `at` items into it, `left` items to go
+  __device__ __forceinline__ QWalk(const QStreamParams& p_, int u_, long long at, int left_, int lane_)
+      : p(p_), u(u_), cnt(0), left(left_), lane(lane_), have(-1), len(0), tokens(0) {
+    tokens = fetch();
+    const int nb = tokens / kQB;
+    tile = (int)(at / nb);
+    j0 = (int)(at % nb);
+    cnt = min(nb - j0, left);
+  }
+  __device__ __forceinline__ int fetch() {  // tokens of unit u; 32 lengths at a time (whole warp)
+    if (have < 0 || u >= have + 32) {
+      have = u;
+      len = u + lane < p.U ? max(0, quant_len(p.lens, u + lane, p.max_blocks, nullptr, false)) : 0;
+    }
+    return __shfl_sync(0xffffffffu, len, u - have);
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next() {
+    left -= cnt;
+    if (left <= 0) return;
+    j0 = 0;
+    if (++tile == p.tiles) {
+      tile = 0;
+      do {
+        ++u;
+        tokens = fetch();
+      } while (tokens < kQB);
+    }
+    cnt = min(tokens / kQB, left);
+  }
+  __device__ __forceinline__ long long vu() const { return (long long)u * p.tiles + tile; }
+};
+
+// Queries of one row group of 8 (whole warp) as B operands, and the rows' factors.
+template <int D, bool F32>
+__device__ __forceinline__ void qa_queries(const QStreamParams& p, int u, int row0, int n, int qn, uint8_t* q_s, float* rs_s,
+                                           int* vis_s, int lane) {
+  constexpr int KS = D / 16;
+  const int g = lane >> 2, c = lane & 3, b = u / p.Hkv, h = u % p.Hkv;
+  const QRow w = qa_row(row0 + g, p.G, n, qn);
+  float f[KS][4];
+  float mx = 0.f;
+  const long long src = b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + 4 * c;
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    f[k][0] = f[k][1] = f[k][2] = f[k][3] = 0.f;
+    if (w.t < qn) {
+      if constexpr (F32) {
+        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + src + 16 * k);
+        f[k][0] = x.x; f[k][1] = x.y; f[k][2] = x.z; f[k][3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(p.q) + src + 16 * k);
+        f[k][0] = bf16_lo(x.x); f[k][1] = bf16_hi(x.x); f[k][2] = bf16_lo(x.y); f[k][3] = bf16_hi(x.y);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(f[k][i]));
+  }
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  // 2^ex <= mx < 2^(ex + 1), kept where both 2^ex and 2^-ex are normal numbers
+  const int ex = min(max((int)(__float_as_uint(mx) >> 23), 1), 253) - 127;
+  const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    const float x0 = f[k][0] * down, x1 = f[k][1] * down, x2 = f[k][2] * down, x3 = f[k][3] * down;
+    const uint32_t h0 = f16x2(x0, x1), h1 = f16x2(x2, x3);
+    if constexpr (F32) {
+      const float2 y0 = f32x2(h0), y1 = f32x2(h1);
+      reinterpret_cast<uint4*>(q_s)[k * 32 + lane] =
+          make_uint4(h0, h1, f16x2(x0 - y0.x, x1 - y0.y), f16x2(x2 - y1.x, x3 - y1.y));
+    } else {
+      reinterpret_cast<uint2*>(q_s)[k * 32 + lane] = make_uint2(h0, h1);
+    }
+  }
+  if (c == 0) {
+    rs_s[g] = up * kQScale<D>;
+    vis_s[g] = w.sees;
+  }
+}
+
+template <int D, int NT, int RG, bool F32>
+__global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_stream_kernel(QStreamParams p) {
+  using Gm = QGeom<D, NT, RG, F32>;
+  constexpr int KS = Gm::KS, ROWS = Gm::ROWS, STAGES = Gm::STAGES, UB = Gm::UB, SL = Gm::SL, W = Gm::W, IS = Gm::IS;
+  constexpr int NB = Gm::NB, WR = 8 * NT, kThreads = Gm::THREADS;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* q_s = smem + Gm::Q_OFF;
-  float* red = reinterpret_cast<float*>(smem + Gm::RED_OFF);
-  float2* red_ml = reinterpret_cast<float2*>(smem + Gm::ML_OFF);  // [4][8]
-  float* rs_s = reinterpret_cast<float*>(smem + Gm::ROW_OFF);     // [ROWS] factor of a row's logits
-  int* vis_s = reinterpret_cast<int*>(rs_s + ROWS);               // [ROWS] tokens it sees
-  int4* desc = reinterpret_cast<int4*>(smem + Gm::DESC_OFF);      // unit, tile, block, flags
+  int* null_s = reinterpret_cast<int*>(smem + Gm::NULL_OFF);  // [STAGES] the table names no unit
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Gm::BAR_OFF);
   uint64_t* empty = full + STAGES;
-  uint64_t* join = empty + STAGES;
-  __shared__ long long s_scan[8];
+  uint64_t* q_full = empty + STAGES;    // [NB] queries of a segment are there
+  uint64_t* dump_full = q_full + NB;    // [NB] the warps' parts of a segment are there
+  uint64_t* dump_free = dump_full + NB;
+  // per buffer: queries, factors of the rows' logits, tokens they see, parts
+  auto q_of = [&](int k) { return smem + Gm::Q_OFF + (k % NB) * Gm::Q_BYTES; };
+  auto rs_of = [&](int k) { return reinterpret_cast<float*>(smem + Gm::ROW_OFF) + (k % NB) * 2 * ROWS; };
+  auto vis_of = [&](int k) { return reinterpret_cast<int*>(rs_of(k) + ROWS); };
+  auto red_of = [&](int k) { return reinterpret_cast<float*>(smem + Gm::RED_OFF + (k % NB) * Gm::RED_BYTES); };  // [W][WR][RP]
+  auto ml_of = [&](int k) { return reinterpret_cast<float2*>(smem + Gm::ML_OFF + (k % NB) * Gm::ML_BYTES); };    // [W][WR]
+  __shared__ long long s_scan[kThreads / 32];
   __shared__ long long s_before;
   __shared__ int s_unit;
   __shared__ volatile int s_bad;
-  enum { kFirst = 1, kLast = 2, kNull = 4 };
 
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 4);
+      mbar_init(&empty[s], RG);
     }
-    mbar_init(join, 4);
+    for (int s = 0; s < NB; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&dump_full[s], W);
+      mbar_init(&dump_free[s], 1);
+    }
     fence_mbar_init();
     s_bad = 0;
   }
   // ---- the share: prefix sums of the units' full blocks ----
-  const int per = (p.U + kQaThreads - 1) / kQaThreads;
+  const int per = (p.U + kThreads - 1) / kThreads;
   const int a0 = min(p.U, tid * per), a1 = min(p.U, a0 + per);
   long long mine = 0;
   for (int u = a0; u < a1; ++u) mine += max(0, quant_len(p.lens, u, p.max_blocks, p.status, cta == 0)) / kQB;
@@ -194,7 +313,7 @@ __global__ void __launch_bounds__(kQaThreads, QGeom<D, NT, F32>::PER_SM) quant_s
   __syncthreads();
   long long total = 0, before = inc - mine;
 #pragma unroll
-  for (int w = 0; w < kQaThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
@@ -216,340 +335,397 @@ __global__ void __launch_bounds__(kQaThreads, QGeom<D, NT, F32>::PER_SM) quant_s
   }
   __syncthreads();
   const int items = (int)(g1 - g0);
+  bool ok = true;  // no wait has given up
+  // Waits (whole warp) for a phase, with a limit, unless another warp has given up.
+  auto wait = [&](uint64_t* bar, int phase) {
+    return __all_sync(0xffffffffu, s_bad == 0 && mbar_wait_bounded(bar, (uint32_t)(phase & 1)));
+  };
 
-  if (warp == 4) {
-    // ---- producer ----
-    int u = s_unit, it = 0, issued = 0;
-    long long ub = s_before;  // first item of unit u
-    bool go = true;
-    while (it < items && go) {
-      const int nb = max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
-      const int32_t* row = p.tab + (long long)u * p.max_blocks;
-      int at = (int)(g0 + it - ub);  // item inside the unit
-      for (int tile = nb > 0 ? at / nb : p.tiles; tile < p.tiles && it < items && go; ++tile) {
-        const int j0 = at - tile * nb, j1 = (int)min((long long)nb, (long long)j0 + (items - it));
-        if (j0 == 0 && lane == 0) p.base[(long long)u * p.tiles + tile] = ub + (long long)tile * nb;
-        int next = j0 + lane < j1 ? row[j0 + lane] : -1;
-        for (int jb = j0; jb < j1 && go; jb += 32) {
-          const int cur = next;
-          next = jb + 32 + lane < j1 ? row[jb + 32 + lane] : -1;
-          const int cnt = min(32, j1 - jb);
-          for (int i = 0; i < cnt; ++i, ++it) {
-            const int idx = __shfl_sync(0xffffffffu, cur, i);
-            const int s = it % STAGES, j = jb + i;
-            if (lane == 0) {
-              if (it >= STAGES && !mbar_wait_bounded(&empty[s], (uint32_t)((it / STAGES - 1) & 1))) {
-                s_bad = 1;
-                quant_flag(p.status, kQErrWait);
-              }
-              if (s_bad == 0) {
-                const bool bad = idx < 0 || (long long)idx >= p.n_units;
-                desc[s] = make_int4(u, tile, j, (j == j0 ? kFirst : 0) | (j == j1 - 1 ? kLast : 0) | (bad ? kNull : 0));
-                if (bad) {
-                  quant_flag(p.status, kQErrIndex);
-                  mbar_arrive(&full[s]);
-                } else {
-                  mbar_arrive_expect_tx(&full[s], UB);
-                  bulk_g2s(smem + s * UB, p.units + (long long)idx * UB, UB, &full[s]);
-                }
-                issued = it + 1;
-              }
-            }
-            go = __shfl_sync(0xffffffffu, s_bad == 0 ? 1 : 0, 0) != 0;
-            if (!go) break;
-          }
-        }
-        at += j1 - j0;
+  if (warp == W) {
+    // ---- producer: lane s owns stage s and brings it items s, s + STAGES, ... ----
+    int it = lane, u = s_unit, tile = 0, j = 0, nb = 0, idx = -1;
+    long long pos = g0 - s_before + it;  // from the start of unit u
+    auto seek = [&]() {                  // (u, tile, j) of the item, and its table entry
+      if (it >= items) return;
+      for (;;) {
+        nb = max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
+        if (pos < (long long)nb * p.tiles) break;
+        pos -= (long long)nb * p.tiles;
+        ++u;
       }
-      ub += (long long)nb * p.tiles;
-      ++u;
+      tile = (int)pos / nb;
+      j = (int)pos - tile * nb;
+      idx = p.tab[(long long)u * p.max_blocks + j];
+    };
+    if (lane >= STAGES) it = items;
+    seek();
+    int fills = 0;
+    uint64_t since = global_ns();
+    for (int spin = 0; __any_sync(0xffffffffu, it < items); ++spin) {
+      bool moved = false;
+      if (it < items && (fills == 0 || mbar_test(&empty[lane], (uint32_t)((fills - 1) & 1)))) {
+        const bool bad = idx < 0 || (long long)idx >= p.n_units;
+        null_s[lane] = bad;
+        if (bad) {
+          quant_flag(p.status, kQErrIndex);
+          mbar_arrive(&full[lane]);
+        } else {
+          mbar_arrive_expect_tx(&full[lane], UB);
+          bulk_g2s(smem + lane * UB, p.units + (long long)idx * UB, UB, &full[lane]);
+        }
+        if (j == 0) p.base[(long long)u * p.tiles + tile] = g0 + it;
+        ++fills;
+        it += STAGES;
+        pos += STAGES;
+        seek();
+        moved = true;
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+        spin = 0;
+        since = global_ns();
+      } else if ((spin & 63) == 63 && (s_bad != 0 || global_ns() - since > 2000000000ull)) {
+        ok = false;
+      }
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+    }
+    if (!ok && lane == 0) {
+      s_bad = 1;
+      quant_flag(p.status, kQErrWait);
     }
     __syncthreads();
-    if (s_bad != 0 && lane == 0) {  // drain: the last copy issued into each stage
-      for (int s = 0; s < STAGES; ++s) {
-        int last = -1;
-        for (int i = s; i < issued; i += STAGES) last = i;
-        if (last >= 0) mbar_wait_bounded(&full[s], (uint32_t)((last / STAGES) & 1));
+    if (s_bad != 0 && fills > 0) mbar_wait_bounded(&full[lane], (uint32_t)((fills - 1) & 1));  // drain
+    return;
+  }
+
+  if (warp == W + 1) {
+    // ---- helper: prepares the queries of coming segments, joins the warps' parts ----
+    QWalk ahead(p, s_unit, g0 - s_before, items, lane);
+    long long slot[NB];
+    int prepared = 0;
+    auto prepare = [&]() {
+      const int b = ahead.u / p.Hkv, qn = quant_count(p.q_len, b, p.T, p.status, lane == 0);
+#pragma unroll 1
+      for (int r = 0; r < ROWS / 8; ++r)
+        qa_queries<D, F32>(p, ahead.u, ahead.tile * ROWS + 8 * r, ahead.tokens, qn, q_of(prepared) + r * KS * 32 * (F32 ? 16 : 8),
+                           rs_of(prepared) + 8 * r, vis_of(prepared) + 8 * r, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[prepared % NB]);
+#pragma unroll
+      for (int x = 0; x < NB; ++x)
+        if (x == prepared % NB) slot[x] = cta + ahead.vu();
+      ++prepared;
+      ahead.next();
+    };
+    for (int x = 0; x < NB && ahead.more(); ++x) prepare();
+    for (int k = 0; k < prepared && ok; ++k) {
+      if (!(ok = wait(&dump_full[k % NB], k / NB))) break;
+      const float* red = red_of(k);
+      const float2* ml = ml_of(k);
+      long long to = slot[0];
+#pragma unroll
+      for (int x = 1; x < NB; ++x)
+        if (x == k % NB) to = slot[x];
+#pragma unroll 1
+      for (int r = 0; r < ROWS; ++r) {
+        const int w0 = r / WR * IS, rr = r % WR;  // the warps of this row, and their row
+        float M = ml[w0 * WR + rr].x;
+#pragma unroll
+        for (int w = 1; w < IS; ++w) M = max_nan(M, ml[(w0 + w) * WR + rr].x);
+        const float mu = finite_max(M);
+        float wt[IS], L = 0.f;
+#pragma unroll
+        for (int w = 0; w < IS; ++w) {
+          const float2 y = ml[(w0 + w) * WR + rr];
+          wt[w] = exp_from(y.x, mu);
+          L += wt[w] * y.y;
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane < D / 4) {
+#pragma unroll
+          for (int w = 0; w < IS; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(red + ((w0 + w) * WR + rr) * Gm::RP + 4 * lane);
+            acc.x += wt[w] * y.x; acc.y += wt[w] * y.y; acc.z += wt[w] * y.z; acc.w += wt[w] * y.w;
+          }
+          reinterpret_cast<float4*>(p.part_acc + (to * ROWS + r) * D)[lane] = acc;
+        }
+        if (lane == 0) p.part_ml[to * ROWS + r] = make_float2(M, L);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dump_free[k % NB]);
+      if (ahead.more()) prepare();  // (every warp has left segment k, whose queries were in this buffer)
     }
+    if (!ok && lane == 0) {
+      s_bad = 1;
+      quant_flag(p.status, kQErrWait);
+    }
+    __syncthreads();
     return;
   }
 
   // ---- consumers ----
   const int g = lane >> 2, c = lane & 3;
-  const int tok = 16 * warp + 4 * (g >> 1) + (g & 1);  // this lane's tokens: tok and tok + 2
-  uint32_t joins = 0;
-  // All four warps, with a limit: false where one of them gave up.
-  auto sync4 = [&]() -> bool {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(join);
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(join, joins & 1));
-    ++joins;
-    if (!ok && lane == 0) {
-      s_bad = 1;
-      quant_flag(p.status, kQErrWait);
+  const int tok = 4 * (g >> 1) + (g & 1);  // this lane's tokens of a slice: tok and tok + 2
+  const int is = warp % IS, rg = warp / IS;
+  QWalk seg(p, s_unit, g0 - s_before, items, lane);
+  int it0 = 0;  // first item of the segment
+  for (int k = 0; seg.more(); ++k, it0 += seg.cnt, seg.next()) {
+    if (!(ok = wait(&q_full[k % NB], k / NB))) break;
+    const long long vu = seg.vu();
+    const uint8_t* q_s = q_of(k) + rg * NT * KS * 32 * (F32 ? 16 : 8);
+    const float* rs_s = rs_of(k) + rg * WR;
+    const int* vis_s = vis_of(k) + rg * WR;
+    float o[NT][KS][4], m_run[NT][2], l_run[NT][2], fac[1][2];
+    int vis[1][2];  // (of more than 8 rows these two stay in shared memory)
+    uint32_t qr[NT == 1 && !F32 ? KS : 1][2];
+    int least = 0x7fffffff;  // tokens that all of this lane's rows see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (NT == 1) {
+          fac[0][x] = rs_s[2 * c + x];
+          vis[0][x] = vis_s[2 * c + x];
+        }
+        least = min(least, vis_s[nt * 8 + 2 * c + x]);
+        m_run[nt][x] = -INFINITY;
+        l_run[nt][x] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
     }
-    return ok;
-  };
-  float o[NT][KS][4], m_run[NT][2], l_run[NT][2], fac[NT][2];
-  int vis[NT][2];
-  uint32_t qr[NT == 1 && !F32 ? KS : 1][2];
-  int least = 0;  // tokens that every row of the tile sees
-  for (int it = 0; it < items; ++it) {
-    if (__any_sync(0xffffffffu, s_bad != 0)) break;
-    const int s = it % STAGES;
-    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (uint32_t)((it / STAGES) & 1)))) {
-      if (lane == 0) {
-        s_bad = 1;
-        quant_flag(p.status, kQErrWait);
-      }
-      break;
-    }
-    const int4 de = desc[s];
-    const int u = de.x, tile = de.y, j = de.z;
-    const long long vu = (long long)u * p.tiles + tile;
-    if (de.w & kFirst) {
-      // queries of the tile: warp w prepares row group w, w + 4, ...
-      const int b = u / p.Hkv, h = u % p.Hkv;
-      const int n = quant_len(p.lens, u, p.max_blocks, nullptr, false);
-      const int qn = quant_count(p.q_len, b, p.T, p.status, true);
-      for (int nt = warp; nt < NT; nt += 4) {
-        const QRow w = qa_row(tile * ROWS + nt * 8 + g, p.G, n, qn);
-        float f[KS][4];
-        float mx = 0.f;
-        const long long at = b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + 4 * c;
+    if constexpr (NT == 1 && !F32) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          f[k][0] = f[k][1] = f[k][2] = f[k][3] = 0.f;
-          if (w.t < qn) {
-            if constexpr (F32) {
-              const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + at + 16 * k);
-              f[k][0] = x.x; f[k][1] = x.y; f[k][2] = x.z; f[k][3] = x.w;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(p.q) + at + 16 * k);
-              f[k][0] = bf16_lo(x.x); f[k][1] = bf16_hi(x.x); f[k][2] = bf16_lo(x.y); f[k][3] = bf16_hi(x.y);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(f[k][i]));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // 2^ex <= mx < 2^(ex + 1), kept where both 2^ex and 2^-ex are normal numbers
-        const int ex = min(max((int)(__float_as_uint(mx) >> 23), 1), 253) - 127;
-        const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const float x0 = f[k][0] * down, x1 = f[k][1] * down, x2 = f[k][2] * down, x3 = f[k][3] * down;
-          const uint32_t h0 = f16x2(x0, x1), h1 = f16x2(x2, x3);
-          if constexpr (F32) {
-            const float2 y0 = f32x2(h0), y1 = f32x2(h1);
-            reinterpret_cast<uint4*>(q_s)[(nt * KS + k) * 32 + lane] =
-                make_uint4(h0, h1, f16x2(x0 - y0.x, x1 - y0.y), f16x2(x2 - y1.x, x3 - y1.y));
-          } else {
-            reinterpret_cast<uint2*>(q_s)[(nt * KS + k) * 32 + lane] = make_uint2(h0, h1);
-          }
-        }
-        if (c == 0) {
-          rs_s[nt * 8 + g] = up * kQScale<D>;
-          vis_s[nt * 8 + g] = w.sees;
-        }
-      }
-      if (!sync4()) break;
-      least = 0x7fffffff;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          fac[nt][x] = rs_s[nt * 8 + 2 * c + x];
-          vis[nt][x] = vis_s[nt * 8 + 2 * c + x];
-          least = min(least, vis[nt][x]);
-          m_run[nt][x] = -INFINITY;
-          l_run[nt][x] = 0.f;
-        }
-#pragma unroll
-        for (int mt = 0; mt < KS; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
-      }
-      if constexpr (NT == 1 && !F32) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint2 x = reinterpret_cast<const uint2*>(q_s)[k * 32 + lane];
-          qr[k][0] = x.x;
-          qr[k][1] = x.y;
-        }
+      for (int x = 0; x < KS; ++x) {
+        const uint2 y = reinterpret_cast<const uint2*>(q_s)[x * 32 + lane];
+        qr[x][0] = y.x;
+        qr[x][1] = y.y;
       }
     }
 
-    float2* note = p.blk == nullptr ? nullptr : p.blk + ((vu * p.max_blocks + j) * 4 + warp) * ROWS;
-    if (de.w & kNull) {
-      if (note != nullptr && lane < ROWS) note[lane] = make_float2(-INFINITY, 0.f);
-    } else {
+    for (int it = it0 + (is + IS - it0 % IS) % IS; it < it0 + seg.cnt; it += IS) {
+      const int s = it % STAGES, j = seg.j0 + it - it0;
+      if (!(ok = wait(&full[s], it / STAGES))) break;
+      const bool null_unit = null_s[s] != 0;
       const uint8_t* unit = smem + s * UB;
-      const uint4* kw = reinterpret_cast<const uint4*>(unit + warp * 32 * D) + lane;
-      // ---- logits ----
-      float sc[NT][2][4];
+      const float* es = reinterpret_cast<const float*>(unit + quant_e_off(D));
+      const float ks = es[kQB], vs = es[kQB + 1] * 0x1p-14f;
+      const bool edge = j * kQB + kQB > least;
+      float blk_l[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) blk_l[nt][0] = blk_l[nt][1] = 0.f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sc[nt][0][x] = sc[nt][1][x] = 0.f;
+      for (int s0 = 0; s0 < 4; s0 += SL) {
+        if (null_unit) break;
+        const uint4* kw = reinterpret_cast<const uint4*>(unit) + s0 * 2 * D + lane;
+        // ---- logits ----
+        float sc[NT][SL][4];
 #pragma unroll
-      for (int jj = 0; jj < KS / 2; ++jj) {
-        const uint4 w = kw[jj * 32];
-        const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int k = 2 * jj + y;
-          const uint32_t a[4] = {e4m3x2_f16x2(wd[2 * y]), e4m3x2_f16x2(wd[2 * y + 1]), e4m3x2_f16x2(wd[2 * y] >> 16),
-                                 e4m3x2_f16x2(wd[2 * y + 1] >> 16)};
+          for (int w = 0; w < SL; ++w) sc[nt][w][0] = sc[nt][w][1] = sc[nt][w][2] = sc[nt][w][3] = 0.f;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (NT == 1 && !F32) {
-              mma16816(sc[nt][y], a, qr[k][0], qr[k][1]);
-            } else if constexpr (F32) {
-              const uint4 x = reinterpret_cast<const uint4*>(q_s)[(nt * KS + k) * 32 + lane];
-              mma16816(sc[nt][0], a, x.x, x.y);
-              mma16816(sc[nt][1], a, x.z, x.w);
-            } else {
-              const uint2 x = reinterpret_cast<const uint2*>(q_s)[(nt * KS + k) * 32 + lane];
-              mma16816(sc[nt][y], a, x.x, x.y);
+        for (int jj = 0; jj < KS / 2; ++jj) {
+          uint4 v[SL];
+#pragma unroll
+          for (int w = 0; w < SL; ++w) v[w] = kw[w * 2 * D + jj * 32];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int kk = 2 * jj + y;
+            uint32_t qb[NT][F32 ? 4 : 2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (F32) {
+                const uint4 x = reinterpret_cast<const uint4*>(q_s)[(nt * KS + kk) * 32 + lane];
+                qb[nt][0] = x.x; qb[nt][1] = x.y; qb[nt][2] = x.z; qb[nt][3] = x.w;
+              } else if constexpr (NT == 1) {
+                qb[nt][0] = qr[kk][0];
+                qb[nt][1] = qr[kk][1];
+              } else {
+                const uint2 x = reinterpret_cast<const uint2*>(q_s)[(nt * KS + kk) * 32 + lane];
+                qb[nt][0] = x.x;
+                qb[nt][1] = x.y;
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < SL; ++w) {
+              const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
+              const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (F32) mma16816(sc[nt][w], a, qb[nt][2], qb[nt][3]);
+                mma16816(sc[nt][w], a, qb[nt][0], qb[nt][1]);
+              }
             }
           }
         }
-      }
-      // ---- softmax over the warp's 16 tokens ----
-      const float* es = reinterpret_cast<const float*>(unit + quant_e_off(D));
-      const float e0 = es[tok], e1 = es[tok + 2];
-      const float ks = es[kQB], vs = es[kQB + 1] * 0x1p-14f;
-      const bool off0 = e0 == -INFINITY, off1 = e1 == -INFINITY;
-      const int pos = j * kQB + tok;
-      const bool edge = j * kQB + kQB > least;
-      float corr[NT][2], vsc[NT][2];
-      uint32_t pb[NT][2], pl[F32 ? NT : 1][2];
+        // ---- softmax over the 16 SL tokens ----
+        float ev[SL][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float pr[2][2];  // [column][token]
+        for (int w = 0; w < SL; ++w) {
+          ev[w][0] = es[16 * (s0 + w) + tok];
+          ev[w][1] = es[16 * (s0 + w) + tok + 2];
+        }
+        const int pos = j * kQB + 16 * s0 + tok;
+        float corr[NT][2], vsc[NT][2];
+        uint32_t pb[NT][SL][2], pl[F32 ? NT : 1][SL][2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float f = fac[nt][x] * ks;
-          float l0 = (sc[nt][0][x] + sc[nt][1][x]) * f + e0, l1 = (sc[nt][0][2 + x] + sc[nt][1][2 + x]) * f + e1;
-          if (off0 || (edge && pos >= vis[nt][x])) l0 = -INFINITY;
-          if (off1 || (edge && pos + 2 >= vis[nt][x])) l1 = -INFINITY;
-          float mx = max_nan(l0, l1);
-          mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float mn = max_nan(m_run[nt][x], mx), mu = finite_max(mn);
-          corr[nt][x] = exp_from(m_run[nt][x], mu);
-          vsc[nt][x] = mx == -INFINITY ? 0.f : vs;  // (nothing visible: whatever the block holds)
-          pr[x][0] = exp_from(l0, mu);
-          pr[x][1] = exp_from(l1, mu);
-          const float sum = pr[x][0] + pr[x][1];
-          l_run[nt][x] = l_run[nt][x] * corr[nt][x] + sum;
-          m_run[nt][x] = mn;
-          if (note != nullptr) {
-            float t = sum;
-            t += __shfl_xor_sync(0xffffffffu, t, 4);
-            t += __shfl_xor_sync(0xffffffffu, t, 8);
-            t += __shfl_xor_sync(0xffffffffu, t, 16);
-            if (g == 0) note[nt * 8 + 2 * c + x] = make_float2(mn, t);
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float f = (NT == 1 ? fac[0][x] : rs_s[nt * 8 + 2 * c + x]) * ks;
+            const int sees = NT == 1 ? vis[0][x] : vis_s[nt * 8 + 2 * c + x];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < SL; ++w)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                float& l = sc[nt][w][2 * y + x];
+                l = l * f + ev[w][y];
+                if (ev[w][y] == -INFINITY || (edge && pos + 16 * w + 2 * y >= sees)) l = -INFINITY;
+                mx = max_nan(mx, l);
+              }
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = max_nan(m_run[nt][x], mx), mu = finite_max(mn);
+            corr[nt][x] = exp_from(m_run[nt][x], mu);
+            vsc[nt][x] = mx == -INFINITY ? 0.f : vs;  // (nothing visible: whatever the block holds)
+            m_run[nt][x] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < SL; ++w)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                float& l = sc[nt][w][2 * y + x];
+                l = exp_from(l, mu);
+                sum += l;
+                l *= 16384.f;
+              }
+            l_run[nt][x] = l_run[nt][x] * corr[nt][x] + sum;
+            blk_l[nt][x] = blk_l[nt][x] * corr[nt][x] + sum;
+          }
+#pragma unroll
+          for (int w = 0; w < SL; ++w)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float x0 = sc[nt][w][2 * y], x1 = sc[nt][w][2 * y + 1];
+              const uint32_t hh = f16x2(x0, x1);
+              pb[nt][w][y] = transpose8x8(hh);
+              if constexpr (F32) {
+                const float2 r = f32x2(hh);
+                pl[nt][w][y] = transpose8x8(f16x2(x0 - r.x, x1 - r.y));
+              }
+            }
+        }
+        // ---- o = o * corr + scale * (V^T P) ----
+        const uint4* vw = kw + D;  // 16 D bytes on
+#pragma unroll
+        for (int jj = 0; jj < KS / 2; ++jj) {
+          uint4 v[SL];
+#pragma unroll
+          for (int w = 0; w < SL; ++w) v[w] = vw[w * 2 * D + jj * 32];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float t[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
+#pragma unroll
+            for (int w = 0; w < SL; ++w) {
+              const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
+              const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (F32) mma16816(t[nt], a, pl[nt][w][0], pl[nt][w][1]);
+                mma16816(t[nt], a, pb[nt][w][0], pb[nt][w][1]);
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                float& oo = o[nt][2 * jj + y][x];
+                oo = oo * corr[nt][x & 1] + t[nt][x] * vsc[nt][x & 1];
+              }
           }
         }
-        const float q00 = pr[0][0] * 16384.f, q10 = pr[1][0] * 16384.f, q01 = pr[0][1] * 16384.f, q11 = pr[1][1] * 16384.f;
-        const uint32_t h0 = f16x2(q00, q10), h1 = f16x2(q01, q11);
-        pb[nt][0] = transpose8x8(h0);
-        pb[nt][1] = transpose8x8(h1);
-        if constexpr (F32) {
-          const float2 y0 = f32x2(h0), y1 = f32x2(h1);
-          pl[nt][0] = transpose8x8(f16x2(q00 - y0.x, q10 - y0.y));
-          pl[nt][1] = transpose8x8(f16x2(q01 - y1.x, q11 - y1.y));
-        }
       }
-      // ---- o = o * corr + scale * (V^T P) ----
-      const uint4* vw = kw + D;  // 16 D bytes on
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      if (p.blk != nullptr) {  // the block's sums, for the accumulated weights
+        float2* note = p.blk + (vu * p.max_blocks + j) * ROWS;
 #pragma unroll
-      for (int jj = 0; jj < KS / 2; ++jj) {
-        const uint4 w = vw[jj * 32];
-        const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+        for (int nt = 0; nt < NT; ++nt) {
+          float t[2];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t a[4] = {e4m3x2_f16x2(wd[2 * y]), e4m3x2_f16x2(wd[2 * y + 1]), e4m3x2_f16x2(wd[2 * y] >> 16),
-                                 e4m3x2_f16x2(wd[2 * y + 1] >> 16)};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float t[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(t, a, pb[nt][0], pb[nt][1]);
-            if constexpr (F32) mma16816(t, a, pl[nt][0], pl[nt][1]);
-            float* oo = o[nt][2 * jj + y];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) oo[x] = oo[x] * corr[nt][x & 1] + t[x] * vsc[nt][x & 1];
+          for (int x = 0; x < 2; ++x) {
+            t[x] = blk_l[nt][x];
+            t[x] += __shfl_xor_sync(0xffffffffu, t[x], 4);
+            t[x] += __shfl_xor_sync(0xffffffffu, t[x], 8);
+            t[x] += __shfl_xor_sync(0xffffffffu, t[x], 16);
           }
+          const int r = rg * WR + nt * 8 + 2 * c;
+          if (g == 0 && seg.tile * ROWS + r < p.T * p.G)
+            *reinterpret_cast<float4*>(note + r) = make_float4(m_run[nt][0], t[0], m_run[nt][1], t[1]);
         }
       }
+    }
+    // ---- the warp's part of the segment goes to the helper ----
+    if (ok && k >= NB) ok = wait(&dump_free[k % NB], k / NB - 1);
+    if (!ok) break;
+    float* red = red_of(k) + warp * WR * Gm::RP;
+    float2* ml = ml_of(k) + warp * WR;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float l = l_run[nt][x];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (g == 0) ml[nt * 8 + 2 * c + x] = make_float2(m_run[nt][x], l);
+      }
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) red[(nt * 8 + 2 * c + (x & 1)) * Gm::RP + mt * 16 + g + 8 * (x >> 1)] = o[nt][mt][x];
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
-
-    if (de.w & kLast) {
-      // ---- the four warps' parts become the CTA's part of the unit ----
-      const long long slot = cta + vu;
-      bool ok = true;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt > 0 && !(ok = ok && sync4())) break;  // the buffer is free
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float l = l_run[nt][x];
-          l += __shfl_xor_sync(0xffffffffu, l, 4);
-          l += __shfl_xor_sync(0xffffffffu, l, 8);
-          l += __shfl_xor_sync(0xffffffffu, l, 16);
-          if (g == 0) red_ml[warp * 8 + 2 * c + x] = make_float2(m_run[nt][x], l);
-        }
-#pragma unroll
-        for (int mt = 0; mt < KS; ++mt)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            red[(warp * 8 + 2 * c + (x & 1)) * Gm::RP + mt * 16 + g + 8 * (x >> 1)] = o[nt][mt][x];
-        if (!(ok = ok && sync4())) break;
-        for (int i = tid; i < 8 * D / 4; i += 128) {
-          const int r = i / (D / 4), x = i % (D / 4);
-          float M = red_ml[r].x;
-#pragma unroll
-          for (int w = 1; w < 4; ++w) M = max_nan(M, red_ml[w * 8 + r].x);
-          const float mu = finite_max(M);
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float L = 0.f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const float2 ml = red_ml[w * 8 + r];
-            const float wt = exp_from(ml.x, mu);
-            const float4 y = *reinterpret_cast<const float4*>(red + (w * 8 + r) * Gm::RP + 4 * x);
-            acc.x += wt * y.x; acc.y += wt * y.y; acc.z += wt * y.z; acc.w += wt * y.w;
-            L += wt * ml.y;
-          }
-          const long long at = slot * ROWS + nt * 8 + r;
-          reinterpret_cast<float4*>(p.part_acc + at * D)[x] = acc;
-          if (x == 0) p.part_ml[at] = make_float2(M, L);
-        }
-      }
-      if (!ok) break;
-      if (!sync4()) break;  // the buffers are free for the next unit
-    }
+    if (lane == 0) mbar_arrive(&dump_full[k % NB]);
+  }
+  if (!ok && lane == 0) {
+    s_bad = 1;
+    quant_flag(p.status, kQErrWait);
   }
   __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
-// Tail attention and the join. Grid (units x tiles, z): CTA y of z owns d / z dims.
+// Tail attention and the join. Grid (units x tiles, z): CTA y of z writes d / z dims.
+// Before the stream has finished: the tail in fp32, eight rows at a time, its keys and
+// values in registers from one round of loads. After: every thread merges its share
+// of the unit's parts for four dims of a row, the shares join in shared memory.
 // ---------------------------------------------------------------------------
+constexpr int kQcRows = 8;
+
+template <int D>
+constexpr size_t combine_smem(int rows) {  // q, partial logits, weights, tail output, the join
+  return (size_t)(kQcRows * D + 4 * kQcRows * kQB + kQcRows * kQB + rows * D) * 4 + kQcThreads * (16 + 8);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams p, int rows) {
-  constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE, MAXR = 32;
+  constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE, MAXR = 64;
+  constexpr int KC = NCH / 4;                        // 16-byte key chunks of a thread: token tid % 64
+  constexpr int TG = kQcThreads / NCH, TPT = kQB / TG;  // value tokens: TPT of one 16-byte column
+  constexpr int CPW = 32 / TG;                       // columns of a warp; its lanes: token group x column
   extern __shared__ __align__(16) uint8_t csmem[];
-  float* q_s = reinterpret_cast<float*>(csmem);      // [rows][D]
-  float* p_s = q_s + rows * D;                       // [rows][64] logits, then weights (-1: masked)
-  float* o_s = p_s + rows * kQB;                     // [rows][dims] the tail's output, then the join's parts
-  __shared__ float m_s[MAXR], l_s[MAXR], inv_s[MAXR];
-  __shared__ int sees_s[MAXR];
+  float* q_s = reinterpret_cast<float*>(csmem);      // [8][D]
+  float* pd_s = q_s + kQcRows * D;                   // [4][8][64] partial logits
+  float* w_s = pd_s + 4 * kQcRows * kQB;             // [8][64] weights, -1: masked
+  float* o_s = w_s + kQcRows * kQB;                  // [rows][D] the tail's output
+  float4* ja_s = reinterpret_cast<float4*>(o_s + rows * D);    // [threads]
+  float2* jm_s = reinterpret_cast<float2*>(ja_s + kQcThreads);  // [threads]
+  __shared__ float m_s[MAXR], l_s[MAXR], tw_s[MAXR];
   griddep_launch_dependents();
   const int vu = blockIdx.x, u = vu / p.tiles, tile = vu % p.tiles, b = u / p.Hkv, h = u % p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -557,86 +733,100 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
   const int qn = quant_count(p.q_len, b, p.T, p.status, tid == 0);
   const int nb = n / kQB, nt = n % kQB;
   const int r0 = tile * rows, live = min(rows, max(0, qn * p.G - r0));  // rows of the tile that exist
-  const int dims = D / gridDim.y, d0 = blockIdx.y * dims;
-  const uint8_t* tail = p.tail + (long long)u * p.payload;
-  if (tid < live) sees_s[tid] = qa_row(r0 + tid, p.G, n, qn).sees;
-  if (nt > 0) {
-    const float scale = kQScale<D>;
-    for (int i = tid; i < live * (D / CE); i += kQcThreads) {
-      const int r = i / (D / CE), x = i % (D / CE);
-      const QRow w = qa_row(r0 + r, p.G, n, qn);
-      const T* src = reinterpret_cast<const T*>(p.q) + b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + x * CE;
-      const uint4 y = *reinterpret_cast<const uint4*>(src);
-      const T* e = reinterpret_cast<const T*>(&y);
+  if (nt > 0 && live > 0) {
+    const uint8_t* tail = p.tail + (long long)u * p.payload;
+    const int t = tid % kQB, cg = tid / kQB;
+    const int col = warp * CPW + lane % CPW, t0 = lane / CPW * TPT;
+    uint4 kr[KC], vr[TPT];
 #pragma unroll
-      for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = to_f32(e[k]) * scale;
-    }
-    __syncthreads();
-    // logits: a thread has one token and every fourth row
-    const int t = tid % kQB, rg = tid / kQB;
-    const float e = t < nt ? reinterpret_cast<const float*>(tail + 2 * (size_t)kQB * D * ELT)[t] : -INFINITY;
-    float dot[MAXR / 4];
+    for (int i = 0; i < KC; ++i)
+      kr[i] = t < nt ? *reinterpret_cast<const uint4*>(tail + ((size_t)(cg * KC + i) * kQB + t) * 16) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int k = 0; k < MAXR / 4; ++k) dot[k] = 0.f;
-    if (t < nt) {
-#pragma unroll 4
-      for (int ch = 0; ch < NCH; ++ch) {
-        const uint4 y = *reinterpret_cast<const uint4*>(tail + ((size_t)ch * kQB + t) * 16);
-        const T* kv = reinterpret_cast<const T*>(&y);
+    for (int i = 0; i < TPT; ++i)
+      vr[i] = t0 + i < nt ? *reinterpret_cast<const uint4*>(tail + (size_t)kQB * D * ELT + (size_t)(t0 + i) * D * ELT + col * 16)
+                          : make_uint4(0, 0, 0, 0);
+    const float* es = reinterpret_cast<const float*>(tail + 2 * (size_t)kQB * D * ELT);
+    const float e0 = lane < nt ? es[lane] : -INFINITY, e1 = lane + 32 < nt ? es[lane + 32] : -INFINITY;
+    for (int rb = 0; rb < live; rb += kQcRows) {
+      const int cnt = min(kQcRows, live - rb);
+      for (int i = tid; i < cnt * NCH; i += kQcThreads) {
+        const int r = i / NCH, x = i % NCH;
+        const QRow w = qa_row(r0 + rb + r, p.G, n, qn);
+        const T* src = reinterpret_cast<const T*>(p.q) + b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + x * CE;
+        const uint4 y = *reinterpret_cast<const uint4*>(src);
+        const T* e = reinterpret_cast<const T*>(&y);
 #pragma unroll
-        for (int k = 0; k < MAXR / 4; ++k) {
-          const int r = rg + 4 * k;
-          if (r < live) {
+        for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = to_f32(e[k]) * kQScale<D>;
+      }
+      __syncthreads();
 #pragma unroll
-            for (int x = 0; x < CE; ++x) dot[k] += q_s[r * D + ch * CE + x] * to_f32(kv[x]);
+      for (int r = 0; r < kQcRows; ++r) {
+        if (r < cnt) {
+          float dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < KC; ++i) {
+            const T* kv = reinterpret_cast<const T*>(&kr[i]);
+            const float* qv = q_s + r * D + (cg * KC + i) * CE;
+#pragma unroll
+            for (int x = 0; x < CE; ++x) dot += qv[x] * to_f32(kv[x]);
           }
+          pd_s[(cg * kQcRows + r) * kQB + t] = dot;
         }
       }
-    }
+      __syncthreads();
+      if (warp < cnt) {  // a warp has a row
+        const int sees = qa_row(r0 + rb + warp, p.G, n, qn).sees - nb * kQB;
+        float x0 = e0, x1 = e1;
 #pragma unroll
-    for (int k = 0; k < MAXR / 4; ++k) {
-      const int r = rg + 4 * k;
-      if (r < live) p_s[r * kQB + t] = (e == -INFINITY || nb * kQB + t >= sees_s[r]) ? -INFINITY : dot[k] + e;
-    }
-    __syncthreads();
-    for (int r = warp; r < live; r += kQcThreads / 32) {
-      const float x0 = p_s[r * kQB + lane], x1 = p_s[r * kQB + 32 + lane];
-      float m = max_nan(x0, x1);
+        for (int k = 0; k < 4; ++k) {
+          x0 += pd_s[(k * kQcRows + warp) * kQB + lane];
+          x1 += pd_s[(k * kQcRows + warp) * kQB + 32 + lane];
+        }
+        if (e0 == -INFINITY || lane >= sees) x0 = -INFINITY;
+        if (e1 == -INFINITY || lane + 32 >= sees) x1 = -INFINITY;
+        float m = max_nan(x0, x1);
 #pragma unroll
-      for (int s = 1; s < 32; s <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
-      const float mu = finite_max(m), y0 = exp_from(x0, mu), y1 = exp_from(x1, mu);
-      float l = y0 + y1;
+        for (int s = 1; s < 32; s <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
+        const float mu = finite_max(m), y0 = exp_from(x0, mu), y1 = exp_from(x1, mu);
+        float l = y0 + y1;
 #pragma unroll
-      for (int s = 1; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-      p_s[r * kQB + lane] = x0 == -INFINITY ? -1.f : y0;
-      p_s[r * kQB + 32 + lane] = x1 == -INFINITY ? -1.f : y1;
-      if (lane == 0) {
-        m_s[r] = m;
-        l_s[r] = l;
+        for (int s = 1; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+        w_s[warp * kQB + lane] = x0 == -INFINITY ? -1.f : y0;
+        w_s[warp * kQB + 32 + lane] = x1 == -INFINITY ? -1.f : y1;
+        if (lane == 0) {
+          m_s[rb + warp] = m;
+          l_s[rb + warp] = l;
+        }
       }
-    }
-    __syncthreads();
-    const T* vt = reinterpret_cast<const T*>(tail + (size_t)kQB * D * ELT) + d0;
-    for (int i = tid; i < live * dims; i += kQcThreads) {
-      const int r = i / dims, x = i % dims;
-      float acc = 0.f;
-#pragma unroll 8
-      for (int t2 = 0; t2 < nt; ++t2) {
-        const float w = p_s[r * kQB + t2];
-        if (w >= 0.f || w != w) acc += w * to_f32(vt[t2 * D + x]);  // a masked token's value is not looked at
+      __syncthreads();
+#pragma unroll 1
+      for (int r = 0; r < cnt; ++r) {
+        float acc[CE];
+#pragma unroll
+        for (int x = 0; x < CE; ++x) acc[x] = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPT; ++i) {
+          const float w = w_s[r * kQB + t0 + i];
+          const T* vv = reinterpret_cast<const T*>(&vr[i]);
+          if (!(w < 0.f)) {  // a masked token's value is not looked at
+#pragma unroll
+            for (int x = 0; x < CE; ++x) acc[x] += w * to_f32(vv[x]);
+          }
+        }
+#pragma unroll
+        for (int s = CPW; s < 32; s <<= 1)
+#pragma unroll
+          for (int x = 0; x < CE; ++x) acc[x] += __shfl_xor_sync(0xffffffffu, acc[x], s);
+        if (lane < CPW) {
+#pragma unroll
+          for (int x = 0; x < CE; ++x) o_s[(rb + r) * D + col * CE + x] = acc[x];
+        }
       }
-      o_s[i] = acc;
+      __syncthreads();
     }
-  } else {
-    if (tid < live) {
-      m_s[tid] = -INFINITY;
-      l_s[tid] = 0.f;
-    }
-    for (int i = tid; i < live * dims; i += kQcThreads) o_s[i] = 0.f;
   }
-  __syncthreads();
   griddep_wait();  // the stream's parts
-  // parts of this unit and tile: CTAs [c0, c1] of the stream, slot c + vu each
+  // parts of this unit and tile: CTAs [c0, c0 + parts) of the stream, slot c + vu each
   int c0 = 0, parts = 0;
   if (nb > 0) {
     const long long total = *p.total, first = p.base[vu];
@@ -645,131 +835,132 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
     parts = qa_cta_of(first + nb - 1, total, active) - c0 + 1;
   }
   const long long slot0 = (long long)c0 + vu;
-  float tw = 0.f;
-  for (int r = warp; r < live; r += kQcThreads / 32) {
-    float m = m_s[r];
-    for (int i = lane; i < parts; i += 32) m = max_nan(m, p.part_ml[(slot0 + i) * rows + r].x);
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
-    const float mu = finite_max(m);
-    float l = 0.f;
-    for (int i = lane; i < parts; i += 32) {
-      const float2 ml = p.part_ml[(slot0 + i) * rows + r];
-      l += ml.y * exp_from(ml.x, mu);
-    }
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-    const float lt = l_s[r] * exp_from(m_s[r], mu);
-    l += lt;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __syncwarp();
-    if (lane == 0) {
-      const float tail_scale = exp_from(m_s[r], mu) * inv;
-      m_s[r] = mu;
-      inv_s[r] = inv;
-      l_s[r] = tail_scale;
-      if (blockIdx.y == 0) {
-        const QRow w = qa_row(r0 + r, p.G, n, qn);
-        if (p.lse != nullptr)
-          p.lse[((long long)b * p.T + w.t) * p.Hq + h * p.G + w.g] = l == 0.f ? -INFINITY : mu + logf(l);
-        if (p.blk != nullptr) p.rowstat[(long long)vu * rows + r] = make_float2(mu, inv);
-      }
-      tw += lt * inv;
-    }
-  }
-  __syncthreads();
-  if (p.blk != nullptr && blockIdx.y == 0) {
-    // the tail's weight over the rows, in a fixed order; rows that do not exist weigh nothing
-    __shared__ float tw_s[kQcThreads / 32];
-    if (lane == 0) tw_s[warp] = tw;
-    for (int r = live + tid; r < rows; r += kQcThreads) p.rowstat[(long long)vu * rows + r] = make_float2(0.f, 0.f);
-    __syncthreads();
-    if (tid == 0) {
-      float s = 0.f;
-      for (int w = 0; w < kQcThreads / 32; ++w) s += tw_s[w];
-      p.tail_w[vu] = s;
-    }
-  }
-  // outputs: groups of threads take every gth part, joined through shared memory
-  const int vec = live * dims / 4;  // float4 outputs
+  const int dims = D / gridDim.y, d0 = blockIdx.y * dims, cols = dims / 4, vec = live * cols;
   int groups = 1;
-  while (groups * 2 * vec <= kQcThreads && groups * 2 <= parts) groups *= 2;
-  float4* part_s = reinterpret_cast<float4*>(o_s + rows * dims);  // [groups][vec] where groups > 1
+  while (groups * 2 * vec <= kQcThreads && groups < parts) groups *= 2;
   for (int base = 0; base < vec; base += kQcThreads) {
-    const int slot_i = groups > 1 ? tid % vec : base + tid, grp = groups > 1 ? tid / vec : 0;
-    const bool on = slot_i < vec && grp < groups;
+    const int at = groups > 1 ? tid % vec : base + tid, grp = groups > 1 ? tid / vec : 0;
+    const bool on = at < vec && grp < groups;
+    const int r = on ? at / cols : 0, x = on ? at % cols : 0;
+    float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    int r = 0, x = 0;
+    auto merge = [&](float2 ml, float4 y) {
+      const float mn = max_nan(m, ml.x), mu = finite_max(mn);
+      const float a = exp_from(m, mu), c = exp_from(ml.x, mu);
+      acc.x = acc.x * a + y.x * c; acc.y = acc.y * a + y.y * c; acc.z = acc.z * a + y.z * c; acc.w = acc.w * a + y.w * c;
+      l = l * a + ml.y * c;
+      m = mn;
+    };
     if (on) {
-      r = slot_i / (dims / 4);
-      x = slot_i % (dims / 4);
-      const float mu = m_s[r], inv = inv_s[r];
       const float* src = p.part_acc + (slot0 * rows + r) * D + d0 + 4 * x;
       const float2* ml = p.part_ml + slot0 * rows + r;
-#pragma unroll 4
-      for (int i = grp; i < parts; i += groups) {
-        const float w = exp_from(ml[(long long)i * rows].x, mu) * inv;
-        const float4 y = *reinterpret_cast<const float4*>(src + (long long)i * rows * D);
-        acc.x += w * y.x; acc.y += w * y.y; acc.z += w * y.z; acc.w += w * y.w;
+      for (int i0 = grp; i0 < parts; i0 += 4 * groups) {
+        float2 mm[4];
+        float4 yy[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + k * groups;
+          mm[k] = i < parts ? ml[(long long)i * rows] : make_float2(-INFINITY, 0.f);
+          yy[k] = i < parts ? *reinterpret_cast<const float4*>(src + (long long)i * rows * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) merge(mm[k], yy[k]);
       }
     }
     if (groups > 1) {
-      if (on && grp > 0) part_s[grp * vec + slot_i] = acc;
+      if (on && grp > 0) {
+        ja_s[grp * vec + at] = acc;
+        jm_s[grp * vec + at] = make_float2(m, l);
+      }
       __syncthreads();
       if (on && grp == 0)
-        for (int k = 1; k < groups; ++k) {
-          const float4 y = part_s[k * vec + slot_i];
-          acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
-        }
+        for (int k = 1; k < groups; ++k) merge(jm_s[k * vec + at], ja_s[k * vec + at]);
     }
     if (on && grp == 0) {
-      const float ts = l_s[r];
-      const float4 y = *reinterpret_cast<const float4*>(o_s + r * dims + 4 * x);
-      if (nt > 0) {
-        acc.x += ts * y.x; acc.y += ts * y.y; acc.z += ts * y.z; acc.w += ts * y.w;
-      }
+      if (nt > 0) merge(make_float2(m_s[r], l_s[r]), *reinterpret_cast<const float4*>(o_s + r * D + d0 + 4 * x));
+      const float mu = finite_max(m), inv = l == 0.f ? 0.f : 1.f / l;
       const QRow w = qa_row(r0 + r, p.G, n, qn);
-      T* dst = reinterpret_cast<T*>(p.out) + (((long long)b * p.T + w.t) * p.Hq + h * p.G + w.g) * D + d0 + 4 * x;
-      dst[0] = from_f32<T>(acc.x);
-      dst[1] = from_f32<T>(acc.y);
-      dst[2] = from_f32<T>(acc.z);
-      dst[3] = from_f32<T>(acc.w);
+      const long long row = ((long long)b * p.T + w.t) * p.Hq + h * p.G + w.g;
+      T* dst = reinterpret_cast<T*>(p.out) + row * D + d0 + 4 * x;
+      if constexpr (ELT == 4) {
+        *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      } else {
+        const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+      }
+      if (x == 0 && blockIdx.y == 0) {
+        if (p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : mu + logf(l);
+        if (p.blk != nullptr) {
+          p.rowstat[(long long)vu * rows + r] = make_float2(mu, inv);
+          tw_s[r] = nt > 0 ? l_s[r] * exp_from(m_s[r], mu) * inv : 0.f;
+        }
+      }
+    }
+  }
+  if (p.blk != nullptr && blockIdx.y == 0) {
+    for (int r = live + tid; r < rows; r += kQcThreads) p.rowstat[(long long)vu * rows + r] = make_float2(0.f, 0.f);
+    __syncthreads();
+    if (tid == 0) {  // the tail's weight, the rows in order
+      float w = 0.f;
+      for (int r = 0; r < live; ++r) w += tw_s[r];
+      p.tail_w[vu] = w;
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Accumulated weights: a warp per block. mass = decay * mass + sum over the tiles,
-// slices and rows of (slice sum) * exp(slice maximum - row maximum) / row sum, the
-// lanes in a fixed order. Entries without tokens only decay.
+// Accumulated weights: mass = decay * mass + sum over the tiles and rows of
+// (block sum) * exp(block maximum - row maximum) / row sum, the lanes in a fixed
+// order. Entries without tokens only decay. A warp takes 32 / min(rows, 32) blocks at
+// once, four times.
 // ---------------------------------------------------------------------------
 template <int ROWS>
+__host__ __device__ constexpr int weights_per_cta() {
+  return kQcThreads / 32 * (ROWS < 32 ? 32 / ROWS : 1) * 4;
+}
+
+template <int ROWS>
 __global__ void __launch_bounds__(kQcThreads) quant_weights_kernel(QStreamParams p) {
+  constexpr int RL = ROWS < 32 ? ROWS : 32, PW = 32 / RL, RPL = ROWS / RL;  // lanes of a block, blocks at once, rows of a lane
   const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)), nb = n / kQB, nt = n % kQB;
-  griddep_wait();
-  for (int j = blockIdx.y * (kQcThreads / 32) + warp; j < p.max_blocks; j += gridDim.y * (kQcThreads / 32)) {
-    float w = 0.f;
-    if (j < nb) {
-      for (int tile = 0; tile < p.tiles; ++tile) {
-        const long long vu = (long long)u * p.tiles + tile;
-        const float2* note = p.blk + (vu * p.max_blocks + j) * 4 * ROWS;
+  const int first = blockIdx.y * weights_per_cta<ROWS>() + warp * PW * 4 + lane / RL, r0 = lane % RL;
+  float* mass = p.mass + (long long)u * p.max_blocks;
+  float old[4], w[4];
 #pragma unroll
-        for (int i = 0; i < ROWS / 8; ++i) {
-          const int x = lane + 32 * i;
-          const float2 ml = note[x], st = p.rowstat[vu * ROWS + x % ROWS];
-          w += ml.y * exp_from(ml.x, st.x) * st.y;
-        }
+  for (int i = 0; i < 4; ++i) {
+    const int j = first + i * PW;
+    old[i] = r0 == 0 && j < p.max_blocks && p.decay != 0.f ? mass[j] * p.decay : 0.f;
+    w[i] = 0.f;
+  }
+  griddep_wait();
+  for (int tile = 0; tile < p.tiles; ++tile) {
+    const long long vu = (long long)u * p.tiles + tile;
+#pragma unroll
+    for (int k = 0; k < RPL; ++k) {
+      const int r = r0 + k * RL;
+      const bool on = tile * ROWS + r < p.T * p.G;
+      const float2 st = on ? p.rowstat[vu * ROWS + r] : make_float2(0.f, 0.f);
+      float2 ml[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = first + i * PW;
+        ml[i] = on && j < nb ? p.blk[(vu * p.max_blocks + j) * ROWS + r] : make_float2(-INFINITY, 0.f);
       }
 #pragma unroll
-      for (int s = 1; s < 32; s <<= 1) w += __shfl_xor_sync(0xffffffffu, w, s);
-    } else if (j == nb && nt > 0) {
-      for (int tile = 0; tile < p.tiles; ++tile) w += p.tail_w[(long long)u * p.tiles + tile];
+      for (int i = 0; i < 4; ++i) {
+        const int j = first + i * PW;
+        if (on && j < nb) w[i] += ml[i].y * exp_from(ml[i].x, st.x) * st.y;
+        if (j == nb && nt > 0 && r == 0) w[i] += p.tail_w[vu];
+      }
     }
-    if (lane == 0) {
-      float* m = p.mass + (long long)u * p.max_blocks + j;
-      *m = (p.decay == 0.f ? 0.f : *m * p.decay) + w;
-    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = first + i * PW;
+#pragma unroll
+    for (int s = 1; s < RL; s <<= 1) w[i] += __shfl_xor_sync(0xffffffffu, w[i], s);
+    if (r0 == 0 && j < p.max_blocks) mass[j] = old[i] + w[i];
   }
 }
 
@@ -801,33 +992,39 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, int NT, bool F32>
+template <int D, int NT, int RG, bool F32>
 cudaError_t stream_variant(const QPlan& pl, const QStreamParams& p, cudaStream_t stream) {
-  constexpr int smem = QGeom<D, NT, F32>::SMEM;
+  using Gm = QGeom<D, NT, RG, F32>;
   static std::atomic<int> lim[64];
-  const cudaError_t e = raise_smem_limit((const void*)quant_stream_kernel<D, NT, F32>, smem, lim);
+  const cudaError_t e = raise_smem_limit((const void*)quant_stream_kernel<D, NT, RG, F32>, Gm::SMEM, lim);
   if (e != cudaSuccess) return e;
-  quant_stream_kernel<D, NT, F32><<<pl.ctas, kQaThreads, smem, stream>>>(p);
+  quant_stream_kernel<D, NT, RG, F32><<<pl.ctas, Gm::THREADS, Gm::SMEM, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t stream_launches(const Shape& s, const QPlan& pl, const QStreamParams& p, cudaStream_t stream) {
   constexpr bool F32 = sizeof(T) == 4;
-  cudaError_t e = pl.rows == 8    ? stream_variant<D, 1, F32>(pl, p, stream)
-                  : pl.rows == 16 ? stream_variant<D, 2, F32>(pl, p, stream)
-                                  : stream_variant<D, 4, F32>(pl, p, stream);
+  cudaError_t e = pl.rows == 8    ? stream_variant<D, 1, 1, F32>(pl, p, stream)
+                  : pl.rows == 16 ? stream_variant<D, 2, 1, F32>(pl, p, stream)
+                  : pl.rows == 32 ? stream_variant<D, 2, 2, F32>(pl, p, stream)
+                                  : stream_variant<D, 2, 4, F32>(pl, p, stream);
   if (e != cudaSuccess) return e;
-  const int vu = s.U * pl.tiles;
-  const int z = vu * 4 <= 304 ? 4 : vu * 2 <= 304 ? 2 : 1;
-  const size_t smem = (size_t)pl.rows * (D + kQB + D / z) * 4 + kQcThreads * 16;
+  // few units have many parts each: more CTAs share the join
+  const int vu = s.U * pl.tiles, z = vu <= 16 ? 4 : vu <= 32 ? 2 : 1;
+  const size_t smem = combine_smem<D>(pl.rows);
+  static std::atomic<int> lim[64];
+  e = raise_smem_limit((const void*)quant_combine_kernel<T, D>, smem, lim);
+  if (e != cudaSuccess) return e;
   e = launch_dependent(quant_combine_kernel<T, D>, dim3(vu, z), kQcThreads, smem, stream, p, pl.rows);
   if (e != cudaSuccess || p.mass == nullptr) return e;
-  const int y = std::min(p.max_blocks, std::max(1, (p.max_blocks + 31) / 32));
-  const dim3 grid(s.U, y);
-  return pl.rows == 8    ? launch_dependent(quant_weights_kernel<8>, grid, kQcThreads, 0, stream, p)
-         : pl.rows == 16 ? launch_dependent(quant_weights_kernel<16>, grid, kQcThreads, 0, stream, p)
-                         : launch_dependent(quant_weights_kernel<32>, grid, kQcThreads, 0, stream, p);
+  auto weights = [&](auto kernel, int per) {
+    return launch_dependent(kernel, dim3(s.U, (p.max_blocks + per - 1) / per), kQcThreads, 0, stream, p);
+  };
+  return pl.rows == 8    ? weights(quant_weights_kernel<8>, weights_per_cta<8>())
+         : pl.rows == 16 ? weights(quant_weights_kernel<16>, weights_per_cta<16>())
+         : pl.rows == 32 ? weights(quant_weights_kernel<32>, weights_per_cta<32>())
+                         : weights(quant_weights_kernel<64>, weights_per_cta<64>());
 }
 #endif
 
