@@ -30,7 +30,7 @@ Layout layout(const Shape& s, const QPlan& pl, int max_blocks, bool mass) {
   w.part_ml = take(slots * pl.rows * 8);
   w.part_acc = take(slots * pl.rows * s.d * 4);
   w.rowstat = take(vu * pl.rows * 8);
-  w.tail_w = take(vu * 4);
+  w.tail_w = take(vu * pl.rows * 4);
   w.blk = take(mass ? vu * max_blocks * pl.rows * 8 : 0);
   w.total = at;
   return w;
@@ -38,12 +38,12 @@ Layout layout(const Shape& s, const QPlan& pl, int max_blocks, bool mass) {
 
 }  // namespace
 
-// Rows of a tile: 8, 16, 32 or 64, the least that holds the call's rows: the rows of a
+// Rows of a tile: 8, 16 or 32, the least that holds the call's rows: the rows of a
 // tile share one pass over the cache, and every row costs its products.
 QPlan quant_attn_plan(const Shape& s, int T) {
   QPlan pl;
   const int rows = T * s.G;
-  pl.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  pl.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   pl.tiles = (rows + pl.rows - 1) / pl.rows;
   pl.ctas = sm_count();
   return pl;

@@ -73,7 +73,7 @@ struct QStreamParams {
   float2* part_ml;    // [ctas + units x tiles][rows] maximum and sum of a part
   float* part_acc;    // ... [rows][d] its output (not normalised)
   float2* rowstat;    // [units x tiles][rows] final maximum and 1 / sum
-  float* tail_w;      // [units x tiles] weight of the tail
+  float* tail_w;      // [units x tiles][rows] weight of the tail
   float2* blk;        // [units x tiles][max_blocks][rows] maximum and sum of a block, or null
 };
 
@@ -154,10 +154,12 @@ __device__ __forceinline__ QRow qa_row(int r, int G, int n, int qn) {
 template <int D, int NT, int RG, bool F32>
 struct QGeom {
   static constexpr int ROWS = 8 * NT * RG, KS = D / 16, UB = quant_unit_bytes(D);
-  static constexpr int IS = NT == 1 ? (D == 128 ? 4 : 8) : RG == 1 ? (D == 128 ? 5 : 6) : 8 / RG;
+  // Eight warps in all leave each one 255 registers, which 16 rows of output need; more
+  // leave 168.
+  static constexpr int IS = NT == 1 ? (D == 128 ? 4 : 8) : RG == 1 ? 6 : 3;
   static constexpr int W = IS * RG;             // consumer warps; a producer and a helper come on top
   static constexpr int THREADS = 32 * (W + 2);
-  static constexpr int STAGES = D == 64 ? 2 * 8 / IS * IS : RG == 1 ? 2 * IS : RG == 4 && F32 ? 6 : 8;
+  static constexpr int STAGES = D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 8 : RG == 1 ? 6 : 9;
   static constexpr int SL = NT == 1 ? 4 : 2;    // slices of a block that a warp takes at once
   static constexpr int NB = NT == 1 ? 2 : 1;    // buffers for queries and for parts
   static constexpr int RP = D + 4;              // padded row of a part
@@ -380,6 +382,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
         seek();
         moved = true;
       }
+      if (!__any_sync(0xffffffffu, moved)) __nanosleep(40);  // (leaves the issue slots to the others)
       if (__any_sync(0xffffffffu, moved)) {
         spin = 0;
         since = global_ns();
@@ -700,39 +703,35 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
 }
 
 // ---------------------------------------------------------------------------
-// Tail attention and the join. Grid (units x tiles, z): CTA y of z writes d / z dims.
-// Before the stream has finished: the tail in fp32, eight rows at a time, its keys and
+// Tail attention and the join. Grid (units x tiles, row groups of 8, z): a CTA writes
+// d / z dims of 8 rows. Before the stream has finished: the tail in fp32, its keys and
 // values in registers from one round of loads. After: every thread merges its share
 // of the unit's parts for four dims of a row, the shares join in shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kQcRows = 8;
 
-template <int D>
-constexpr size_t combine_smem(int rows) {  // q, partial logits, weights, tail output, the join
-  return (size_t)(kQcRows * D + 4 * kQcRows * kQB + kQcRows * kQB + rows * D) * 4 + kQcThreads * (16 + 8);
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams p, int rows) {
-  constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE, MAXR = 64;
+  constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE;
   constexpr int KC = NCH / 4;                        // 16-byte key chunks of a thread: token tid % 64
   constexpr int TG = kQcThreads / NCH, TPT = kQB / TG;  // value tokens: TPT of one 16-byte column
   constexpr int CPW = 32 / TG;                       // columns of a warp; its lanes: token group x column
-  extern __shared__ __align__(16) uint8_t csmem[];
-  float* q_s = reinterpret_cast<float*>(csmem);      // [8][D]
-  float* pd_s = q_s + kQcRows * D;                   // [4][8][64] partial logits
-  float* w_s = pd_s + 4 * kQcRows * kQB;             // [8][64] weights, -1: masked
-  float* o_s = w_s + kQcRows * kQB;                  // [rows][D] the tail's output
-  float4* ja_s = reinterpret_cast<float4*>(o_s + rows * D);    // [threads]
-  float2* jm_s = reinterpret_cast<float2*>(ja_s + kQcThreads);  // [threads]
-  __shared__ float m_s[MAXR], l_s[MAXR], tw_s[MAXR];
+  __shared__ __align__(16) float q_s[kQcRows * D];
+  __shared__ __align__(16) float o_s[kQcRows * D];   // the tail's output
+  __shared__ float pd_s[4][kQcRows][kQB];            // partial logits
+  __shared__ float w_s[kQcRows][kQB];                // weights, -1: masked
+  __shared__ float4 ja_s[kQcThreads];
+  __shared__ float2 jm_s[kQcThreads];
+  __shared__ float m_s[kQcRows], l_s[kQcRows];
   griddep_launch_dependents();
   const int vu = blockIdx.x, u = vu / p.tiles, tile = vu % p.tiles, b = u / p.Hkv, h = u % p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n = max(0, quant_len(p.lens, u, p.max_blocks, p.status, tid == 0));
-  const int qn = quant_count(p.q_len, b, p.T, p.status, tid == 0);
+  const bool flag = tid == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+  const int n = max(0, quant_len(p.lens, u, p.max_blocks, p.status, flag));
+  const int qn = quant_count(p.q_len, b, p.T, p.status, flag);
   const int nb = n / kQB, nt = n % kQB;
-  const int r0 = tile * rows, live = min(rows, max(0, qn * p.G - r0));  // rows of the tile that exist
+  const int rt = blockIdx.y * kQcRows, r0 = tile * rows + rt;        // first row, in the tile and in the request
+  const int live = min(kQcRows, max(0, qn * p.G - r0));              // rows that exist
   if (nt > 0 && live > 0) {
     const uint8_t* tail = p.tail + (long long)u * p.payload;
     const int t = tid % kQB, cg = tid / kQB;
@@ -747,83 +746,80 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
                           : make_uint4(0, 0, 0, 0);
     const float* es = reinterpret_cast<const float*>(tail + 2 * (size_t)kQB * D * ELT);
     const float e0 = lane < nt ? es[lane] : -INFINITY, e1 = lane + 32 < nt ? es[lane + 32] : -INFINITY;
-    for (int rb = 0; rb < live; rb += kQcRows) {
-      const int cnt = min(kQcRows, live - rb);
-      for (int i = tid; i < cnt * NCH; i += kQcThreads) {
-        const int r = i / NCH, x = i % NCH;
-        const QRow w = qa_row(r0 + rb + r, p.G, n, qn);
-        const T* src = reinterpret_cast<const T*>(p.q) + b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + x * CE;
-        const uint4 y = *reinterpret_cast<const uint4*>(src);
-        const T* e = reinterpret_cast<const T*>(&y);
+    for (int i = tid; i < live * NCH; i += kQcThreads) {
+      const int r = i / NCH, x = i % NCH;
+      const QRow w = qa_row(r0 + r, p.G, n, qn);
+      const T* src = reinterpret_cast<const T*>(p.q) + b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + x * CE;
+      const uint4 y = *reinterpret_cast<const uint4*>(src);
+      const T* e = reinterpret_cast<const T*>(&y);
 #pragma unroll
-        for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = to_f32(e[k]) * kQScale<D>;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int r = 0; r < kQcRows; ++r) {
-        if (r < cnt) {
-          float dot = 0.f;
-#pragma unroll
-          for (int i = 0; i < KC; ++i) {
-            const T* kv = reinterpret_cast<const T*>(&kr[i]);
-            const float* qv = q_s + r * D + (cg * KC + i) * CE;
-#pragma unroll
-            for (int x = 0; x < CE; ++x) dot += qv[x] * to_f32(kv[x]);
-          }
-          pd_s[(cg * kQcRows + r) * kQB + t] = dot;
-        }
-      }
-      __syncthreads();
-      if (warp < cnt) {  // a warp has a row
-        const int sees = qa_row(r0 + rb + warp, p.G, n, qn).sees - nb * kQB;
-        float x0 = e0, x1 = e1;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x0 += pd_s[(k * kQcRows + warp) * kQB + lane];
-          x1 += pd_s[(k * kQcRows + warp) * kQB + 32 + lane];
-        }
-        if (e0 == -INFINITY || lane >= sees) x0 = -INFINITY;
-        if (e1 == -INFINITY || lane + 32 >= sees) x1 = -INFINITY;
-        float m = max_nan(x0, x1);
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
-        const float mu = finite_max(m), y0 = exp_from(x0, mu), y1 = exp_from(x1, mu);
-        float l = y0 + y1;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-        w_s[warp * kQB + lane] = x0 == -INFINITY ? -1.f : y0;
-        w_s[warp * kQB + 32 + lane] = x1 == -INFINITY ? -1.f : y1;
-        if (lane == 0) {
-          m_s[rb + warp] = m;
-          l_s[rb + warp] = l;
-        }
-      }
-      __syncthreads();
-#pragma unroll 1
-      for (int r = 0; r < cnt; ++r) {
-        float acc[CE];
-#pragma unroll
-        for (int x = 0; x < CE; ++x) acc[x] = 0.f;
-#pragma unroll
-        for (int i = 0; i < TPT; ++i) {
-          const float w = w_s[r * kQB + t0 + i];
-          const T* vv = reinterpret_cast<const T*>(&vr[i]);
-          if (!(w < 0.f)) {  // a masked token's value is not looked at
-#pragma unroll
-            for (int x = 0; x < CE; ++x) acc[x] += w * to_f32(vv[x]);
-          }
-        }
-#pragma unroll
-        for (int s = CPW; s < 32; s <<= 1)
-#pragma unroll
-          for (int x = 0; x < CE; ++x) acc[x] += __shfl_xor_sync(0xffffffffu, acc[x], s);
-        if (lane < CPW) {
-#pragma unroll
-          for (int x = 0; x < CE; ++x) o_s[(rb + r) * D + col * CE + x] = acc[x];
-        }
-      }
-      __syncthreads();
+      for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = to_f32(e[k]) * kQScale<D>;
     }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kQcRows; ++r) {
+      if (r < live) {
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+          const T* kv = reinterpret_cast<const T*>(&kr[i]);
+          const float* qv = q_s + r * D + (cg * KC + i) * CE;
+#pragma unroll
+          for (int x = 0; x < CE; ++x) dot += qv[x] * to_f32(kv[x]);
+        }
+        pd_s[cg][r][t] = dot;
+      }
+    }
+    __syncthreads();
+    if (warp < live) {  // a warp has a row
+      const int sees = qa_row(r0 + warp, p.G, n, qn).sees - nb * kQB;
+      float x0 = e0, x1 = e1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x0 += pd_s[k][warp][lane];
+        x1 += pd_s[k][warp][32 + lane];
+      }
+      if (e0 == -INFINITY || lane >= sees) x0 = -INFINITY;
+      if (e1 == -INFINITY || lane + 32 >= sees) x1 = -INFINITY;
+      float m = max_nan(x0, x1);
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
+      const float mu = finite_max(m), y0 = exp_from(x0, mu), y1 = exp_from(x1, mu);
+      float l = y0 + y1;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+      w_s[warp][lane] = x0 == -INFINITY ? -1.f : y0;
+      w_s[warp][32 + lane] = x1 == -INFINITY ? -1.f : y1;
+      if (lane == 0) {
+        m_s[warp] = m;
+        l_s[warp] = l;
+      }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int r = 0; r < live; ++r) {
+      float acc[CE];
+#pragma unroll
+      for (int x = 0; x < CE; ++x) acc[x] = 0.f;
+#pragma unroll
+      for (int i = 0; i < TPT; ++i) {
+        const float w = w_s[r][t0 + i];
+        const T* vv = reinterpret_cast<const T*>(&vr[i]);
+        if (!(w < 0.f)) {  // a masked token's value is not looked at
+#pragma unroll
+          for (int x = 0; x < CE; ++x) acc[x] += w * to_f32(vv[x]);
+        }
+      }
+#pragma unroll
+      for (int s = CPW; s < 32; s <<= 1)
+#pragma unroll
+        for (int x = 0; x < CE; ++x) acc[x] += __shfl_xor_sync(0xffffffffu, acc[x], s);
+      if (lane < CPW) {
+#pragma unroll
+        for (int x = 0; x < CE; ++x) o_s[r * D + col * CE + x] = acc[x];
+      }
+    }
+    __syncthreads();
   }
   griddep_wait();  // the stream's parts
   // parts of this unit and tile: CTAs [c0, c0 + parts) of the stream, slot c + vu each
@@ -835,132 +831,121 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
     parts = qa_cta_of(first + nb - 1, total, active) - c0 + 1;
   }
   const long long slot0 = (long long)c0 + vu;
-  const int dims = D / gridDim.y, d0 = blockIdx.y * dims, cols = dims / 4, vec = live * cols;
+  const int dims = D / gridDim.z, d0 = blockIdx.z * dims, cols = dims / 4, vec = live * cols;  // vec <= the threads
   int groups = 1;
   while (groups * 2 * vec <= kQcThreads && groups < parts) groups *= 2;
-  for (int base = 0; base < vec; base += kQcThreads) {
-    const int at = groups > 1 ? tid % vec : base + tid, grp = groups > 1 ? tid / vec : 0;
-    const bool on = at < vec && grp < groups;
-    const int r = on ? at / cols : 0, x = on ? at % cols : 0;
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto merge = [&](float2 ml, float4 y) {
-      const float mn = max_nan(m, ml.x), mu = finite_max(mn);
-      const float a = exp_from(m, mu), c = exp_from(ml.x, mu);
-      acc.x = acc.x * a + y.x * c; acc.y = acc.y * a + y.y * c; acc.z = acc.z * a + y.z * c; acc.w = acc.w * a + y.w * c;
-      l = l * a + ml.y * c;
-      m = mn;
-    };
-    if (on) {
-      const float* src = p.part_acc + (slot0 * rows + r) * D + d0 + 4 * x;
-      const float2* ml = p.part_ml + slot0 * rows + r;
-      for (int i0 = grp; i0 < parts; i0 += 4 * groups) {
-        float2 mm[4];
-        float4 yy[4];
+  const int at = vec > 0 ? tid % vec : 0, grp = vec > 0 ? tid / vec : 0;
+  const bool on = vec > 0 && grp < groups;
+  const int r = at / cols, x = at % cols;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto merge = [&](float2 ml, float4 y) {
+    const float mn = max_nan(m, ml.x), mu = finite_max(mn);
+    const float a = exp_from(m, mu), c = exp_from(ml.x, mu);
+    acc.x = acc.x * a + y.x * c; acc.y = acc.y * a + y.y * c; acc.z = acc.z * a + y.z * c; acc.w = acc.w * a + y.w * c;
+    l = l * a + ml.y * c;
+    m = mn;
+  };
+  if (on) {
+    const float* src = p.part_acc + (slot0 * rows + rt + r) * D + d0 + 4 * x;
+    const float2* ml = p.part_ml + slot0 * rows + rt + r;
+    for (int i0 = grp; i0 < parts; i0 += 4 * groups) {
+      float2 mm[4];
+      float4 yy[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = i0 + k * groups;
-          mm[k] = i < parts ? ml[(long long)i * rows] : make_float2(-INFINITY, 0.f);
-          yy[k] = i < parts ? *reinterpret_cast<const float4*>(src + (long long)i * rows * D) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * groups;
+        mm[k] = i < parts ? ml[(long long)i * rows] : make_float2(-INFINITY, 0.f);
+        yy[k] = i < parts ? *reinterpret_cast<const float4*>(src + (long long)i * rows * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) merge(mm[k], yy[k]);
-      }
+      for (int k = 0; k < 4; ++k) merge(mm[k], yy[k]);
     }
-    if (groups > 1) {
-      if (on && grp > 0) {
-        ja_s[grp * vec + at] = acc;
-        jm_s[grp * vec + at] = make_float2(m, l);
-      }
-      __syncthreads();
-      if (on && grp == 0)
-        for (int k = 1; k < groups; ++k) merge(jm_s[k * vec + at], ja_s[k * vec + at]);
+  }
+  if (groups > 1) {
+    if (on && grp > 0) {
+      ja_s[grp * vec + at] = acc;
+      jm_s[grp * vec + at] = make_float2(m, l);
     }
-    if (on && grp == 0) {
-      if (nt > 0) merge(make_float2(m_s[r], l_s[r]), *reinterpret_cast<const float4*>(o_s + r * D + d0 + 4 * x));
-      const float mu = finite_max(m), inv = l == 0.f ? 0.f : 1.f / l;
-      const QRow w = qa_row(r0 + r, p.G, n, qn);
-      const long long row = ((long long)b * p.T + w.t) * p.Hq + h * p.G + w.g;
-      T* dst = reinterpret_cast<T*>(p.out) + row * D + d0 + 4 * x;
-      if constexpr (ELT == 4) {
-        *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-      } else {
-        const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
-      }
-      if (x == 0 && blockIdx.y == 0) {
-        if (p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : mu + logf(l);
-        if (p.blk != nullptr) {
-          p.rowstat[(long long)vu * rows + r] = make_float2(mu, inv);
-          tw_s[r] = nt > 0 ? l_s[r] * exp_from(m_s[r], mu) * inv : 0.f;
-        }
+    __syncthreads();
+    if (on && grp == 0)
+      for (int k = 1; k < groups; ++k) merge(jm_s[k * vec + at], ja_s[k * vec + at]);
+  }
+  if (on && grp == 0) {
+    if (nt > 0) merge(make_float2(m_s[r], l_s[r]), *reinterpret_cast<const float4*>(o_s + r * D + d0 + 4 * x));
+    const float mu = finite_max(m), inv = l == 0.f ? 0.f : 1.f / l;
+    const QRow w = qa_row(r0 + r, p.G, n, qn);
+    const long long row = ((long long)b * p.T + w.t) * p.Hq + h * p.G + w.g;
+    T* dst = reinterpret_cast<T*>(p.out) + row * D + d0 + 4 * x;
+    if constexpr (ELT == 4) {
+      *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    } else {
+      const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+    }
+    if (x == 0 && blockIdx.z == 0) {
+      if (p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : mu + logf(l);
+      if (p.blk != nullptr) {
+        p.rowstat[(long long)vu * rows + rt + r] = make_float2(mu, inv);
+        p.tail_w[(long long)vu * rows + rt + r] = nt > 0 ? l_s[r] * exp_from(m_s[r], mu) * inv : 0.f;
       }
     }
   }
-  if (p.blk != nullptr && blockIdx.y == 0) {
-    for (int r = live + tid; r < rows; r += kQcThreads) p.rowstat[(long long)vu * rows + r] = make_float2(0.f, 0.f);
-    __syncthreads();
-    if (tid == 0) {  // the tail's weight, the rows in order
-      float w = 0.f;
-      for (int r = 0; r < live; ++r) w += tw_s[r];
-      p.tail_w[vu] = w;
-    }
+  if (p.blk != nullptr && blockIdx.z == 0 && tid >= live && tid < kQcRows) {  // rows that do not exist weigh nothing
+    p.rowstat[(long long)vu * rows + rt + tid] = make_float2(0.f, 0.f);
+    p.tail_w[(long long)vu * rows + rt + tid] = 0.f;
   }
 }
 
 // ---------------------------------------------------------------------------
 // Accumulated weights: mass = decay * mass + sum over the tiles and rows of
 // (block sum) * exp(block maximum - row maximum) / row sum, the lanes in a fixed
-// order. Entries without tokens only decay. A warp takes 32 / min(rows, 32) blocks at
-// once, four times.
+// order. Entries without tokens only decay. A warp takes 32 / rows blocks at once,
+// four times.
 // ---------------------------------------------------------------------------
 template <int ROWS>
 __host__ __device__ constexpr int weights_per_cta() {
-  return kQcThreads / 32 * (ROWS < 32 ? 32 / ROWS : 1) * 4;
+  return kQcThreads / 32 * (32 / ROWS) * 4;
 }
 
 template <int ROWS>
 __global__ void __launch_bounds__(kQcThreads) quant_weights_kernel(QStreamParams p) {
-  constexpr int RL = ROWS < 32 ? ROWS : 32, PW = 32 / RL, RPL = ROWS / RL;  // lanes of a block, blocks at once, rows of a lane
-  const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int PW = 32 / ROWS;  // blocks at once
+  const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane % ROWS;
   const int n = max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)), nb = n / kQB, nt = n % kQB;
-  const int first = blockIdx.y * weights_per_cta<ROWS>() + warp * PW * 4 + lane / RL, r0 = lane % RL;
+  const int first = blockIdx.y * weights_per_cta<ROWS>() + warp * PW * 4 + lane / ROWS;
   float* mass = p.mass + (long long)u * p.max_blocks;
   float old[4], w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int j = first + i * PW;
-    old[i] = r0 == 0 && j < p.max_blocks && p.decay != 0.f ? mass[j] * p.decay : 0.f;
+    old[i] = r == 0 && j < p.max_blocks && p.decay != 0.f ? mass[j] * p.decay : 0.f;
     w[i] = 0.f;
   }
   griddep_wait();
   for (int tile = 0; tile < p.tiles; ++tile) {
     const long long vu = (long long)u * p.tiles + tile;
+    const bool on = tile * ROWS + r < p.T * p.G;
+    const float2 st = on ? p.rowstat[vu * ROWS + r] : make_float2(0.f, 0.f);
+    float2 ml[4];
 #pragma unroll
-    for (int k = 0; k < RPL; ++k) {
-      const int r = r0 + k * RL;
-      const bool on = tile * ROWS + r < p.T * p.G;
-      const float2 st = on ? p.rowstat[vu * ROWS + r] : make_float2(0.f, 0.f);
-      float2 ml[4];
+    for (int i = 0; i < 4; ++i) {
+      const int j = first + i * PW;
+      ml[i] = on && j < nb ? p.blk[(vu * p.max_blocks + j) * ROWS + r] : make_float2(-INFINITY, 0.f);
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = first + i * PW;
-        ml[i] = on && j < nb ? p.blk[(vu * p.max_blocks + j) * ROWS + r] : make_float2(-INFINITY, 0.f);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = first + i * PW;
-        if (on && j < nb) w[i] += ml[i].y * exp_from(ml[i].x, st.x) * st.y;
-        if (j == nb && nt > 0 && r == 0) w[i] += p.tail_w[vu];
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int j = first + i * PW;
+      if (on && j < nb) w[i] += ml[i].y * exp_from(ml[i].x, st.x) * st.y;
+      if (j == nb && nt > 0) w[i] += p.tail_w[vu * ROWS + r];
     }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int j = first + i * PW;
 #pragma unroll
-    for (int s = 1; s < RL; s <<= 1) w[i] += __shfl_xor_sync(0xffffffffu, w[i], s);
-    if (r0 == 0 && j < p.max_blocks) mass[j] = old[i] + w[i];
+    for (int s = 1; s < ROWS; s <<= 1) w[i] += __shfl_xor_sync(0xffffffffu, w[i], s);
+    if (r == 0 && j < p.max_blocks) mass[j] = old[i] + w[i];
   }
 }
 
@@ -1007,24 +992,18 @@ cudaError_t stream_launches(const Shape& s, const QPlan& pl, const QStreamParams
   constexpr bool F32 = sizeof(T) == 4;
   cudaError_t e = pl.rows == 8    ? stream_variant<D, 1, 1, F32>(pl, p, stream)
                   : pl.rows == 16 ? stream_variant<D, 2, 1, F32>(pl, p, stream)
-                  : pl.rows == 32 ? stream_variant<D, 2, 2, F32>(pl, p, stream)
-                                  : stream_variant<D, 2, 4, F32>(pl, p, stream);
+                                  : stream_variant<D, 2, 2, F32>(pl, p, stream);
   if (e != cudaSuccess) return e;
   // few units have many parts each: more CTAs share the join
-  const int vu = s.U * pl.tiles, z = vu <= 16 ? 4 : vu <= 32 ? 2 : 1;
-  const size_t smem = combine_smem<D>(pl.rows);
-  static std::atomic<int> lim[64];
-  e = raise_smem_limit((const void*)quant_combine_kernel<T, D>, smem, lim);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(quant_combine_kernel<T, D>, dim3(vu, z), kQcThreads, smem, stream, p, pl.rows);
+  const int vu = s.U * pl.tiles, y = pl.rows / kQcRows, z = vu * y <= 16 ? 4 : vu * y <= 32 ? 2 : 1;
+  e = launch_dependent(quant_combine_kernel<T, D>, dim3(vu, y, z), kQcThreads, 0, stream, p, pl.rows);
   if (e != cudaSuccess || p.mass == nullptr) return e;
   auto weights = [&](auto kernel, int per) {
     return launch_dependent(kernel, dim3(s.U, (p.max_blocks + per - 1) / per), kQcThreads, 0, stream, p);
   };
   return pl.rows == 8    ? weights(quant_weights_kernel<8>, weights_per_cta<8>())
          : pl.rows == 16 ? weights(quant_weights_kernel<16>, weights_per_cta<16>())
-         : pl.rows == 32 ? weights(quant_weights_kernel<32>, weights_per_cta<32>())
-                         : weights(quant_weights_kernel<64>, weights_per_cta<64>());
+                         : weights(quant_weights_kernel<32>, weights_per_cta<32>());
 }
 #endif
 
