@@ -406,39 +406,55 @@ def nosa_sparse_attention_noalloc(cfg: NosaConfig, units, block_tab, tail, tail_
 # ---------------------------------------------------------------------------
 # the 8-bit block cache (state and layouts: include/nosa.h)
 # ---------------------------------------------------------------------------
-def _on(cfg: NosaConfig, t, shape, dtype, what, align=4, allow_none=False):
-    """_ptr for a tensor that must live on cfg's device."""
-    if t is not None and t.is_cuda and t.get_device() != cfg.device:
+# These calls are short enough for the binding to count, so each tensor is checked in one
+# expression and the reason for a refusal is looked for afterwards.
+def _arg(t, device, shape, dtype, what, align=4):
+    """Pointer of a contiguous tensor of this shape and type on cuda:device."""
+    if (t.get_device() == device and t.dtype is dtype and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
+        p = t.data_ptr()
+        if p % align == 0:
+            return p
+    if t.is_cuda and t.get_device() != device:
         raise ValueError(f"{what} is on cuda:{t.get_device()}, the configuration's device is "
-                         f"cuda:{cfg.device}")
-    return _ptr(t, shape, dtype, what, align, allow_none)
+                         f"cuda:{device}")
+    return _ptr(t, shape, dtype, what, align)
 
 
-def _rows(cfg: NosaConfig, t, shape, dtype, what):
+def _rows(t, device, shape, dtype, what):
     """Pointer and strides (None where contiguous) of [batch][n][heads][d] rows."""
-    if t is None or t.is_contiguous():
-        return _on(cfg, t, shape, dtype, what, 16), None
-    if tuple(t.shape) != shape:
+    if t.is_contiguous():
+        return _arg(t, device, shape, dtype, what, 16), None
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
     st = t.stride()
     if st[3] != 1:
         raise ValueError(f"{what}: the elements of a row must be consecutive")
-    row = t[0, 0, 0] if t.numel() else t.reshape(-1)
-    return _on(cfg, row, None, dtype, what, 16), (C.c_int64 * 3)(*st[:3])
+    # (a dimension of one element is never stepped along)
+    return (_arg(t[0, 0, 0], device, None, dtype, what, 16),
+            (C.c_int64 * 3)(*(s if n > 1 else 0 for s, n in zip(st[:3], shape))))
 
 
-def _units(cfg: NosaConfig, t):
-    """Pointer and number of the 8-bit units in t."""
-    size = nosa_quant_unit_bytes(cfg)
-    n, rest = divmod(t.numel(), size) if size else (0, 0)
+def _cache_args(cfg: NosaConfig, units, block_tab, tail, lens, torch):
+    """(units, number of units, block_tab, tail, lens) of a cache, checked."""
+    dev, d, U = cfg.device, cfg.head_dim, cfg.batch * cfg.n_kv_heads
+    elt = 4 if cfg.dtype == NOSA_F32 else 2
+    size = (2 * 64 * d + 4 * 64 + 8 + 31) // 32 * 32          # nosa_quant_unit_bytes
+    payload = (2 * 64 * d * elt + 4 * 64 + 255) // 256 * 256  # nosa_payload_bytes
+    n, rest = divmod(units.numel(), size)
     if rest:
         raise ValueError(f"units must hold whole units of {size} bytes")
-    return _on(cfg, t, None, _torch().uint8, "units", 16), n
+    if tail.numel() != U * payload:
+        raise ValueError("tail must hold one block unit per request and KV head")
+    return (_arg(units, dev, None, torch.uint8, "units", 16), n,
+            _arg(block_tab, dev, (U, block_tab.shape[1]), torch.int32, "block_tab"),
+            _arg(tail, dev, None, torch.uint8, "tail", 16),
+            _arg(lens, dev, (U,), torch.int32, "lens"))
 
 
-def _device_stream(cfg: NosaConfig, stream):
-    """The given stream, or the current one of cfg's device."""
-    return _stream(_torch().cuda.current_stream(cfg.device) if stream is None else stream)
+def _device_stream(device, stream, torch):
+    """The given stream, or the current one of the device."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def nosa_quant_unit_bytes(cfg: NosaConfig) -> int:
@@ -452,24 +468,19 @@ def nosa_quant_append(cfg: NosaConfig, k, v, e, units, block_tab, tail, lens, le
     The new lengths go to lens_out (lens itself by default); n_new [batch] int32 gives the
     valid tokens of each request."""
     torch = _torch()
-    U = cfg.batch * cfg.n_kv_heads
+    dev, batch = cfg.device, cfg.batch
     dt, i32 = _dtype_of(cfg), torch.int32
-    n, blocks = k.shape[1], block_tab.shape[1]
-    shp = (cfg.batch, n, cfg.n_kv_heads, cfg.head_dim)
-    kp, ks = _rows(cfg, k, shp, dt, "k")
-    vp, vs = _rows(cfg, v, shp, dt, "v")
-    up, nu = _units(cfg, units)
-    lp = _on(cfg, lens, (U,), i32, "lens")
-    if tail.numel() != U * nosa_payload_bytes(cfg):
-        raise ValueError("tail must hold one block unit per request and KV head")
+    shp = (batch, k.shape[1], cfg.n_kv_heads, cfg.head_dim)
+    kp, ks = _rows(k, dev, shp, dt, "k")
+    vp, vs = _rows(v, dev, shp, dt, "v")
+    up, nu, tab, tl, lp = _cache_args(cfg, units, block_tab, tail, lens, torch)
     _check(lib.nosa_quant_append(
-        C.byref(cfg), blocks, n, kp, ks, vp, vs,
-        _on(cfg, e, shp[:3], torch.float32, "e", allow_none=True),
-        _on(cfg, n_new, (cfg.batch,), i32, "n_new", allow_none=True), up, nu,
-        _on(cfg, block_tab, (U, blocks), i32, "block_tab"),
-        _on(cfg, tail, None, torch.uint8, "tail", 16), lp,
-        lp if lens_out is None else _on(cfg, lens_out, (U,), i32, "lens_out"),
-        _on(cfg, status, (1,), i32, "status", allow_none=True), _device_stream(cfg, stream)))
+        C.byref(cfg), block_tab.shape[1], shp[1], kp, ks, vp, vs,
+        None if e is None else _arg(e, dev, shp[:3], torch.float32, "e"),
+        None if n_new is None else _arg(n_new, dev, (batch,), i32, "n_new"), up, nu, tab, tl, lp,
+        lp if lens_out is None else _arg(lens_out, dev, lens.shape, i32, "lens_out"),
+        None if status is None else _arg(status, dev, (1,), i32, "status"),
+        _device_stream(dev, stream, torch)))
 
 
 def nosa_quant_attention_workspace_bytes(cfg: NosaConfig, max_blocks: int, n_queries: int = 1,
@@ -484,27 +495,24 @@ def nosa_quant_attention(cfg: NosaConfig, units, block_tab, tail, lens, q, out, 
     cache; writes out (and lse [batch][n][Hq]) and, given mass [U][max_blocks], accumulates the
     blocks' attention weight. Returns the workspace (allocated here when not passed)."""
     torch = _torch()
-    U = cfg.batch * cfg.n_kv_heads
+    dev = cfg.device
     dt, i32, f32 = _dtype_of(cfg), torch.int32, torch.float32
-    n, blocks = q.shape[1], block_tab.shape[1]
-    shp = (cfg.batch, n, cfg.n_q_heads, cfg.head_dim)
-    qp, qs = _rows(cfg, q, shp, dt, "q")
-    up, nu = _units(cfg, units)
-    if tail.numel() != U * nosa_payload_bytes(cfg):
-        raise ValueError("tail must hold one block unit per request and KV head")
+    shp = (cfg.batch, q.shape[1], cfg.n_q_heads, cfg.head_dim)
+    qp, qs = _rows(q, dev, shp, dt, "q")
+    up, nu, tab, tl, lp = _cache_args(cfg, units, block_tab, tail, lens, torch)
     if workspace is None:
         workspace = torch.empty(
-            nosa_quant_attention_workspace_bytes(cfg, blocks, n, mass is not None),
+            nosa_quant_attention_workspace_bytes(cfg, block_tab.shape[1], shp[1], mass is not None),
             dtype=torch.uint8, device=q.device)
     _check(lib.nosa_quant_attention(
-        C.byref(cfg), blocks, n, up, nu, _on(cfg, block_tab, (U, blocks), i32, "block_tab"),
-        _on(cfg, tail, None, torch.uint8, "tail", 16), _on(cfg, lens, (U,), i32, "lens"), qp, qs,
-        _on(cfg, q_len, (cfg.batch,), i32, "q_len", allow_none=True),
-        _on(cfg, out, shp, dt, "out", 16),
-        _on(cfg, lse, shp[:3], f32, "lse", allow_none=True),
-        _on(cfg, mass, (U, blocks), f32, "mass", allow_none=True), decay,
-        _on(cfg, workspace, None, torch.uint8, "workspace", 256), workspace.numel(),
-        _on(cfg, status, (1,), i32, "status", allow_none=True), _device_stream(cfg, stream)))
+        C.byref(cfg), block_tab.shape[1], shp[1], up, nu, tab, tl, lp, qp, qs,
+        None if q_len is None else _arg(q_len, dev, (cfg.batch,), i32, "q_len"),
+        _arg(out, dev, shp, dt, "out", 16),
+        None if lse is None else _arg(lse, dev, shp[:3], f32, "lse"),
+        None if mass is None else _arg(mass, dev, block_tab.shape, f32, "mass"), decay,
+        _arg(workspace, dev, None, torch.uint8, "workspace", 256), workspace.numel(),
+        None if status is None else _arg(status, dev, (1,), i32, "status"),
+        _device_stream(dev, stream, torch)))
     return workspace
 
 
@@ -513,15 +521,17 @@ def nosa_quant_evict(cfg: NosaConfig, budget, n_recent, block_tab, mass, lens, t
     """Evicts the blocks of least accumulated weight from every unit with more than `budget` full
     blocks (its newest n_recent stay). Works in place unless outputs are given."""
     torch = _torch()
-    U, blocks = cfg.batch * cfg.n_kv_heads, block_tab.shape[1]
+    dev = cfg.device
+    shp = (cfg.batch * cfg.n_kv_heads, block_tab.shape[1])
     i32, f32 = torch.int32, torch.float32
-    tp = _on(cfg, block_tab, (U, blocks), i32, "block_tab")
-    mp = _on(cfg, mass, (U, blocks), f32, "mass")
-    lp = _on(cfg, lens, (U,), i32, "lens")
+    tp = _arg(block_tab, dev, shp, i32, "block_tab")
+    mp = _arg(mass, dev, shp, f32, "mass")
+    lp = _arg(lens, dev, shp[:1], i32, "lens")
     _check(lib.nosa_quant_evict(
-        C.byref(cfg), blocks, int(budget), int(n_recent), tp, mp, lp,
-        tp if tab_out is None else _on(cfg, tab_out, (U, blocks), i32, "tab_out"),
-        mp if mass_out is None else _on(cfg, mass_out, (U, blocks), f32, "mass_out"),
-        lp if lens_out is None else _on(cfg, lens_out, (U,), i32, "lens_out"),
-        _on(cfg, order, (U, blocks), i32, "order", allow_none=True),
-        _on(cfg, status, (1,), i32, "status", allow_none=True), _device_stream(cfg, stream)))
+        C.byref(cfg), shp[1], budget, n_recent, tp, mp, lp,
+        tp if tab_out is None else _arg(tab_out, dev, shp, i32, "tab_out"),
+        mp if mass_out is None else _arg(mass_out, dev, shp, f32, "mass_out"),
+        lp if lens_out is None else _arg(lens_out, dev, shp[:1], i32, "lens_out"),
+        None if order is None else _arg(order, dev, shp, i32, "order"),
+        None if status is None else _arg(status, dev, (1,), i32, "status"),
+        _device_stream(dev, stream, torch)))

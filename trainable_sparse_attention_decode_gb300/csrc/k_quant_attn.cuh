@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
 #pragma unroll
       for (int x = 1; x < NB; ++x)
         if (x == k % NB) to = slot[x];
-#pragma unroll 1
+#pragma unroll 4
       for (int r = 0; r < ROWS; ++r) {
         const int w0 = r / WR * IS, rr = r % WR;  // the warps of this row, and their row
         float M = ml[w0 * WR + rr].x;

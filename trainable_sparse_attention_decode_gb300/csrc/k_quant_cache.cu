@@ -14,6 +14,11 @@ template <> struct Row8<__nv_bfloat16> {
   uint4 r;
   __device__ __forceinline__ void load(const void* p) { r = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  // largest magnitude as the bit pattern of an fp32 number
+  __device__ __forceinline__ uint32_t amax() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu), __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu));
+    return max(m & 0xFFFF0000u, m << 16);
+  }
   __device__ __forceinline__ void get(float* f) const {
     f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x); f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
     f[4] = bf16_lo(r.z); f[5] = bf16_hi(r.z); f[6] = bf16_lo(r.w); f[7] = bf16_hi(r.w);
@@ -26,6 +31,14 @@ template <> struct Row8<float> {
     b = reinterpret_cast<const float4*>(p)[1];
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ uint32_t amax() const {
+    float f[8];
+    get(f);
+    uint32_t m = 0;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) m = max(m, __float_as_uint(f[x]) & 0x7FFFFFFFu);
+    return m;
+  }
   __device__ __forceinline__ void get(float* f) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
@@ -40,6 +53,19 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
+// A unit on its way through shared memory: runs of 512 bytes (32 lanes x 16) padded to
+// 544, so that the words that a warp's patches write together, which lie 512 bytes
+// apart in the unit, fall into different banks.
+template <int D>
+struct UnitImage {
+  static constexpr int RUNS = 2 * kQB * D / 512, PITCH = 544;
+  __align__(16) uint8_t code[RUNS * PITCH];
+  __align__(16) float rest[kQB + 8];  // logits, scales, zeros
+  uint32_t amax[2];
+  static_assert(quant_unit_bytes(D) - quant_e_off(D) == (kQB + 8) * 4, "what follows the codes");
+  __device__ __forceinline__ uint8_t* at(int off) { return code + off / 512 * PITCH + off % 512; }
+};
+
 // Quantises block j of the unit's new blocks (0: the one that the tail began) and
 // stores it: x -> e4m3(x * (448 / max |x|)), the maximum over the block's tokens
 // whose logit is not -inf; the others become zeros. A thread owns patches of 4
@@ -48,15 +74,14 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // is read once; the image is put together in shared memory and leaves in 16-byte
 // stores.
 template <typename T, int D>
-__device__ void quant_block(const QAppendArgs& p, int Hkv, int u, int j, int n0, const uint8_t* tail,
-                            uint8_t* img, uint32_t* red) {
+__device__ void quant_block(const QAppendArgs& p, int Hkv, int u, int j, int n0, const uint8_t* tail, UnitImage<D>& img) {
   constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NT = kAppendThreads;
   constexpr int NP = 16 * (D / 8);  // patches of K (and of V)
   constexpr int PPT = 2 * NP / NT;  // patches per thread: 2 (d = 128) or 1
   static_assert(PPT * NT == 2 * NP, "patches must divide over the threads");
   const int tid = threadIdx.x, b = u / Hkv, h = u % Hkv;
   const int old = n0 % kQB, blk = n0 / kQB + j;
-  float* e_s = reinterpret_cast<float*>(img + quant_e_off(D));
+  const int idx = p.tab[(long long)u * p.max_blocks + blk];
 
   Row8<T> row[PPT][4];
 #pragma unroll
@@ -88,9 +113,9 @@ __device__ void quant_block(const QAppendArgs& p, int Hkv, int u, int j, int n0,
       ev = reinterpret_cast<const float*>(tail + 2 * (size_t)kQB * D * ELT)[tid];
     else if (p.e != nullptr)
       ev = p.e[((long long)b * p.n + (pos - old)) * Hkv + h];
-    e_s[tid] = ev;
+    img.rest[tid] = ev;
   }
-  if (tid < 2) red[tid] = 0;
+  if (tid < 2) img.amax[tid] = 0;
   __syncthreads();
 
   // Maximum of the magnitudes' bit patterns: a NaN or an infinity comes out on top.
@@ -100,22 +125,19 @@ __device__ void quant_block(const QAppendArgs& p, int Hkv, int u, int j, int n0,
     uint32_t mx = 0;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      if (e_s[4 * tg + r] == -INFINITY) row[i][r].zero();
-      float f[8];
-      row[i][r].get(f);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) mx = max(mx, __float_as_uint(f[x]) & 0x7FFFFFFFu);
+      if (img.rest[4 * tg + r] == -INFINITY) row[i][r].zero();
+      mx = max(mx, row[i][r].amax());
     }
     mx = __reduce_max_sync(0xffffffffu, mx);
-    if ((tid & 31) == 0) atomicMax(red + isv, mx);
+    if ((tid & 31) == 0) atomicMax(img.amax + isv, mx);
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < PPT; ++i) {
     const int id = tid + i * NT, isv = id / NP, pt = id % NP, c8 = pt % (D / 8), tg = pt / (D / 8);
-    const float amax = __uint_as_float(red[isv]);
-    const bool finite = red[isv] < 0x7F800000u;
-    const float inv = (finite && amax >= 0x1p-100f) ? 448.f / amax : 0.f;
+    const uint32_t bits = img.amax[isv];
+    const float amax = __uint_as_float(bits);
+    const float inv = (bits < 0x7F800000u && amax >= 0x1p-100f) ? 448.f / amax : 0.f;
     float f[4][8];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -126,32 +148,34 @@ __device__ void quant_block(const QAppendArgs& p, int Hkv, int u, int j, int n0,
     if (isv) {  // one word: the patch's four tokens of one dim
 #pragma unroll
       for (int x = 0; x < 8; ++x)
-        *reinterpret_cast<uint32_t*>(img + quant_v_off(4 * tg, c8 * 8 + x, D)) =
+        *reinterpret_cast<uint32_t*>(img.at(quant_v_off(4 * tg, c8 * 8 + x, D))) =
             e4m3x4(f[0][x], f[1][x], f[2][x], f[3][x]);
-    } else {  // one word: four dims of one token
+    } else {  // two words: four dims of tokens r and r + 2
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int x = 0; x < 8; x += 4)
-          *reinterpret_cast<uint32_t*>(img + quant_k_off(4 * tg + r, c8 * 8 + x, D)) =
-              e4m3x4(f[r][x], f[r][x + 1], f[r][x + 2], f[r][x + 3]);
+          *reinterpret_cast<uint2*>(img.at(quant_k_off(4 * tg + r, c8 * 8 + x, D))) =
+              make_uint2(e4m3x4(f[r][x], f[r][x + 1], f[r][x + 2], f[r][x + 3]),
+                         e4m3x4(f[r + 2][x], f[r + 2][x + 1], f[r + 2][x + 2], f[r + 2][x + 3]));
     }
   }
-  if (tid < 2) {
-    const float amax = __uint_as_float(red[tid]);
-    const float sc = red[tid] >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : amax >= 0x1p-100f ? amax / 448.f : 0.f;
-    reinterpret_cast<float*>(img + quant_scale_off(D))[tid] = sc;
+  if (tid < 8) {
+    const uint32_t bits = tid < 2 ? img.amax[tid] : 0u;
+    const float amax = __uint_as_float(bits);
+    img.rest[kQB + tid] = bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : amax >= 0x1p-100f ? amax / 448.f : 0.f;
   }
-  constexpr int kUsed = quant_scale_off(D) + 8;
-  for (int o = kUsed + tid * 4; o < quant_unit_bytes(D); o += NT * 4) *reinterpret_cast<uint32_t*>(img + o) = 0;
   __syncthreads();
-  const int idx = p.tab[(long long)u * p.max_blocks + blk];
   if (idx < 0 || (long long)idx >= p.n_units) {
     if (tid == 0) quant_flag(p.status, kQErrIndex);
     return;
   }
-  uint4* dst = reinterpret_cast<uint4*>(p.units + (long long)idx * quant_unit_bytes(D));
-  for (int o = tid; o < quant_unit_bytes(D) / 16; o += NT) dst[o] = reinterpret_cast<const uint4*>(img)[o];
+  uint8_t* dst = p.units + (long long)idx * quant_unit_bytes(D);
+#pragma unroll
+  for (int o = tid * 16; o < quant_e_off(D); o += NT * 16)
+    *reinterpret_cast<uint4*>(dst + o) = *reinterpret_cast<const uint4*>(img.at(o));
+  if (tid < (kQB + 8) / 4)
+    reinterpret_cast<uint4*>(dst + quant_e_off(D))[tid] = reinterpret_cast<const uint4*>(img.rest)[tid];
 }
 
 // What the call does to unit u: tokens before it, new ones (0 where the unit is left as it was).
@@ -174,28 +198,27 @@ __device__ __forceinline__ UnitAppend unit_append(const QAppendArgs& p, int Hkv,
 // Blocks that the call completes: grid (units, most blocks), so that neighbouring
 // CTAs read the heads of the same tokens.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads) quant_blocks_kernel(QAppendArgs p, int Hkv, long long payload) {
-  __shared__ __align__(16) uint8_t img[quant_unit_bytes(D)];
-  __shared__ uint32_t red[2];
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 || D == 64 ? 4 : 2)
+quant_blocks_kernel(QAppendArgs p, int Hkv, long long payload) {
+  __shared__ UnitImage<D> img;
   const int u = blockIdx.x, j = blockIdx.y;
   const UnitAppend a = unit_append(p, Hkv, u, false);
   if (j >= (a.n0 % kQB + a.add) / kQB) return;
-  quant_block<T, D>(p, Hkv, u, j, a.n0, p.tail + u * payload, img, red);
+  quant_block<T, D>(p, Hkv, u, j, a.n0, p.tail + u * payload, img);
 }
 
 // The unit's tail and length; with BLOCK also the one block that at most 64 new
 // tokens can complete (single tokens: one launch).
 template <typename T, int D, bool BLOCK>
 __global__ void __launch_bounds__(kAppendThreads) quant_tail_kernel(QAppendArgs p, int Hkv, long long payload) {
-  __shared__ __align__(16) uint8_t img[BLOCK ? quant_unit_bytes(D) : 16];
-  __shared__ uint32_t red[2];
   constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE;
   const int u = blockIdx.x, b = u / Hkv, h = u % Hkv, tid = threadIdx.x;
   const UnitAppend a = unit_append(p, Hkv, u, tid == 0);
   uint8_t* tail = p.tail + u * payload;
   const int old = a.n0 % kQB, done = (old + a.add) / kQB;
-  if (BLOCK && done > 0) {
-    quant_block<T, D>(p, Hkv, u, 0, a.n0, tail, img, red);
+  if constexpr (BLOCK) {
+    __shared__ UnitImage<D> img;
+    if (done > 0) quant_block<T, D>(p, Hkv, u, 0, a.n0, tail, img);
   }
   __syncthreads();  // the old tail and length have been read
   const int first = done > 0 ? 0 : old, left = old + a.add - done * kQB;
