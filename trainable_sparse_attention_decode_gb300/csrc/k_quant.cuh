@@ -91,6 +91,7 @@ struct QAttnArgs {
   int* status;
 };
 
+int quant_sm_count();  // of the current device
 cudaError_t launch_quant_append(const Shape& s, const QAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_quant_evict(const Shape& s, const QEvictArgs& a, cudaStream_t stream);
 size_t quant_attn_workspace(const Shape& s, int max_blocks, int T, bool mass);
@@ -114,6 +115,23 @@ __device__ __forceinline__ int quant_count(const int32_t* count, int b, int n, i
   if (c >= 0 && c <= n) return c;
   if (flag) quant_flag(status, kQErrIndex);
   return c < 0 ? 0 : n;
+}
+
+// Launches `kernel` so that it may begin while the one before it in the stream runs
+// (it waits with griddepcontrol.wait before it reads that kernel's results).
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 #endif
 

@@ -2,9 +2,8 @@
 #include "k_quant_attn.cuh"
 
 namespace nosa {
-namespace {
 
-int sm_count() {
+int quant_sm_count() {
   static std::atomic<int> cache[64];
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
@@ -13,6 +12,8 @@ int sm_count() {
   if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
+
+namespace {
 
 struct Layout {
   size_t base, part_ml, part_acc, rowstat, tail_w, blk, total;
@@ -45,7 +46,7 @@ QPlan quant_attn_plan(const Shape& s, int T) {
   const int rows = T * s.G;
   pl.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   pl.tiles = (rows + pl.rows - 1) / pl.rows;
-  pl.ctas = sm_count();
+  pl.ctas = quant_sm_count();
   return pl;
 }
 

@@ -960,23 +960,6 @@ cudaError_t launch_quant_stream_bf16(const Shape& s, const QPlan& pl, const QStr
 cudaError_t launch_quant_stream_f32(const Shape& s, const QPlan& pl, const QStreamParams& p, cudaStream_t stream);
 
 #ifdef __CUDACC__
-// Launches `kernel` so that it may begin while the one before it in the stream runs
-// (it waits with griddepcontrol.wait before it reads that kernel's results).
-template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int D, int NT, int RG, bool F32>
 cudaError_t stream_variant(const QPlan& pl, const QStreamParams& p, cudaStream_t stream) {
   using Gm = QGeom<D, NT, RG, F32>;

@@ -66,32 +66,53 @@ struct UnitImage {
   __device__ __forceinline__ uint8_t* at(int off) { return code + off / 512 * PITCH + off % 512; }
 };
 
-// Quantises block j of the unit's new blocks (0: the one that the tail began) and
-// stores it: x -> e4m3(x * (448 / max |x|)), the maximum over the block's tokens
-// whose logit is not -inf; the others become zeros. A thread owns patches of 4
-// tokens x 8 dims, the smallest piece whose key and value words are whole, so the
-// block stays in registers between the maximum and the conversion and the input
-// is read once; the image is put together in shared memory and leaves in 16-byte
-// stores.
+// Quantises blocks of a unit's tokens: x -> e4m3(x * (448 / max |x|)), the maximum
+// over the block's tokens whose logit is not -inf; the others become zeros. A thread
+// owns patches of 4 tokens x 8 dims, the smallest piece whose key and value words are
+// whole, so a block stays in registers between the maximum and the conversion and the
+// input is read once; the image is put together in shared memory and leaves in 16-byte
+// stores. (One wave of CTAs that load the next block while they store one was slower than
+// a CTA per block: 50 us against 43 for 4 x 8192 tokens of 8 heads of 128 in bf16.)
 template <typename T, int D>
-__device__ void quant_block(const QAppendArgs& p, int Hkv, int u, int j, int n0, const uint8_t* tail, UnitImage<D>& img) {
-  constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NT = kAppendThreads;
-  constexpr int NP = 16 * (D / 8);  // patches of K (and of V)
-  constexpr int PPT = 2 * NP / NT;  // patches per thread: 2 (d = 128) or 1
+struct BlockQuant {
+  static constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NT = kAppendThreads;
+  static constexpr int NP = 16 * (D / 8);  // patches of K (and of V)
+  static constexpr int PPT = 2 * NP / NT;  // patches per thread: 2 (d = 128) or 1
   static_assert(PPT * NT == 2 * NP, "patches must divide over the threads");
-  const int tid = threadIdx.x, b = u / Hkv, h = u % Hkv;
-  const int old = n0 % kQB, blk = n0 / kQB + j;
-  const int idx = p.tab[(long long)u * p.max_blocks + blk];
-
+  const QAppendArgs& p;
+  const uint8_t* tail;
+  int Hkv, u, b, h, n0, old, tid;
   Row8<T> row[PPT][4];
+  float ev;
+  int idx;
+
+  __device__ __forceinline__ BlockQuant(const QAppendArgs& p_, int Hkv_, int u_, int n0_, const uint8_t* tail_)
+      : p(p_), tail(tail_), Hkv(Hkv_), u(u_), b(u_ / Hkv_), h(u_ % Hkv_), n0(n0_), old(n0_ % kQB), tid(threadIdx.x) {}
+
+  // Patch i of this thread: keys (isv 0) or values, 16-byte column pair c8, tokens 4 tg ...
+  __device__ __forceinline__ void patch(int i, int& isv, int& c8, int& tg) const {
+    const int id = tid + i * NT;
+    isv = id / NP;
+    c8 = id % NP % (D / 8);
+    tg = id % NP / (D / 8);
+  }
+
+  // Starts the loads of block j of the new blocks (0: the one that the tail began).
+  __device__ __forceinline__ void load(int j) {
+    idx = p.tab[(long long)u * p.max_blocks + n0 / kQB + j];
+    const int first = j * kQB - old;  // the block's first token among the new ones, or before them
 #pragma unroll
-  for (int i = 0; i < PPT; ++i) {
-    const int id = tid + i * NT, isv = id / NP, pt = id % NP, c8 = pt % (D / 8), tg = pt / (D / 8);
+    for (int i = 0; i < PPT; ++i) {
+      int isv, c8, tg;
+      patch(i, isv, c8, tg);
+      const QStrides& st = isv ? p.vs : p.ks;
+      const T* src = reinterpret_cast<const T*>(isv ? p.v : p.k) + b * st.b + h * st.h + (first + 4 * tg) * st.t + c8 * 8;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 4 * tg + r, pos = j * kQB + t;
-      if (pos < old) {  // from the tail: keys in 16-byte chunks, values in rows
-        if (isv) {
+      for (int r = 0; r < 4; ++r, src += st.t) {
+        const int t = 4 * tg + r;
+        if (first >= 0 || first + t >= 0) {
+          row[i][r].load(src);
+        } else if (isv) {  // from the tail: values in rows, keys in 16-byte chunks
           row[i][r].load(tail + ((size_t)kQB * D + (size_t)t * D + c8 * 8) * ELT);
         } else if constexpr (CE == 8) {
           row[i][r].load(tail + ((size_t)c8 * kQB + t) * 16);
@@ -100,83 +121,95 @@ __device__ void quant_block(const QAppendArgs& p, int Hkv, int u, int j, int n0,
           f.a = *reinterpret_cast<const float4*>(tail + ((size_t)(2 * c8) * kQB + t) * 16);
           f.b = *reinterpret_cast<const float4*>(tail + ((size_t)(2 * c8 + 1) * kQB + t) * 16);
         }
-      } else {
-        const QStrides& st = isv ? p.vs : p.ks;
-        row[i][r].load(reinterpret_cast<const T*>(isv ? p.v : p.k) + b * st.b + (pos - old) * st.t + h * st.h + c8 * 8);
       }
     }
+    ev = 0.f;
+    if (tid < kQB) {
+      if (first + tid < 0)
+        ev = reinterpret_cast<const float*>(tail + 2 * (size_t)kQB * D * ELT)[tid];
+      else if (p.e != nullptr)
+        ev = p.e[((long long)b * p.n + first + tid) * Hkv + h];
+    }
   }
-  if (tid < kQB) {
-    const int pos = j * kQB + tid;
-    float ev = 0.f;
-    if (pos < old)
-      ev = reinterpret_cast<const float*>(tail + 2 * (size_t)kQB * D * ELT)[tid];
-    else if (p.e != nullptr)
-      ev = p.e[((long long)b * p.n + (pos - old)) * Hkv + h];
-    img.rest[tid] = ev;
-  }
-  if (tid < 2) img.amax[tid] = 0;
-  __syncthreads();
 
-  // Maximum of the magnitudes' bit patterns: a NaN or an infinity comes out on top.
+  // The loaded block into shared memory (whole CTA).
+  __device__ __forceinline__ void encode(UnitImage<D>& img) {
+    if (tid < kQB) img.rest[tid] = ev;
+    if (tid < 2) img.amax[tid] = 0;
+    __syncthreads();
+    // Maximum of the magnitudes' bit patterns: a NaN or an infinity comes out on top.
 #pragma unroll
-  for (int i = 0; i < PPT; ++i) {
-    const int id = tid + i * NT, isv = id / NP, tg = id % NP / (D / 8);
-    uint32_t mx = 0;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (img.rest[4 * tg + r] == -INFINITY) row[i][r].zero();
-      mx = max(mx, row[i][r].amax());
+    for (int i = 0; i < PPT; ++i) {
+      int isv, c8, tg;
+      patch(i, isv, c8, tg);
+      const float4 e = reinterpret_cast<const float4*>(img.rest)[tg];
+      if (e.x == -INFINITY) row[i][0].zero();
+      if (e.y == -INFINITY) row[i][1].zero();
+      if (e.z == -INFINITY) row[i][2].zero();
+      if (e.w == -INFINITY) row[i][3].zero();
+      uint32_t mx = max(max(row[i][0].amax(), row[i][1].amax()), max(row[i][2].amax(), row[i][3].amax()));
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      if ((tid & 31) == 0) atomicMax(img.amax + isv, mx);
     }
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if ((tid & 31) == 0) atomicMax(img.amax + isv, mx);
-  }
-  __syncthreads();
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < PPT; ++i) {
-    const int id = tid + i * NT, isv = id / NP, pt = id % NP, c8 = pt % (D / 8), tg = pt / (D / 8);
-    const uint32_t bits = img.amax[isv];
-    const float amax = __uint_as_float(bits);
-    const float inv = (bits < 0x7F800000u && amax >= 0x1p-100f) ? 448.f / amax : 0.f;
-    float f[4][8];
+    for (int i = 0; i < PPT; ++i) {
+      int isv, c8, tg;
+      patch(i, isv, c8, tg);
+      const uint32_t bits = img.amax[isv];
+      const float amax = __uint_as_float(bits);
+      const float inv = amax >= 0x1p-100f ? 448.f / amax : 0.f;
+      if (bits >= 0x7F800000u) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      row[i][r].get(f[r]);
+        for (int r = 0; r < 4; ++r) row[i][r].zero();
+      }
+      float2 f[4][4];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) f[r][x] = inv > 0.f ? f[r][x] * inv : 0.f;
+      for (int r = 0; r < 4; ++r) {
+        row[i][r].get(reinterpret_cast<float*>(f[r]));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) f[r][x] = __fmul2_rn(f[r][x], make_float2(inv, inv));
+      }
+      if (isv) {  // one word: the patch's four tokens of one dim
+        uint8_t* to = img.at(quant_v_off(4 * tg, c8 * 8, D));  // dims of a column pair are 64 bytes apart
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          *reinterpret_cast<uint32_t*>(to + 128 * x) = e4m3x4(f[0][x].x, f[1][x].x, f[2][x].x, f[3][x].x);
+          *reinterpret_cast<uint32_t*>(to + 128 * x + 64) = e4m3x4(f[0][x].y, f[1][x].y, f[2][x].y, f[3][x].y);
+        }
+      } else {  // two words: four dims of tokens r and r + 2
+        uint8_t* to = img.at(quant_k_off(4 * tg, c8 * 8, D));  // next token 64 bytes on, next four dims 16
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int x = 0; x < 4; x += 2)
+            *reinterpret_cast<uint2*>(to + 64 * r + 8 * x) =
+                make_uint2(e4m3x4(f[r][x].x, f[r][x].y, f[r][x + 1].x, f[r][x + 1].y),
+                           e4m3x4(f[r + 2][x].x, f[r + 2][x].y, f[r + 2][x + 1].x, f[r + 2][x + 1].y));
+      }
     }
-    if (isv) {  // one word: the patch's four tokens of one dim
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        *reinterpret_cast<uint32_t*>(img.at(quant_v_off(4 * tg, c8 * 8 + x, D))) =
-            e4m3x4(f[0][x], f[1][x], f[2][x], f[3][x]);
-    } else {  // two words: four dims of tokens r and r + 2
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int x = 0; x < 8; x += 4)
-          *reinterpret_cast<uint2*>(img.at(quant_k_off(4 * tg + r, c8 * 8 + x, D))) =
-              make_uint2(e4m3x4(f[r][x], f[r][x + 1], f[r][x + 2], f[r][x + 3]),
-                         e4m3x4(f[r + 2][x], f[r + 2][x + 1], f[r + 2][x + 2], f[r + 2][x + 3]));
+    if (tid < 8) {
+      const uint32_t bits = tid < 2 ? img.amax[tid] : 0u;
+      const float amax = __uint_as_float(bits);
+      img.rest[kQB + tid] = bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : amax >= 0x1p-100f ? amax / 448.f : 0.f;
     }
+    __syncthreads();
   }
-  if (tid < 8) {
-    const uint32_t bits = tid < 2 ? img.amax[tid] : 0u;
-    const float amax = __uint_as_float(bits);
-    img.rest[kQB + tid] = bits >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : amax >= 0x1p-100f ? amax / 448.f : 0.f;
-  }
-  __syncthreads();
-  if (idx < 0 || (long long)idx >= p.n_units) {
-    if (tid == 0) quant_flag(p.status, kQErrIndex);
-    return;
-  }
-  uint8_t* dst = p.units + (long long)idx * quant_unit_bytes(D);
+
+  // The image to unit `to` of the cache.
+  __device__ __forceinline__ void store(UnitImage<D>& img, int to) const {
+    if (to < 0 || (long long)to >= p.n_units) {
+      if (tid == 0) quant_flag(p.status, kQErrIndex);
+      return;
+    }
+    uint8_t* dst = p.units + (long long)to * quant_unit_bytes(D);
 #pragma unroll
-  for (int o = tid * 16; o < quant_e_off(D); o += NT * 16)
-    *reinterpret_cast<uint4*>(dst + o) = *reinterpret_cast<const uint4*>(img.at(o));
-  if (tid < (kQB + 8) / 4)
-    reinterpret_cast<uint4*>(dst + quant_e_off(D))[tid] = reinterpret_cast<const uint4*>(img.rest)[tid];
-}
+    for (int o = tid * 16; o < quant_e_off(D); o += NT * 16)
+      *reinterpret_cast<uint4*>(dst + o) = *reinterpret_cast<const uint4*>(img.at(o));
+    if (tid < (kQB + 8) / 4)
+      reinterpret_cast<uint4*>(dst + quant_e_off(D))[tid] = reinterpret_cast<const uint4*>(img.rest)[tid];
+  }
+};
 
 // What the call does to unit u: tokens before it, new ones (0 where the unit is left as it was).
 struct UnitAppend {
@@ -201,10 +234,14 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 || D == 64 ? 4 : 2)
 quant_blocks_kernel(QAppendArgs p, int Hkv, long long payload) {
   __shared__ UnitImage<D> img;
+  griddep_launch_dependents();
   const int u = blockIdx.x, j = blockIdx.y;
   const UnitAppend a = unit_append(p, Hkv, u, false);
   if (j >= (a.n0 % kQB + a.add) / kQB) return;
-  quant_block<T, D>(p, Hkv, u, j, a.n0, p.tail + u * payload, img);
+  BlockQuant<T, D> q(p, Hkv, u, a.n0, p.tail + u * payload);
+  q.load(j);
+  q.encode(img);
+  q.store(img, q.idx);
 }
 
 // The unit's tail and length; with BLOCK also the one block that at most 64 new
@@ -218,9 +255,15 @@ __global__ void __launch_bounds__(kAppendThreads) quant_tail_kernel(QAppendArgs 
   const int old = a.n0 % kQB, done = (old + a.add) / kQB;
   if constexpr (BLOCK) {
     __shared__ UnitImage<D> img;
-    if (done > 0) quant_block<T, D>(p, Hkv, u, 0, a.n0, tail, img);
+    if (done > 0) {
+      BlockQuant<T, D> q(p, Hkv, u, a.n0, tail);
+      q.load(0);
+      q.encode(img);
+      q.store(img, q.idx);
+    }
   }
-  __syncthreads();  // the old tail and length have been read
+  griddep_wait();   // ... by the blocks' launch
+  __syncthreads();  // and here: the old tail and length have been read
   const int first = done > 0 ? 0 : old, left = old + a.add - done * kQB;
   for (int i = tid; i < (left - first) * NCH; i += kAppendThreads) {
     const int r = first + i / NCH, c = i % NCH;
@@ -244,7 +287,9 @@ cudaError_t append_variant(const Shape& s, const QAppendArgs& a, cudaStream_t st
   } else {
     const int most = std::min((a.n + kQB - 1) / kQB, a.max_blocks);
     quant_blocks_kernel<T, D><<<dim3(s.U, most), kAppendThreads, 0, stream>>>(a, s.Hkv, s.payload);
-    quant_tail_kernel<T, D, false><<<s.U, kAppendThreads, 0, stream>>>(a, s.Hkv, s.payload);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_dependent(quant_tail_kernel<T, D, false>, dim3(s.U), kAppendThreads, 0, stream, a, s.Hkv, s.payload);
   }
   return cudaGetLastError();
 }
