@@ -117,8 +117,12 @@ __device__ __forceinline__ int quant_count(const int32_t* count, int b, int n, i
   return c < 0 ? 0 : n;
 }
 
-// Launches `kernel` so that it may begin while the one before it in the stream runs
-// (it waits with griddepcontrol.wait before it reads that kernel's results).
+// Launches `kernel` so that it may become resident while the one before it in the
+// stream still runs. Every kernel of the cache is launched so, and each of its CTAs
+// calls griddep_wait before it ends: where a kernel has ended, all before it have.
+// The first kernel of a call waits before it reads anything and only then lets its
+// successor start (griddep_launch_dependents), so that a successor inside the call may
+// read, before its own wait, what was there before the call.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg{};

@@ -39,8 +39,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <map>
-#include <mutex>
+#include <type_traits>
 
 namespace nosa {
 
@@ -160,7 +159,7 @@ struct QGeom {
   static constexpr int W = IS * RG;             // consumer warps; a producer and a helper come on top
   static constexpr int THREADS = 32 * (W + 2);
   static constexpr int STAGES = D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 8 : RG == 1 ? 6 : 9;
-  static constexpr int SL = NT == 1 ? 4 : 2;    // slices of a block that a warp takes at once
+  static constexpr int SL = NT == 2 && F32 && D == 128 ? 2 : 4;  // slices of a block that a warp takes at once
   static constexpr int NB = NT == 1 ? 2 : 1;    // buffers for queries and for parts
   static constexpr int RP = D + 4;              // padded row of a part
   static constexpr int Q_BYTES = NT * RG * KS * 32 * (F32 ? 16 : 8);
@@ -214,51 +213,62 @@ struct QWalk {
   __device__ __forceinline__ long long vu() const { return (long long)u * p.tiles + tile; }
 };
 
-// Queries of one row group of 8 (whole warp) as B operands, and the rows' factors.
-template <int D, bool F32>
+// Queries of GROUPS x 8 rows (whole warp) as B operands, and the rows' factors; all
+// loads come first, so that they cost one round trip.
+template <int D, int GROUPS, bool F32>
 __device__ __forceinline__ void qa_queries(const QStreamParams& p, int u, int row0, int n, int qn, uint8_t* q_s, float* rs_s,
                                            int* vis_s, int lane) {
   constexpr int KS = D / 16;
+  using Raw = typename std::conditional<F32, uint4, uint2>::type;  // four elements
   const int g = lane >> 2, c = lane & 3, b = u / p.Hkv, h = u % p.Hkv;
-  const QRow w = qa_row(row0 + g, p.G, n, qn);
-  float f[KS][4];
-  float mx = 0.f;
-  const long long src = b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + 4 * c;
+  Raw raw[GROUPS][KS];
 #pragma unroll
-  for (int k = 0; k < KS; ++k) {
-    f[k][0] = f[k][1] = f[k][2] = f[k][3] = 0.f;
-    if (w.t < qn) {
+  for (int i = 0; i < GROUPS; ++i) {
+    const QRow w = qa_row(row0 + 8 * i + g, p.G, n, qn);
+    const long long src = b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + 4 * c;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      raw[i][k] = Raw{};
+      if (w.t < qn) raw[i][k] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.q) + (src + 16 * k) * (F32 ? 4 : 2)));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < GROUPS; ++i) {
+    float f[KS][4];
+    float mx = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const Raw x = raw[i][k];
       if constexpr (F32) {
-        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + src + 16 * k);
-        f[k][0] = x.x; f[k][1] = x.y; f[k][2] = x.z; f[k][3] = x.w;
+        f[k][0] = __uint_as_float(x.x); f[k][1] = __uint_as_float(x.y);
+        f[k][2] = __uint_as_float(x.z); f[k][3] = __uint_as_float(x.w);
       } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(p.q) + src + 16 * k);
         f[k][0] = bf16_lo(x.x); f[k][1] = bf16_hi(x.x); f[k][2] = bf16_lo(x.y); f[k][3] = bf16_hi(x.y);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(f[k][i]));
-  }
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-  // 2^ex <= mx < 2^(ex + 1), kept where both 2^ex and 2^-ex are normal numbers
-  const int ex = min(max((int)(__float_as_uint(mx) >> 23), 1), 253) - 127;
-  const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
-#pragma unroll
-  for (int k = 0; k < KS; ++k) {
-    const float x0 = f[k][0] * down, x1 = f[k][1] * down, x2 = f[k][2] * down, x3 = f[k][3] * down;
-    const uint32_t h0 = f16x2(x0, x1), h1 = f16x2(x2, x3);
-    if constexpr (F32) {
-      const float2 y0 = f32x2(h0), y1 = f32x2(h1);
-      reinterpret_cast<uint4*>(q_s)[k * 32 + lane] =
-          make_uint4(h0, h1, f16x2(x0 - y0.x, x1 - y0.y), f16x2(x2 - y1.x, x3 - y1.y));
-    } else {
-      reinterpret_cast<uint2*>(q_s)[k * 32 + lane] = make_uint2(h0, h1);
+      for (int y = 0; y < 4; ++y) mx = fmaxf(mx, fabsf(f[k][y]));
     }
-  }
-  if (c == 0) {
-    rs_s[g] = up * kQScale<D>;
-    vis_s[g] = w.sees;
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // 2^ex <= mx < 2^(ex + 1), kept where both 2^ex and 2^-ex are normal numbers
+    const int ex = min(max((int)(__float_as_uint(mx) >> 23), 1), 253) - 127;
+    const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const float x0 = f[k][0] * down, x1 = f[k][1] * down, x2 = f[k][2] * down, x3 = f[k][3] * down;
+      const uint32_t h0 = f16x2(x0, x1), h1 = f16x2(x2, x3);
+      if constexpr (F32) {
+        const float2 y0 = f32x2(h0), y1 = f32x2(h1);
+        reinterpret_cast<uint4*>(q_s)[(i * KS + k) * 32 + lane] =
+            make_uint4(h0, h1, f16x2(x0 - y0.x, x1 - y0.y), f16x2(x2 - y1.x, x3 - y1.y));
+      } else {
+        reinterpret_cast<uint2*>(q_s)[(i * KS + k) * 32 + lane] = make_uint2(h0, h1);
+      }
+    }
+    if (c == 0) {
+      rs_s[8 * i + g] = up * kQScale<D>;
+      vis_s[8 * i + g] = qa_row(row0 + 8 * i + g, p.G, n, qn).sees;
+    }
   }
 }
 
@@ -285,7 +295,6 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
   __shared__ int s_unit;
   __shared__ volatile int s_bad;
 
-  griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -300,6 +309,8 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
     fence_mbar_init();
     s_bad = 0;
   }
+  griddep_wait();
+  griddep_launch_dependents();
   // ---- the share: prefix sums of the units' full blocks ----
   const int per = (p.U + kThreads - 1) / kThreads;
   const int a0 = min(p.U, tid * per), a1 = min(p.U, a0 + per);
@@ -407,10 +418,11 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
     int prepared = 0;
     auto prepare = [&]() {
       const int b = ahead.u / p.Hkv, qn = quant_count(p.q_len, b, p.T, p.status, lane == 0);
+      constexpr int GR = F32 ? 1 : ROWS / 8;  // row groups at once: 32 rows of bf16 take 64 registers
 #pragma unroll 1
-      for (int r = 0; r < ROWS / 8; ++r)
-        qa_queries<D, F32>(p, ahead.u, ahead.tile * ROWS + 8 * r, ahead.tokens, qn, q_of(prepared) + r * KS * 32 * (F32 ? 16 : 8),
-                           rs_of(prepared) + 8 * r, vis_of(prepared) + 8 * r, lane);
+      for (int r = 0; r < ROWS; r += 8 * GR)
+        qa_queries<D, GR, F32>(p, ahead.u, ahead.tile * ROWS + r, ahead.tokens, qn, q_of(prepared) + r * KS * 4 * (F32 ? 16 : 8),
+                               rs_of(prepared) + r, vis_of(prepared) + r, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[prepared % NB]);
 #pragma unroll
@@ -923,6 +935,7 @@ __global__ void __launch_bounds__(kQcThreads) quant_weights_kernel(QStreamParams
     w[i] = 0.f;
   }
   griddep_wait();
+  griddep_launch_dependents();
   for (int tile = 0; tile < p.tiles; ++tile) {
     const long long vu = (long long)u * p.tiles + tile;
     const bool on = tile * ROWS + r < p.T * p.G;
@@ -966,8 +979,7 @@ cudaError_t stream_variant(const QPlan& pl, const QStreamParams& p, cudaStream_t
   static std::atomic<int> lim[64];
   const cudaError_t e = raise_smem_limit((const void*)quant_stream_kernel<D, NT, RG, F32>, Gm::SMEM, lim);
   if (e != cudaSuccess) return e;
-  quant_stream_kernel<D, NT, RG, F32><<<pl.ctas, Gm::THREADS, Gm::SMEM, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(quant_stream_kernel<D, NT, RG, F32>, dim3(pl.ctas), Gm::THREADS, Gm::SMEM, stream, p);
 }
 
 template <typename T, int D>

@@ -234,6 +234,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 || D == 64 ? 4 : 2)
 quant_blocks_kernel(QAppendArgs p, int Hkv, long long payload) {
   __shared__ UnitImage<D> img;
+  griddep_wait();
   griddep_launch_dependents();
   const int u = blockIdx.x, j = blockIdx.y;
   const UnitAppend a = unit_append(p, Hkv, u, false);
@@ -250,6 +251,8 @@ template <typename T, int D, bool BLOCK>
 __global__ void __launch_bounds__(kAppendThreads) quant_tail_kernel(QAppendArgs p, int Hkv, long long payload) {
   constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE;
   const int u = blockIdx.x, b = u / Hkv, h = u % Hkv, tid = threadIdx.x;
+  if (BLOCK) griddep_wait();  // (the call's first launch)
+  griddep_launch_dependents();
   const UnitAppend a = unit_append(p, Hkv, u, tid == 0);
   uint8_t* tail = p.tail + u * payload;
   const int old = a.n0 % kQB, done = (old + a.add) / kQB;
@@ -262,8 +265,8 @@ __global__ void __launch_bounds__(kAppendThreads) quant_tail_kernel(QAppendArgs 
       q.store(img, q.idx);
     }
   }
-  griddep_wait();   // ... by the blocks' launch
-  __syncthreads();  // and here: the old tail and length have been read
+  if (!BLOCK) griddep_wait();  // the blocks' launch has read the old tail
+  __syncthreads();             // ... and so has this one, and the length
   const int first = done > 0 ? 0 : old, left = old + a.add - done * kQB;
   for (int i = tid; i < (left - first) * NCH; i += kAppendThreads) {
     const int r = first + i / NCH, c = i % NCH;
@@ -283,15 +286,14 @@ __global__ void __launch_bounds__(kAppendThreads) quant_tail_kernel(QAppendArgs 
 template <typename T, int D>
 cudaError_t append_variant(const Shape& s, const QAppendArgs& a, cudaStream_t stream) {
   if (a.n <= kQB) {
-    quant_tail_kernel<T, D, true><<<s.U, kAppendThreads, 0, stream>>>(a, s.Hkv, s.payload);
+    return launch_dependent(quant_tail_kernel<T, D, true>, dim3(s.U), kAppendThreads, 0, stream, a, s.Hkv, s.payload);
   } else {
     const int most = std::min((a.n + kQB - 1) / kQB, a.max_blocks);
-    quant_blocks_kernel<T, D><<<dim3(s.U, most), kAppendThreads, 0, stream>>>(a, s.Hkv, s.payload);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_dependent(quant_blocks_kernel<T, D>, dim3(s.U, most), kAppendThreads, 0, stream, a, s.Hkv, s.payload);
     if (e != cudaSuccess) return e;
     return launch_dependent(quant_tail_kernel<T, D, false>, dim3(s.U), kAppendThreads, 0, stream, a, s.Hkv, s.payload);
   }
-  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -299,9 +301,12 @@ cudaError_t append_variant(const Shape& s, const QAppendArgs& a, cudaStream_t st
 // shared memory once, a radix selection (8 bits at a time over the order-preserving
 // keys) finds the largest weight that still leaves, and a stable partition writes
 // the row back: kept blocks in order, then the evicted ones, which are the next
-// destinations of appended blocks.
+// destinations of appended blocks. The row is read and written once (16 bytes an
+// entry); with rows of hundreds of entries latency is all there is, so a pass costs
+// one barrier: each has a histogram of its own, and every warp adds it up for itself.
 // ---------------------------------------------------------------------------
 constexpr int kEvictThreads = 256;
+constexpr int kEvictAhead = 4;  // entries per thread fetched before the length is known
 
 // Order-preserving key of a weight; NaN ranks above every number.
 __device__ __forceinline__ uint32_t weight_key(uint32_t bits) {
@@ -309,16 +314,20 @@ __device__ __forceinline__ uint32_t weight_key(uint32_t bits) {
   return isnan(f) ? 0xFFFFFFFFu : ordered_key(f);
 }
 
-// Exclusive prefix sum over the block's threads; *total receives the sum.
-__device__ __forceinline__ int block_scan(int v, int* warp_s, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+// Inclusive prefix sum over a warp's lanes.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
   }
-  __syncthreads();  // warp_s is free
+  return v;
+}
+
+// Exclusive prefix sum over the block's threads, *total its sum. warp_s is not used twice.
+__device__ __forceinline__ int block_scan(int v, int* warp_s, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int inc = warp_scan(v, lane);
   if (lane == 31) warp_s[warp] = inc;
   __syncthreads();
   int base = 0, sum = 0;
@@ -334,12 +343,23 @@ __device__ __forceinline__ int block_scan(int v, int* warp_s, int* total) {
 
 __global__ void __launch_bounds__(kEvictThreads) quant_evict_kernel(QEvictArgs p) {
   extern __shared__ uint32_t evict_smem[];
-  __shared__ int hist[256];
-  __shared__ int warp_s[kEvictThreads / 32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_rank;
-  const int u = blockIdx.x, tid = threadIdx.x;
+  __shared__ int hist[4][256];
+  __shared__ int eq_s[kEvictThreads / 32], kept_s[kEvictThreads / 32];
+  const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   const long long row = (long long)u * p.max_blocks;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) hist[k][tid] = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  // the first entries of the row are fetched together with its length
+  uint32_t w0[kEvictAhead];
+  int32_t t0[kEvictAhead];
+#pragma unroll
+  for (int k = 0; k < kEvictAhead; ++k) {
+    const int i = tid + k * kEvictThreads;
+    w0[k] = i < p.max_blocks ? __float_as_uint(p.mass[row + i]) : 0u;
+    t0[k] = i < p.max_blocks ? p.tab[row + i] : 0;
+  }
   const int n0 = quant_len(p.lens, u, p.max_blocks, p.status, tid == 0);
   const int full = n0 < 0 ? 0 : n0 / kQB, over = max(0, full - p.budget);
   if (over == 0) {  // nothing to evict: the row as it is
@@ -351,60 +371,66 @@ __global__ void __launch_bounds__(kEvictThreads) quant_evict_kernel(QEvictArgs p
     if (tid == 0 && p.lens_out != p.lens) p.lens_out[u] = p.lens[u];
     return;
   }
-  uint32_t* w = evict_smem;                                  // [full] weights (bit patterns)
+  uint32_t* w = evict_smem;                                     // [full] weights (bit patterns)
   int32_t* tb = reinterpret_cast<int32_t*>(evict_smem + full);  // [full] table entries
-  for (int i = tid; i < full; i += kEvictThreads) {
+  const int old = full - p.n_recent;                            // >= over: n_recent <= budget
+#pragma unroll
+  for (int k = 0; k < kEvictAhead; ++k) {
+    const int i = tid + k * kEvictThreads;
+    if (i < full) {
+      w[i] = w0[k];
+      tb[i] = t0[k];
+    }
+  }
+  for (int i = tid + kEvictAhead * kEvictThreads; i < full; i += kEvictThreads) {
     w[i] = __float_as_uint(p.mass[row + i]);
     tb[i] = p.tab[row + i];
   }
   const float tail_mass = full < p.max_blocks ? p.mass[row + full] : 0.f;
-  const int old = full - p.n_recent;  // >= over: n_recent <= budget
-  if (tid == 0) {
-    s_prefix = 0;
-    s_rank = over;  // the over-th smallest key among those with the prefix
-  }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
-    __syncthreads();
-    const uint32_t prefix = s_prefix;
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    const int rank = s_rank;
+  __syncthreads();
+  uint32_t cut = 0;  // the over-th smallest key, a digit at a time
+  int rank = over;   // ... among the keys that share the digits so far
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int shift = 24 - 8 * k;
+    const uint32_t mask = k == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
     for (int i = tid; i < old; i += kEvictThreads) {
-      const uint32_t k = weight_key(w[i]);
-      if ((k & mask) == prefix) atomicAdd(hist + ((k >> shift) & 255), 1);
+      const uint32_t key = weight_key(w[i]);
+      if ((key & mask) == cut) atomicAdd(&hist[k][(key >> shift) & 255], 1);
     }
     __syncthreads();
-    int total;
-    const int c = hist[tid];
-    const int before = block_scan(c, warp_s, &total);
-    if (before < rank && rank <= before + c) {  // exactly one thread
-      s_prefix = prefix | ((uint32_t)tid << shift);
-      s_rank = rank - before;
+    int c[8], sum = 0;  // the lane's eight bins
+#pragma unroll
+    for (int x = 0; x < 8; ++x) sum += c[x] = hist[k][8 * lane + x];
+    int before = warp_scan(sum, lane) - sum;
+    const int at = __ffs(__ballot_sync(0xffffffffu, before < rank && rank <= before + sum)) - 1;
+    int bin = 0;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {  // (on lane `at`: the bin that reaches the rank)
+      if (bin == x && before + c[x] < rank) {
+        before += c[x];
+        ++bin;
+      }
     }
-    __syncthreads();
+    cut |= (uint32_t)(8 * at + __shfl_sync(0xffffffffu, bin, at)) << shift;
+    rank -= __shfl_sync(0xffffffffu, before, at);
   }
-  const uint32_t cut = s_prefix;
-  // Blocks below the cut leave; of those at the cut, the s_rank of the highest indices.
+  // Blocks below the cut leave; of those at the cut, the `rank` ones of the highest indices.
   const int per = (old + kEvictThreads - 1) / kEvictThreads, i0 = min(old, tid * per), i1 = min(old, i0 + per);
-  int eq = 0;
-  for (int i = i0; i < i1; ++i) eq += weight_key(w[i]) == cut;
-  int eq_total;
-  int eq_at = block_scan(eq, warp_s, &eq_total);
-  const int eq_keep = eq_total - s_rank;
-  int kept = 0;
-  {
-    int x = eq_at;
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t k = weight_key(w[i]);
-      kept += k > cut || (k == cut && x++ < eq_keep);
-    }
+  int eq = 0, above = 0;
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t key = weight_key(w[i]);
+    eq += key == cut;
+    above += key > cut;
   }
-  int kept_total;
-  int at = block_scan(kept, warp_s, &kept_total);
+  int eq_total, kept_total;
+  int eq_at = block_scan(eq, eq_s, &eq_total);
+  const int eq_keep = eq_total - rank;
+  int at = block_scan(above + max(0, min(eq, eq_keep - eq_at)), kept_s, &kept_total);
   int gone = full - over + (i0 - at);
   for (int i = i0; i < i1; ++i) {
-    const uint32_t k = weight_key(w[i]);
-    const bool keep = k > cut || (k == cut && eq_at++ < eq_keep);
+    const uint32_t key = weight_key(w[i]);
+    const bool keep = key > cut || (key == cut && eq_at++ < eq_keep);
     const int to = keep ? at++ : gone++;
     p.tab_out[row + to] = tb[i];
     if (keep) p.mass_out[row + to] = __uint_as_float(w[i]);
@@ -437,12 +463,11 @@ cudaError_t launch_quant_append(const Shape& s, const QAppendArgs& a, cudaStream
 cudaError_t launch_quant_evict(const Shape& s, const QEvictArgs& a, cudaStream_t stream) {
   const size_t smem = (size_t)a.max_blocks * 8;
   static std::atomic<int> lim[64];
-  if (smem > 40000) {
+  if (smem > 40000) {  // (4.2 KB more are static)
     const cudaError_t e = raise_smem_limit((const void*)quant_evict_kernel, smem, lim);
     if (e != cudaSuccess) return e;
   }
-  quant_evict_kernel<<<s.U, kEvictThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(quant_evict_kernel, dim3(s.U), kEvictThreads, smem, stream, a);
 }
 
 }  // namespace nosa
