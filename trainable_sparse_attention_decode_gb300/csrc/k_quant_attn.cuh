@@ -18,8 +18,9 @@
 //             unit's queries ready, and go on.
 //   combine : one CTA per unit (and row tile) attends to the tail in fp32 while the
 //             stream still runs, then joins the unit's parts.
-//   weights : with accumulated weights, a warp per block adds up what the stream
-//             noted for the block, relative to the rows' final sums.
+//   weights : with accumulated weights, what the stream noted for each block is added
+//             up relative to the rows' final sums: by the join where one CTA has all
+//             rows of a unit (up to 8), else by a launch of its own.
 //
 // The products take the tensor cores' 16 x 8 x 16 shape with the codes as the large
 // operand (tokens x dims, dims x tokens) and the rows as the small one: up to 8 rows
@@ -73,7 +74,7 @@ struct QStreamParams {
   float* part_acc;    // ... [rows][d] its output (not normalised)
   float2* rowstat;    // [units x tiles][rows] final maximum and 1 / sum
   float* tail_w;      // [units x tiles][rows] weight of the tail
-  float2* blk;        // [units x tiles][max_blocks][rows] maximum and sum of a block, or null
+  float2* blk;        // [units x tiles][max_blocks][rows] maximum and sum of a block, or null (no weights asked for)
 };
 
 // 1 / sqrt(d)
@@ -155,12 +156,12 @@ struct QGeom {
   static constexpr int ROWS = 8 * NT * RG, KS = D / 16, UB = quant_unit_bytes(D);
   // Eight warps in all leave each one 255 registers, which 16 rows of output need; more
   // leave 168.
-  static constexpr int IS = NT == 1 ? (D == 128 ? 4 : 8) : RG == 1 ? 6 : 3;
+  static constexpr int IS = NT == 2 ? 6 / RG : RG > 1 ? 8 / RG : D == 128 ? 4 : 8;
   static constexpr int W = IS * RG;             // consumer warps; a producer and a helper come on top
   static constexpr int THREADS = 32 * (W + 2);
-  static constexpr int STAGES = D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 8 : RG == 1 ? 6 : 9;
-  static constexpr int SL = NT == 2 && F32 && D == 128 ? 2 : 4;  // slices of a block that a warp takes at once
-  static constexpr int NB = NT == 1 ? 2 : 1;    // buffers for queries and for parts
+  static constexpr int STAGES = D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 8 : 9;
+  static constexpr int SL = 4;                  // slices of a block that a warp takes at once
+  static constexpr int NB = NT * RG == 1 ? 2 : 1;  // buffers for queries and for parts
   static constexpr int RP = D + 4;              // padded row of a part
   static constexpr int Q_BYTES = NT * RG * KS * 32 * (F32 ? 16 : 8);
   static constexpr int RED_BYTES = W * 8 * NT * RP * 4, ML_BYTES = W * 8 * NT * 8;
@@ -721,9 +722,10 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
 // of the unit's parts for four dims of a row, the shares join in shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kQcRows = 8;
+constexpr int kQcScan = 4;  // lengths of a thread
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams p, int rows) {
+__global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams p, int rows, bool weights) {
   constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE;
   constexpr int KC = NCH / 4;                        // 16-byte key chunks of a thread: token tid % 64
   constexpr int TG = kQcThreads / NCH, TPT = kQB / TG;  // value tokens: TPT of one 16-byte column
@@ -734,7 +736,9 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
   __shared__ float w_s[kQcRows][kQB];                // weights, -1: masked
   __shared__ float4 ja_s[kQcThreads];
   __shared__ float2 jm_s[kQcThreads];
-  __shared__ float m_s[kQcRows], l_s[kQcRows];
+  __shared__ float m_s[kQcRows], l_s[kQcRows], tw_s[kQcRows];
+  __shared__ float2 st_s[kQcRows];
+  __shared__ int2 scan_s[kQcThreads / 32];
   griddep_launch_dependents();
   const int vu = blockIdx.x, u = vu / p.tiles, tile = vu % p.tiles, b = u / p.Hkv, h = u % p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -833,11 +837,42 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
     }
     __syncthreads();
   }
+  // Items of the call and the first one of this unit and tile: added up here, while the
+  // stream runs, where a thread has few lengths to read; else left by the stream.
+  long long total = 0, first = 0;
+  const bool few = p.U <= kQcScan * kQcThreads;
+  if (few) {
+    int all = 0, ahead = 0;
+#pragma unroll
+    for (int k = 0; k < kQcScan; ++k) {
+      const int i = tid + k * kQcThreads;
+      const int c = i < p.U ? max(0, quant_len(p.lens, i, p.max_blocks, nullptr, false)) / kQB : 0;
+      all += c;
+      if (i < u) ahead += c;
+    }
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, s);
+      ahead += __shfl_xor_sync(0xffffffffu, ahead, s);
+    }
+    if (lane == 0) scan_s[warp] = make_int2(all, ahead);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kQcThreads / 32; ++w) {
+      total += scan_s[w].x;
+      first += scan_s[w].y;
+    }
+    total *= p.tiles;
+    first = first * p.tiles + (long long)tile * nb;
+  }
   griddep_wait();  // the stream's parts
   // parts of this unit and tile: CTAs [c0, c0 + parts) of the stream, slot c + vu each
   int c0 = 0, parts = 0;
   if (nb > 0) {
-    const long long total = *p.total, first = p.base[vu];
+    if (!few) {
+      total = *p.total;
+      first = p.base[vu];
+    }
     const int active = qa_active(total, p.ctas);
     c0 = qa_cta_of(first, total, active);
     parts = qa_cta_of(first + nb - 1, total, active) - c0 + 1;
@@ -895,17 +930,52 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
       const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
       *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
     }
-    if (x == 0 && blockIdx.z == 0) {
-      if (p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : mu + logf(l);
+    if (x == 0) {
+      if (p.lse != nullptr && blockIdx.z == 0) p.lse[row] = l == 0.f ? -INFINITY : mu + logf(l);
       if (p.blk != nullptr) {
-        p.rowstat[(long long)vu * rows + rt + r] = make_float2(mu, inv);
-        p.tail_w[(long long)vu * rows + rt + r] = nt > 0 ? l_s[r] * exp_from(m_s[r], mu) * inv : 0.f;
+        const float tw = nt > 0 ? l_s[r] * exp_from(m_s[r], mu) * inv : 0.f;
+        if (weights) {
+          st_s[r] = make_float2(mu, inv);
+          tw_s[r] = tw;
+        } else if (blockIdx.z == 0) {
+          p.rowstat[(long long)vu * rows + rt + r] = make_float2(mu, inv);
+          p.tail_w[(long long)vu * rows + rt + r] = tw;
+        }
       }
     }
   }
-  if (p.blk != nullptr && blockIdx.z == 0 && tid >= live && tid < kQcRows) {  // rows that do not exist weigh nothing
+  if (p.blk != nullptr && !weights && blockIdx.z == 0 && tid >= live && tid < kQcRows) {  // rows that do not exist weigh nothing
     p.rowstat[(long long)vu * rows + rt + tid] = make_float2(0.f, 0.f);
     p.tail_w[(long long)vu * rows + rt + tid] = 0.f;
+  }
+  if (weights) {
+    // All of the unit's rows are here: the accumulated weights too. Eight lanes have a
+    // block's rows; CTA z of the unit takes every gridDim.z-th run of 32 blocks.
+    __syncthreads();
+    const int row = tid % kQcRows, step = kQcThreads / kQcRows * gridDim.z;
+    const float2 st = row < live ? st_s[row] : make_float2(0.f, 0.f);
+    const float tw = row < live ? tw_s[row] : 0.f;
+    float* mass = p.mass + (long long)u * p.max_blocks;
+    const float2* note = p.blk + (long long)u * p.max_blocks * kQcRows + row;
+    for (int j0 = blockIdx.z * (kQcThreads / kQcRows) + tid / kQcRows; j0 - tid / kQcRows < p.max_blocks; j0 += 8 * step) {
+      float2 ml[8];
+      float old[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = j0 + k * step;
+        ml[k] = j < nb && row < live ? note[(long long)j * kQcRows] : make_float2(-INFINITY, 0.f);
+        old[k] = row == 0 && j < p.max_blocks && p.decay != 0.f ? mass[j] * p.decay : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = j0 + k * step;
+        float w = j < nb ? ml[k].y * exp_from(ml[k].x, st.x) * st.y : j == nb ? tw : 0.f;
+        w += __shfl_xor_sync(0xffffffffu, w, 1);
+        w += __shfl_xor_sync(0xffffffffu, w, 2);
+        w += __shfl_xor_sync(0xffffffffu, w, 4);
+        if (row == 0 && j < p.max_blocks) mass[j] = old[k] + w;
+      }
+    }
   }
 }
 
@@ -985,14 +1055,30 @@ cudaError_t stream_variant(const QPlan& pl, const QStreamParams& p, cudaStream_t
 template <typename T, int D>
 cudaError_t stream_launches(const Shape& s, const QPlan& pl, const QStreamParams& p, cudaStream_t stream) {
   constexpr bool F32 = sizeof(T) == 4;
-  cudaError_t e = pl.rows == 8    ? stream_variant<D, 1, 1, F32>(pl, p, stream)
-                  : pl.rows == 16 ? stream_variant<D, 2, 1, F32>(pl, p, stream)
-                                  : stream_variant<D, 2, 2, F32>(pl, p, stream);
+  // 16 and 32 rows as row groups of 8, which convert the codes once each but leave
+  // registers enough for eight consumer warps; 32 rows of bf16 as two groups of 16 on
+  // six. Measured at 4 requests x 8 KV heads x 16384 tokens, d = 128, us: 16 rows 39
+  // (one group of 16: 44), fp32 47 (59); 32 rows 62 (two groups of 16: 60), fp32 78 (89).
+  cudaError_t e;
+  if (pl.rows == 8)
+    e = stream_variant<D, 1, 1, F32>(pl, p, stream);
+  else if (pl.rows == 16)
+    e = stream_variant<D, 1, 2, F32>(pl, p, stream);
+  else if constexpr (F32)
+    e = stream_variant<D, 1, 4, F32>(pl, p, stream);
+  else
+    e = stream_variant<D, 2, 2, F32>(pl, p, stream);
   if (e != cudaSuccess) return e;
   // few units have many parts each: more CTAs share the join
   const int vu = s.U * pl.tiles, y = pl.rows / kQcRows, z = vu * y <= 16 ? 4 : vu * y <= 32 ? 2 : 1;
-  e = launch_dependent(quant_combine_kernel<T, D>, dim3(vu, y, z), kQcThreads, 0, stream, p, pl.rows);
-  if (e != cudaSuccess || p.mass == nullptr) return e;
+  // Where one CTA has all rows of a unit, the join does the accumulated weights too, if
+  // they are few; long tables want the warps of a launch of their own. Measured at 128
+  // units of d = 128 in bf16, us (joined / own launch): 32 blocks 22.1 / 23.1, 128 54.2 /
+  // 54.3, 256 96.7 / 95.5, 512 105.4 / 100.0 (ragged); four CTAs a unit at 16 units: 375
+  // blocks 27.1 / 27.6.
+  const bool joined = p.mass != nullptr && pl.rows == kQcRows && p.max_blocks <= 128 * z;
+  e = launch_dependent(quant_combine_kernel<T, D>, dim3(vu, y, z), kQcThreads, 0, stream, p, pl.rows, joined);
+  if (e != cudaSuccess || p.mass == nullptr || joined) return e;
   auto weights = [&](auto kernel, int per) {
     return launch_dependent(kernel, dim3(s.U, (p.max_blocks + per - 1) / per), kQcThreads, 0, stream, p);
   };
