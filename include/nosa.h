@@ -540,7 +540,8 @@ nosa_status nosa_quant_append(const nosa_config* cfg, int32_t max_blocks, int32_
  * A row that sees no token gives out = 0, lse = -inf. Sums and the softmax are held
  * in fp32, the products take 11-bit (bf16) or 22-bit (fp32) operands.
  *   q    : device [batch][n_queries][n_q_heads][head_dim] of cfg dtype
- *   out  : the same shape, contiguous (written; rows past q_len[b] are left)
+ *   out  : the same shape, contiguous (written; rows past q_len[b] are left); it must
+ *          not overlap q
  *   lse  : device fp32 [batch][n_queries][n_q_heads] or NULL
  *   mass : fp32 [U][max_blocks] or NULL. Every entry becomes decay * mass plus, where
  *          it has tokens, their softmax weights, summed over the request's queries and

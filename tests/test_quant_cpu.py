@@ -58,7 +58,7 @@ def _append(cfg, max_blocks=4, n=1, k=P, ks=None, v=P, vs=None, e=P, n_new=None,
                                       n_units, tab, tail, lens, lens_out, status, None)
 
 
-def _attention(cfg, max_blocks=4, n=1, units=P, n_units=8, tab=P, tail=P, lens=P, q=P, qs=None, q_len=None, out=P,
+def _attention(cfg, max_blocks=4, n=1, units=P, n_units=8, tab=P, tail=P, lens=P, q=P, qs=None, q_len=None, out=2 * P,
                lse=None, mass=None, decay=1.0, ws=P, ws_bytes=1 << 40, status=None):
     return nosa.lib.nosa_quant_attention(C.byref(cfg) if cfg else None, max_blocks, n, units, n_units, tab, tail, lens,
                                          q, qs, q_len, out, lse, mass, decay, ws, ws_bytes, status, None)
@@ -88,7 +88,7 @@ def test_append_refusals(kw, status):
     (dict(lens=None), INVALID), (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(ws=None), INVALID),
     (dict(ws=P + 16), INVALID), (dict(q=P + 8), INVALID), (dict(out=P + 8), INVALID), (dict(lse=P + 2), INVALID),
     (dict(mass=P + 1), INVALID), (dict(mass=P, decay=1.5), INVALID), (dict(mass=P, decay=-0.1), INVALID),
-    (dict(mass=P, decay=float("nan")), INVALID), (dict(qs=(C.c_int64 * 3)(1024, 1024, 4)), INVALID)])
+    (dict(mass=P, decay=float("nan")), INVALID), (dict(out=P), INVALID), (dict(qs=(C.c_int64 * 3)(1024, 1024, 4)), INVALID)])
 def test_attention_refusals(kw, status):
     assert _attention(_cfg(), **kw) == status
     assert nosa.nosa_last_error() != ""

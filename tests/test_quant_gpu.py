@@ -14,6 +14,8 @@ additions. The weights enter the second product with 11 bits (2^-11 of A) where 
 output is bf16, with 22 bits where it is fp32; the output's own rounding is half a
 step, 2^-8 (bf16) or 2^-24 (fp32).
 """
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -22,6 +24,7 @@ import trainable_sparse_attention_decode_gb300 as nosa
 from oracle import quant_oracle as Q
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 B = 64
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 
@@ -322,7 +325,8 @@ class Cache:
             rel = 2 * dl + 2.0 ** -20 + (n / 16 + 16) * 2.0 ** -23
             tol = o_bits * np.abs(want) + (p_bits + 2 * rel[:, None]) * A + 1e-30
             assert np.all(np.abs(got - want) <= tol), (u, np.max(np.abs(got - want) / tol))
-            assert np.all(np.abs(gl - wl)[~empty] <= (dl + rel + 2.0 ** -23 * np.abs(wl))[~empty]), u
+            far = np.abs(gl[~empty] - wl[~empty])
+            assert np.all(far <= (dl + rel)[~empty] + 2.0 ** -23 * np.abs(wl[~empty])), u
             if mass is not None:
                 full = np.zeros(self.cap * B)
                 full[:n] = w.sum(0)
@@ -344,7 +348,8 @@ CASES = [  # dtype, batch, hq, hkv, d, lens by request (heads differ by -h), que
     ("f32", 2, 12, 4, 128, [130, 127], 1), ("bf16", 1, 12, 2, 128, [1300], 1), ("bf16", 1, 8, 1, 64, [4000], 1),
     ("f32", 1, 2, 2, 128, [0], 1), ("bf16", 2, 8, 2, 128, [700, 3], 8), ("f32", 1, 6, 2, 64, [333], 5),
     ("bf16", 1, 8, 1, 128, [640], 32), ("f32", 1, 8, 1, 128, [200], 17), ("bf16", 1, 4, 4, 64, [129], 128),
-    ("bf16", 40, 4, 4, 64, [70 + 5 * i for i in range(40)], 1), ("bf16", 2, 6, 1, 128, [190, 64], 3)]
+    ("bf16", 40, 4, 4, 64, [70 + 5 * i for i in range(40)], 1), ("bf16", 2, 6, 1, 128, [190, 64], 3),
+    ("bf16", 300, 4, 4, 64, [37 * i % 200 for i in range(300)], 1), ("f32", 150, 8, 8, 64, [29 * i % 150 for i in range(150)], 2)]
 
 
 @pytest.mark.parametrize("dtype,batch,hq,hkv,d,lens,T", CASES)
@@ -363,6 +368,11 @@ def test_attention_matches_oracle(dtype, batch, hq, hkv, d, lens, T, with_mass):
     ws, m1 = c.workspace, dev(m0) if with_mass else None
     out2, lse2, _ = c.run(q, mass=m1, decay=0.75, workspace=ws)
     assert torch.equal(out, out2) and torch.equal(lse, lse2) and (mass is None or torch.equal(mass, m1))
+    # and other queries right behind each other: nothing of the call before is left over
+    qs = [query(rng, batch, T, hq, d, dtype) for _ in range(3)]
+    res = [c.run(x, workspace=ws) if mass is None else c.run(x, mass=dev(m0), workspace=ws) for x in qs]
+    c.check(qs[-1], *res[-1][:2])
+    assert not torch.equal(res[0][0], res[2][0]) or not any(lens)
 
 
 @pytest.mark.parametrize("dtype,hq,hkv,d,T", [
@@ -561,6 +571,79 @@ def test_attention_on_two_streams():
     torch.cuda.synchronize()
     for c, q, (out, lse, _) in zip(caches, qs, res):
         c.check(q, out, lse)
+
+
+def test_attention_captured_behind_other_work():
+    """A capture in which the call follows a fork, a join, a copy and a memset."""
+    rng = np.random.default_rng(15)
+    c = Cache(rng, "bf16", 2, 8, 2, 64, [900, 65, 300, 128]).upload()
+    q = query(rng, 2, 1, 8, 64, "bf16")
+    q_in, out, lse = torch.zeros_like(q), torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    mass = torch.zeros(c.tab.shape, device="cuda")
+    ws = torch.empty(nosa.nosa_quant_attention_workspace_bytes(c.cfg, c.cap, 1, True), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            q_in.copy_(q)
+        mass.zero_()
+        main.wait_stream(side)
+        nosa.nosa_quant_attention(c.cfg, c.units, c.t_tab, c.tail, c.t_lens, q_in, out, lse=lse, mass=mass, workspace=ws)
+        other = out.clone()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            nosa.nosa_quant_attention(c.cfg, c.units, c.t_tab, c.tail, c.t_lens, q_in, out, lse=lse, mass=mass, workspace=ws)
+        main.wait_stream(side)
+    for _ in range(3):
+        q.copy_(query(rng, 2, 1, 8, 64, "bf16"))
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        m = f64(mass)  # two calls' weights
+        c.check(q, out, lse, mass0=m / 2, mass=m, decay=1.0)
+        assert torch.equal(other, out)
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured."""
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import numpy as np, torch
+import test_quant_gpu as t
+nosa = t.nosa
+rng = np.random.default_rng(3)
+c = t.Cache(rng, "f32", 1, 4, 2, 64, [300, 100], cap=6).upload()
+q = t.query(rng, 1, 4, 4, 64, "f32")
+out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+mass = torch.zeros(c.tab.shape, device="cuda")
+k = t.query(rng, 1, 70, 2, 64, "f32")
+ws = torch.empty(nosa.nosa_quant_attention_workspace_bytes(c.cfg, c.cap, 4, True), dtype=torch.uint8, device="cuda")
+c.t_tab[:, 2:] = torch.arange(4, dtype=torch.int32, device="cuda") + len(c.images)
+units = torch.zeros(len(c.images) + 4, c.images.shape[1], dtype=torch.uint8, device="cuda")
+units[:len(c.images)] = c.units
+c.t_tab[0, :4] = t.dev(c.tab[0, :4])
+c.t_tab[1, 1] = len(c.images)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+lens = c.t_lens.clone()
+with torch.cuda.graph(g):
+    nosa.nosa_quant_attention(c.cfg, units, c.t_tab, c.tail, lens, q, out, lse=lse, mass=mass, workspace=ws)
+    nosa.nosa_quant_append(c.cfg, k[:, :, :2], k[:, :, :2], None, units, c.t_tab, c.tail, lens)
+    nosa.nosa_quant_evict(c.cfg, 2, 1, c.t_tab, mass, lens)
+g.replay()
+torch.cuda.synchronize()
+c.check(q, out, lse)
+assert lens.tolist() == [64 * 2 + (300 + 70) %% 64, 64 * 2 + (100 + 70) %% 64], lens.tolist()
+print("ok")
+""" % (ROOT, os.path.join(ROOT, "tests"))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
 
 
 # ---------------------------------------------------------------------------

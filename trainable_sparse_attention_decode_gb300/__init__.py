@@ -504,6 +504,8 @@ def nosa_quant_attention(cfg: NosaConfig, units, block_tab, tail, lens, q, out, 
         workspace = torch.empty(
             nosa_quant_attention_workspace_bytes(cfg, block_tab.shape[1], shp[1], mass is not None),
             dtype=torch.uint8, device=q.device)
+        if stream is not None:  # (it may be dropped before that stream has used it)
+            workspace.record_stream(torch.cuda.ExternalStream(_stream(stream), device=dev))
     _check(lib.nosa_quant_attention(
         C.byref(cfg), block_tab.shape[1], shp[1], up, nu, tab, tl, lp, qp, qs,
         None if q_len is None else _arg(q_len, dev, (cfg.batch,), i32, "q_len"),

@@ -870,8 +870,8 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
   int c0 = 0, parts = 0;
   if (nb > 0) {
     if (!few) {
-      total = *p.total;
-      first = p.base[vu];
+      total = __ldcg(p.total);
+      first = __ldcg(p.base + vu);
     }
     const int active = qa_active(total, p.ctas);
     c0 = qa_cta_of(first, total, active);
@@ -902,8 +902,8 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int i = i0 + k * groups;
-        mm[k] = i < parts ? ml[(long long)i * rows] : make_float2(-INFINITY, 0.f);
-        yy[k] = i < parts ? *reinterpret_cast<const float4*>(src + (long long)i * rows * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+        mm[k] = i < parts ? __ldcg(ml + (long long)i * rows) : make_float2(-INFINITY, 0.f);
+        yy[k] = i < parts ? __ldcg(reinterpret_cast<const float4*>(src + (long long)i * rows * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) merge(mm[k], yy[k]);
@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int j = j0 + k * step;
-        ml[k] = j < nb && row < live ? note[(long long)j * kQcRows] : make_float2(-INFINITY, 0.f);
+        ml[k] = j < nb && row < live ? __ldcg(note + (long long)j * kQcRows) : make_float2(-INFINITY, 0.f);
         old[k] = row == 0 && j < p.max_blocks && p.decay != 0.f ? mass[j] * p.decay : 0.f;
       }
 #pragma unroll
@@ -1009,18 +1009,18 @@ __global__ void __launch_bounds__(kQcThreads) quant_weights_kernel(QStreamParams
   for (int tile = 0; tile < p.tiles; ++tile) {
     const long long vu = (long long)u * p.tiles + tile;
     const bool on = tile * ROWS + r < p.T * p.G;
-    const float2 st = on ? p.rowstat[vu * ROWS + r] : make_float2(0.f, 0.f);
+    const float2 st = on ? __ldcg(p.rowstat + vu * ROWS + r) : make_float2(0.f, 0.f);
     float2 ml[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = first + i * PW;
-      ml[i] = on && j < nb ? p.blk[(vu * p.max_blocks + j) * ROWS + r] : make_float2(-INFINITY, 0.f);
+      ml[i] = on && j < nb ? __ldcg(p.blk + (vu * p.max_blocks + j) * ROWS + r) : make_float2(-INFINITY, 0.f);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = first + i * PW;
       if (on && j < nb) w[i] += ml[i].y * exp_from(ml[i].x, st.x) * st.y;
-      if (j == nb && nt > 0) w[i] += p.tail_w[vu * ROWS + r];
+      if (j == nb && nt > 0) w[i] += __ldcg(p.tail_w + vu * ROWS + r);
     }
   }
 #pragma unroll

@@ -126,6 +126,7 @@ nosa_status nosa_quant_attention(const nosa_config* cfg, int32_t max_blocks, int
     return refuse(NOSA_ERR_UNSUPPORTED, "n_queries must be <= " + std::to_string(kQMaxQueries));
   if (n_units < 0 || (n_units > 0 && !units) || !block_tab || !tail || !lens || !q || !out || !workspace)
     return invalid("NULL or negative argument");
+  if (q == out) return invalid("out must not be q");
   if (mass && !(decay >= 0.f && decay <= 1.f)) return invalid("decay must be in [0, 1]");
   if (!aligned_to(units, 16) || !aligned_to(tail, 16) || !aligned_to(q, 16) || !aligned_to(out, 16) ||
       !aligned_to(workspace, 256) || !aligned_to(block_tab, 4) || !aligned_to(lens, 4) || !aligned_to(q_len, 4) ||
