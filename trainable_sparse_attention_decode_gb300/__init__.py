@@ -126,9 +126,15 @@ lib = _load()
 # ---------------------------------------------------------------------------
 # marshalling helpers
 # ---------------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_of(cfg: NosaConfig):
@@ -406,15 +412,28 @@ def nosa_sparse_attention_noalloc(cfg: NosaConfig, units, block_tab, tail, tail_
 # ---------------------------------------------------------------------------
 # the 8-bit block cache (state and layouts: include/nosa.h)
 # ---------------------------------------------------------------------------
-# These calls are short enough for the binding to count, so each tensor is checked in one
+# These calls are short enough for the binding to count, so a tensor is checked in one
 # expression and the reason for a refusal is looked for afterwards.
 def _arg(t, device, shape, dtype, what, align=4):
     """Pointer of a contiguous tensor of this shape and type on cuda:device."""
-    if (t.get_device() == device and t.dtype is dtype and (shape is None or t.shape == shape)
+    if (t.shape == shape and t.dtype is dtype and t.get_device() == device
             and t.is_contiguous()):
         p = t.data_ptr()
-        if p % align == 0:
+        if not p % align:
             return p
+    return _refuse(t, device, shape, dtype, what, align)
+
+
+def _buffer(t, device, dtype, what, align):
+    """Pointer of a contiguous uint8 tensor of any shape on cuda:device."""
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        p = t.data_ptr()
+        if not p % align:
+            return p
+    return _refuse(t, device, None, dtype, what, align)
+
+
+def _refuse(t, device, shape, dtype, what, align):
     if t.is_cuda and t.get_device() != device:
         raise ValueError(f"{what} is on cuda:{t.get_device()}, the configuration's device is "
                          f"cuda:{device}")
@@ -431,30 +450,22 @@ def _rows(t, device, shape, dtype, what):
     if st[3] != 1:
         raise ValueError(f"{what}: the elements of a row must be consecutive")
     # (a dimension of one element is never stepped along)
-    return (_arg(t[0, 0, 0], device, None, dtype, what, 16),
+    return (_arg(t[0, 0, 0], device, shape[3:], dtype, what, 16),
             (C.c_int64 * 3)(*(s if n > 1 else 0 for s, n in zip(st[:3], shape))))
 
 
-def _cache_args(cfg: NosaConfig, units, block_tab, tail, lens, torch):
+def _cache_args(units, block_tab, tail, lens, device, d, elt, U, blocks, torch):
     """(units, number of units, block_tab, tail, lens) of a cache, checked."""
-    dev, d, U = cfg.device, cfg.head_dim, cfg.batch * cfg.n_kv_heads
-    elt = 4 if cfg.dtype == NOSA_F32 else 2
-    size = (2 * 64 * d + 4 * 64 + 8 + 31) // 32 * 32          # nosa_quant_unit_bytes
-    payload = (2 * 64 * d * elt + 4 * 64 + 255) // 256 * 256  # nosa_payload_bytes
-    n, rest = divmod(units.numel(), size)
-    if rest:
+    u8, i32 = torch.uint8, torch.int32
+    size = (128 * d + 295) // 32 * 32                 # nosa_quant_unit_bytes
+    n = units.numel()
+    if n % size:
         raise ValueError(f"units must hold whole units of {size} bytes")
-    if tail.numel() != U * payload:
+    if tail.numel() != U * ((128 * d * elt + 511) // 256 * 256):  # nosa_payload_bytes
         raise ValueError("tail must hold one block unit per request and KV head")
-    return (_arg(units, dev, None, torch.uint8, "units", 16), n,
-            _arg(block_tab, dev, (U, block_tab.shape[1]), torch.int32, "block_tab"),
-            _arg(tail, dev, None, torch.uint8, "tail", 16),
-            _arg(lens, dev, (U,), torch.int32, "lens"))
-
-
-def _device_stream(device, stream, torch):
-    """The given stream, or the current one of the device."""
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    return (_buffer(units, device, u8, "units", 16), n // size,
+            _arg(block_tab, device, (U, blocks), i32, "block_tab"),
+            _buffer(tail, device, u8, "tail", 16), _arg(lens, device, (U,), i32, "lens"))
 
 
 def nosa_quant_unit_bytes(cfg: NosaConfig) -> int:
@@ -468,19 +479,23 @@ def nosa_quant_append(cfg: NosaConfig, k, v, e, units, block_tab, tail, lens, le
     The new lengths go to lens_out (lens itself by default); n_new [batch] int32 gives the
     valid tokens of each request."""
     torch = _torch()
-    dev, batch = cfg.device, cfg.batch
-    dt, i32 = _dtype_of(cfg), torch.int32
-    shp = (batch, k.shape[1], cfg.n_kv_heads, cfg.head_dim)
+    dev, batch, hkv, d = cfg.device, cfg.batch, cfg.n_kv_heads, cfg.head_dim
+    dt, elt = (torch.float32, 4) if cfg.dtype == NOSA_F32 else (torch.bfloat16, 2)
+    n, blocks, U = k.shape[1], block_tab.shape[1], batch * hkv
+    shp = (batch, n, hkv, d)
     kp, ks = _rows(k, dev, shp, dt, "k")
     vp, vs = _rows(v, dev, shp, dt, "v")
-    up, nu, tab, tl, lp = _cache_args(cfg, units, block_tab, tail, lens, torch)
-    _check(lib.nosa_quant_append(
-        C.byref(cfg), block_tab.shape[1], shp[1], kp, ks, vp, vs,
+    up, nu, tab, tl, lp = _cache_args(units, block_tab, tail, lens, dev, d, elt, U, blocks, torch)
+    st = lib.nosa_quant_append(
+        C.byref(cfg), blocks, n, kp, ks, vp, vs,
         None if e is None else _arg(e, dev, shp[:3], torch.float32, "e"),
-        None if n_new is None else _arg(n_new, dev, (batch,), i32, "n_new"), up, nu, tab, tl, lp,
-        lp if lens_out is None else _arg(lens_out, dev, lens.shape, i32, "lens_out"),
-        None if status is None else _arg(status, dev, (1,), i32, "status"),
-        _device_stream(dev, stream, torch)))
+        None if n_new is None else _arg(n_new, dev, (batch,), torch.int32, "n_new"),
+        up, nu, tab, tl, lp,
+        lp if lens_out is None else _arg(lens_out, dev, (U,), torch.int32, "lens_out"),
+        None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
 
 
 def nosa_quant_attention_workspace_bytes(cfg: NosaConfig, max_blocks: int, n_queries: int = 1,
@@ -495,26 +510,29 @@ def nosa_quant_attention(cfg: NosaConfig, units, block_tab, tail, lens, q, out, 
     cache; writes out (and lse [batch][n][Hq]) and, given mass [U][max_blocks], accumulates the
     blocks' attention weight. Returns the workspace (allocated here when not passed)."""
     torch = _torch()
-    dev = cfg.device
-    dt, i32, f32 = _dtype_of(cfg), torch.int32, torch.float32
-    shp = (cfg.batch, q.shape[1], cfg.n_q_heads, cfg.head_dim)
+    dev, batch, d = cfg.device, cfg.batch, cfg.head_dim
+    dt, elt = (torch.float32, 4) if cfg.dtype == NOSA_F32 else (torch.bfloat16, 2)
+    n, blocks, U = q.shape[1], block_tab.shape[1], batch * cfg.n_kv_heads
+    shp = (batch, n, cfg.n_q_heads, d)
     qp, qs = _rows(q, dev, shp, dt, "q")
-    up, nu, tab, tl, lp = _cache_args(cfg, units, block_tab, tail, lens, torch)
+    up, nu, tab, tl, lp = _cache_args(units, block_tab, tail, lens, dev, d, elt, U, blocks, torch)
     if workspace is None:
         workspace = torch.empty(
-            nosa_quant_attention_workspace_bytes(cfg, block_tab.shape[1], shp[1], mass is not None),
+            nosa_quant_attention_workspace_bytes(cfg, blocks, n, mass is not None),
             dtype=torch.uint8, device=q.device)
         if stream is not None:  # (it may be dropped before that stream has used it)
             workspace.record_stream(torch.cuda.ExternalStream(_stream(stream), device=dev))
-    _check(lib.nosa_quant_attention(
-        C.byref(cfg), block_tab.shape[1], shp[1], up, nu, tab, tl, lp, qp, qs,
-        None if q_len is None else _arg(q_len, dev, (cfg.batch,), i32, "q_len"),
+    st = lib.nosa_quant_attention(
+        C.byref(cfg), blocks, n, up, nu, tab, tl, lp, qp, qs,
+        None if q_len is None else _arg(q_len, dev, (batch,), torch.int32, "q_len"),
         _arg(out, dev, shp, dt, "out", 16),
-        None if lse is None else _arg(lse, dev, shp[:3], f32, "lse"),
-        None if mass is None else _arg(mass, dev, block_tab.shape, f32, "mass"), decay,
-        _arg(workspace, dev, None, torch.uint8, "workspace", 256), workspace.numel(),
-        None if status is None else _arg(status, dev, (1,), i32, "status"),
-        _device_stream(dev, stream, torch)))
+        None if lse is None else _arg(lse, dev, shp[:3], torch.float32, "lse"),
+        None if mass is None else _arg(mass, dev, (U, blocks), torch.float32, "mass"), decay,
+        _buffer(workspace, dev, torch.uint8, "workspace", 256), workspace.numel(),
+        None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
     return workspace
 
 
@@ -523,17 +541,18 @@ def nosa_quant_evict(cfg: NosaConfig, budget, n_recent, block_tab, mass, lens, t
     """Evicts the blocks of least accumulated weight from every unit with more than `budget` full
     blocks (its newest n_recent stay). Works in place unless outputs are given."""
     torch = _torch()
-    dev = cfg.device
-    shp = (cfg.batch * cfg.n_kv_heads, block_tab.shape[1])
-    i32, f32 = torch.int32, torch.float32
+    dev, U, blocks = cfg.device, cfg.batch * cfg.n_kv_heads, block_tab.shape[1]
+    shp, i32, f32 = (U, blocks), torch.int32, torch.float32
     tp = _arg(block_tab, dev, shp, i32, "block_tab")
     mp = _arg(mass, dev, shp, f32, "mass")
-    lp = _arg(lens, dev, shp[:1], i32, "lens")
-    _check(lib.nosa_quant_evict(
-        C.byref(cfg), shp[1], budget, n_recent, tp, mp, lp,
+    lp = _arg(lens, dev, (U,), i32, "lens")
+    st = lib.nosa_quant_evict(
+        C.byref(cfg), blocks, budget, n_recent, tp, mp, lp,
         tp if tab_out is None else _arg(tab_out, dev, shp, i32, "tab_out"),
         mp if mass_out is None else _arg(mass_out, dev, shp, f32, "mass_out"),
-        lp if lens_out is None else _arg(lens_out, dev, shp[:1], i32, "lens_out"),
+        lp if lens_out is None else _arg(lens_out, dev, (U,), i32, "lens_out"),
         None if order is None else _arg(order, dev, shp, i32, "order"),
         None if status is None else _arg(status, dev, (1,), i32, "status"),
-        _device_stream(dev, stream, torch)))
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
