@@ -16,8 +16,8 @@
 //             independent chains of products. Where the CTA leaves a unit the warps
 //             leave their parts to a helper warp, which joins them and has the next
 //             unit's queries ready, and go on.
-//   combine : one CTA per unit (and row tile) attends to the tail in fp32 while the
-//             stream still runs, then joins the unit's parts.
+//   combine : a CTA per unit and 8 rows attends to the tail in fp32 while the stream
+//             still runs, then joins the unit's parts.
 //   weights : with accumulated weights, what the stream noted for each block is added
 //             up relative to the rows' final sums: by the join where one CTA has all
 //             rows of a unit (up to 8), else by a launch of its own.
@@ -33,6 +33,21 @@
 // product, scaled by 2^14 so that weights down to 2^-28 of the largest keep their 11
 // bits. Each slice's product starts from zero and enters the fp32 output with the
 // block's value scale, so neither scale ever multiplies an operand.
+//
+// Measured on GB300 (bytes that the call cannot do without / time, of the measured copy
+// rate of 6793 GB/s):
+//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   671 us   96 %
+//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB   100 us   85 %
+//   8 units x 131071 tokens, 4 rows                       0.27 GB    50 us   81 %
+//   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    31 us   66 %
+//   1 unit x 2031 tokens, d = 64, fp32                    0.3 MB      9 us
+// The stream itself runs at the copy rate; what is left is fixed: 3.75 us until the
+// first unit has landed (lengths, table, unit: three dependent reads), about 4 us between
+// the first and the last CTA to end, 1.5 us for the last join inside a CTA, 3 us for the
+// join launch after it and 2.5 us for the weights'. With 32 rows (8 drafted tokens of
+// 4 heads, 32 units of 8200 tokens: 39 - 43 us; 128 rows over 16 units of 16384: 110 us)
+// the products' instructions bound it: 1460 of a warp and block at 1.7 instructions a
+// cycle, six consumer warps being all that the outputs' registers leave room for.
 #pragma once
 
 #include "k_quant.cuh"
@@ -155,7 +170,10 @@ template <int D, int NT, int RG, bool F32>
 struct QGeom {
   static constexpr int ROWS = 8 * NT * RG, KS = D / 16, UB = quant_unit_bytes(D);
   // Eight warps in all leave each one 255 registers, which 16 rows of output need; more
-  // leave 168.
+  // leave 168. Slots and ring for 8 rows, d = 128, measured at 256 units x 65536 tokens, us:
+  // 4 slots and 8 stages 677, 3 and 9 671, 5 and 10 694, 3 and 6 721, 6 and 6 745, 2 and 8
+  // 907 (two warps cannot keep up); the first leaves shared memory for the join's CTAs to
+  // wait on the same SMs. d = 64 (64 units x 16384), 8 and 16 33.6, 4 and 16 33.9, 8 and 8 41.
   static constexpr int IS = NT == 2 ? 6 / RG : RG > 1 ? 8 / RG : D == 128 ? 4 : 8;
   static constexpr int W = IS * RG;             // consumer warps; a producer and a helper come on top
   static constexpr int THREADS = 32 * (W + 2);
