@@ -8,7 +8,7 @@ int quant_sm_count() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 1;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
   if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }

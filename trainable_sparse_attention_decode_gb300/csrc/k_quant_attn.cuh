@@ -36,18 +36,18 @@
 //
 // Measured on GB300 (bytes that the call cannot do without / time, of the measured copy
 // rate of 6793 GB/s):
-//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   671 us   96 %
+//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   669 us   96 %
 //   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB   100 us   85 %
-//   8 units x 131071 tokens, 4 rows                       0.27 GB    50 us   81 %
-//   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    31 us   66 %
+//   8 units x 131071 tokens, 4 rows                       0.27 GB    49 us   81 %
+//   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    31 us   67 %
 //   1 unit x 2031 tokens, d = 64, fp32                    0.3 MB      9 us
 // The stream itself runs at the copy rate; what is left is fixed: 3.75 us until the
 // first unit has landed (lengths, table, unit: three dependent reads), about 4 us between
 // the first and the last CTA to end, 1.5 us for the last join inside a CTA, 3 us for the
 // join launch after it and 2.5 us for the weights'. With 32 rows (8 drafted tokens of
-// 4 heads, 32 units of 8200 tokens: 39 - 43 us; 128 rows over 16 units of 16384: 110 us)
-// the products' instructions bound it: 1460 of a warp and block at 1.7 instructions a
-// cycle, six consumer warps being all that the outputs' registers leave room for.
+// 4 heads, 32 units of 8200 tokens: 39 - 43 us; 128 rows over 16 units of 16384: 105 us)
+// the products' instructions bound it: about 1300 of a warp and block at 1.7 a cycle, six
+// consumer warps being all that the outputs' registers leave room for.
 #pragma once
 
 #include "k_quant.cuh"
@@ -106,6 +106,11 @@ __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0
 // exp(x - m) for the base-2 exponential; x = -inf gives 0 for every finite m.
 __device__ __forceinline__ float exp_from(float x, float m) { return exp2f((x - m) * kQLog2e); }
 
+__device__ __forceinline__ float ex2(float x) {  // results below 2^-126 are 0
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
   uint32_t r;
   asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(w));
@@ -593,6 +598,9 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
           }
         }
         // ---- softmax over the 16 SL tokens ----
+        // (Warp-wide branches around the masks or the rescaling, and packed pairs, were all
+        // slower: they keep the next products' loads from moving up. 256 units x 65536
+        // tokens, us: as it is 669, masks behind a branch 675, packed 723.)
         float ev[SL][2];
 #pragma unroll
         for (int w = 0; w < SL; ++w) {
@@ -631,9 +639,13 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 float& l = sc[nt][w][2 * y + x];
-                l = exp_from(l, mu);
+                // times 2^14: for bf16 in the exponent, which costs 2^-21.5 of a weight
+                if constexpr (F32) {
+                  l = ex2((l - mu) * kQLog2e) * 16384.f;
+                } else {
+                  l = ex2(fmaf(l - mu, kQLog2e, 14.f));
+                }
                 sum += l;
-                l *= 16384.f;
               }
             l_run[nt][x] = l_run[nt][x] * corr[nt][x] + sum;
             blk_l[nt][x] = blk_l[nt][x] * corr[nt][x] + sum;
@@ -696,6 +708,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
             t[x] += __shfl_xor_sync(0xffffffffu, t[x], 4);
             t[x] += __shfl_xor_sync(0xffffffffu, t[x], 8);
             t[x] += __shfl_xor_sync(0xffffffffu, t[x], 16);
+            t[x] *= 0x1p-14f;
           }
           const int r = rg * WR + nt * 8 + 2 * c;
           if (g == 0 && seg.tile * ROWS + r < p.T * p.G)
@@ -716,6 +729,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
+        l *= 0x1p-14f;
         if (g == 0) ml[nt * 8 + 2 * c + x] = make_float2(m_run[nt][x], l);
       }
 #pragma unroll
