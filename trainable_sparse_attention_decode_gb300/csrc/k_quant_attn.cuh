@@ -36,16 +36,16 @@
 //
 // Measured on GB300 (bytes that the call cannot do without / time, of the measured copy
 // rate of 6793 GB/s):
-//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   669 us   96 %
-//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB   100 us   85 %
-//   8 units x 131071 tokens, 4 rows                       0.27 GB    49 us   81 %
-//   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    31 us   67 %
+//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   661 us   97 %
+//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB    99 us   86 %
+//   8 units x 131071 tokens, 4 rows                       0.27 GB    49 us   82 %
+//   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    30 us   67 %
 //   1 unit x 2031 tokens, d = 64, fp32                    0.3 MB      9 us
 // The stream itself runs at the copy rate; what is left is fixed: 3.75 us until the
 // first unit has landed (lengths, table, unit: three dependent reads), about 4 us between
 // the first and the last CTA to end, 1.5 us for the last join inside a CTA, 3 us for the
 // join launch after it and 2.5 us for the weights'. With 32 rows (8 drafted tokens of
-// 4 heads, 32 units of 8200 tokens: 39 - 43 us; 128 rows over 16 units of 16384: 105 us)
+// 4 heads, 32 units of 8200 tokens: 40 us; 128 rows over 16 units of 16384 tokens: 98 us)
 // the products' instructions bound it: about 1300 of a warp and block at 1.7 a cycle, six
 // consumer warps being all that the outputs' registers leave room for.
 #pragma once
@@ -184,17 +184,17 @@ struct QGeom {
   static constexpr int THREADS = 32 * (W + 2);
   static constexpr int STAGES = D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 8 : 9;
   static constexpr int SL = 4;                  // slices of a block that a warp takes at once
-  static constexpr int NB = NT * RG == 1 ? 2 : 1;  // buffers for queries and for parts
+  static constexpr int NQ = 2, ND = NT * RG == 1 ? 2 : 1;  // buffers for queries and for the warps' parts
   static constexpr int RP = D + 4;              // padded row of a part
   static constexpr int Q_BYTES = NT * RG * KS * 32 * (F32 ? 16 : 8);
   static constexpr int RED_BYTES = W * 8 * NT * RP * 4, ML_BYTES = W * 8 * NT * 8;
   static constexpr int Q_OFF = STAGES * UB;
-  static constexpr int RED_OFF = Q_OFF + NB * Q_BYTES;
-  static constexpr int ML_OFF = RED_OFF + NB * RED_BYTES;
-  static constexpr int ROW_OFF = ML_OFF + NB * ML_BYTES;
-  static constexpr int NULL_OFF = ROW_OFF + NB * ROWS * 8;
+  static constexpr int RED_OFF = Q_OFF + NQ * Q_BYTES;
+  static constexpr int ML_OFF = RED_OFF + ND * RED_BYTES;
+  static constexpr int ROW_OFF = ML_OFF + ND * ML_BYTES;
+  static constexpr int NULL_OFF = ROW_OFF + NQ * ROWS * 8;
   static constexpr int BAR_OFF = NULL_OFF + (STAGES * 4 + 7) / 8 * 8;
-  static constexpr int SMEM = BAR_OFF + (2 * STAGES + 3 * NB) * 8;
+  static constexpr int SMEM = BAR_OFF + (2 * STAGES + NQ + 2 * ND) * 8;
   static_assert(STAGES % IS == 0 && STAGES <= 32, "a stage has one slot and one producer lane");
   static_assert(UB % 16 == 0 && Q_OFF % 16 == 0 && RED_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
   static_assert(SMEM <= 227 * 1024 - 256, "shared memory");
@@ -300,20 +300,20 @@ template <int D, int NT, int RG, bool F32>
 __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_stream_kernel(QStreamParams p) {
   using Gm = QGeom<D, NT, RG, F32>;
   constexpr int KS = Gm::KS, ROWS = Gm::ROWS, STAGES = Gm::STAGES, UB = Gm::UB, SL = Gm::SL, W = Gm::W, IS = Gm::IS;
-  constexpr int NB = Gm::NB, WR = 8 * NT, kThreads = Gm::THREADS;
+  constexpr int NQ = Gm::NQ, ND = Gm::ND, WR = 8 * NT, kThreads = Gm::THREADS;
   extern __shared__ __align__(128) uint8_t smem[];
   int* null_s = reinterpret_cast<int*>(smem + Gm::NULL_OFF);  // [STAGES] the table names no unit
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Gm::BAR_OFF);
   uint64_t* empty = full + STAGES;
-  uint64_t* q_full = empty + STAGES;    // [NB] queries of a segment are there
-  uint64_t* dump_full = q_full + NB;    // [NB] the warps' parts of a segment are there
-  uint64_t* dump_free = dump_full + NB;
+  uint64_t* q_full = empty + STAGES;    // [NQ] queries of a segment are there
+  uint64_t* dump_full = q_full + NQ;    // [ND] the warps' parts of a segment are there
+  uint64_t* dump_free = dump_full + ND;
   // per buffer: queries, factors of the rows' logits, tokens they see, parts
-  auto q_of = [&](int k) { return smem + Gm::Q_OFF + (k % NB) * Gm::Q_BYTES; };
-  auto rs_of = [&](int k) { return reinterpret_cast<float*>(smem + Gm::ROW_OFF) + (k % NB) * 2 * ROWS; };
+  auto q_of = [&](int k) { return smem + Gm::Q_OFF + (k % NQ) * Gm::Q_BYTES; };
+  auto rs_of = [&](int k) { return reinterpret_cast<float*>(smem + Gm::ROW_OFF) + (k % NQ) * 2 * ROWS; };
   auto vis_of = [&](int k) { return reinterpret_cast<int*>(rs_of(k) + ROWS); };
-  auto red_of = [&](int k) { return reinterpret_cast<float*>(smem + Gm::RED_OFF + (k % NB) * Gm::RED_BYTES); };  // [W][WR][RP]
-  auto ml_of = [&](int k) { return reinterpret_cast<float2*>(smem + Gm::ML_OFF + (k % NB) * Gm::ML_BYTES); };    // [W][WR]
+  auto red_of = [&](int k) { return reinterpret_cast<float*>(smem + Gm::RED_OFF + (k % ND) * Gm::RED_BYTES); };  // [W][WR][RP]
+  auto ml_of = [&](int k) { return reinterpret_cast<float2*>(smem + Gm::ML_OFF + (k % ND) * Gm::ML_BYTES); };    // [W][WR]
   __shared__ long long s_scan[kThreads / 32];
   __shared__ long long s_before;
   __shared__ int s_unit;
@@ -325,8 +325,8 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], RG);
     }
-    for (int s = 0; s < NB; ++s) {
-      mbar_init(&q_full[s], 1);
+    for (int s = 0; s < NQ; ++s) mbar_init(&q_full[s], 1);
+    for (int s = 0; s < ND; ++s) {
       mbar_init(&dump_full[s], W);
       mbar_init(&dump_free[s], 1);
     }
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
   if (warp == W + 1) {
     // ---- helper: prepares the queries of coming segments, joins the warps' parts ----
     QWalk ahead(p, s_unit, g0 - s_before, items, lane);
-    long long slot[NB];
+    long long slot[NQ];
     int prepared = 0;
     auto prepare = [&]() {
       const int b = ahead.u / p.Hkv, qn = quant_count(p.q_len, b, p.T, p.status, lane == 0);
@@ -448,22 +448,22 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
         qa_queries<D, GR, F32>(p, ahead.u, ahead.tile * ROWS + r, ahead.tokens, qn, q_of(prepared) + r * KS * 4 * (F32 ? 16 : 8),
                                rs_of(prepared) + r, vis_of(prepared) + r, lane);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[prepared % NB]);
+      if (lane == 0) mbar_arrive(&q_full[prepared % NQ]);
 #pragma unroll
-      for (int x = 0; x < NB; ++x)
-        if (x == prepared % NB) slot[x] = cta + ahead.vu();
+      for (int x = 0; x < NQ; ++x)
+        if (x == prepared % NQ) slot[x] = cta + ahead.vu();
       ++prepared;
       ahead.next();
     };
-    for (int x = 0; x < NB && ahead.more(); ++x) prepare();
+    for (int x = 0; x < NQ && ahead.more(); ++x) prepare();
     for (int k = 0; k < prepared && ok; ++k) {
-      if (!(ok = wait(&dump_full[k % NB], k / NB))) break;
+      if (!(ok = wait(&dump_full[k % ND], k / ND))) break;
       const float* red = red_of(k);
       const float2* ml = ml_of(k);
       long long to = slot[0];
 #pragma unroll
-      for (int x = 1; x < NB; ++x)
-        if (x == k % NB) to = slot[x];
+      for (int x = 1; x < NQ; ++x)
+        if (x == k % NQ) to = slot[x];
 #pragma unroll 4
       for (int r = 0; r < ROWS; ++r) {
         const int w0 = r / WR * IS, rr = r % WR;  // the warps of this row, and their row
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
         if (lane == 0) p.part_ml[to * ROWS + r] = make_float2(M, L);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&dump_free[k % NB]);
+      if (lane == 0) mbar_arrive(&dump_free[k % ND]);
       if (ahead.more()) prepare();  // (every warp has left segment k, whose queries were in this buffer)
     }
     if (!ok && lane == 0) {
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
   QWalk seg(p, s_unit, g0 - s_before, items, lane);
   int it0 = 0;  // first item of the segment
   for (int k = 0; seg.more(); ++k, it0 += seg.cnt, seg.next()) {
-    if (!(ok = wait(&q_full[k % NB], k / NB))) break;
+    if (!(ok = wait(&q_full[k % NQ], k / NQ))) break;
     const long long vu = seg.vu();
     const uint8_t* q_s = q_of(k) + rg * NT * KS * 32 * (F32 ? 16 : 8);
     const float* rs_s = rs_of(k) + rg * WR;
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
       }
     }
     // ---- the warp's part of the segment goes to the helper ----
-    if (ok && k >= NB) ok = wait(&dump_free[k % NB], k / NB - 1);
+    if (ok && k >= ND) ok = wait(&dump_free[k % ND], k / ND - 1);
     if (!ok) break;
     float* red = red_of(k) + warp * WR * Gm::RP;
     float2* ml = ml_of(k) + warp * WR;
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
         for (int x = 0; x < 4; ++x) red[(nt * 8 + 2 * c + (x & 1)) * Gm::RP + mt * 16 + g + 8 * (x >> 1)] = o[nt][mt][x];
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&dump_full[k % NB]);
+    if (lane == 0) mbar_arrive(&dump_full[k % ND]);
   }
   if (!ok && lane == 0) {
     s_bad = 1;
@@ -1089,8 +1089,9 @@ cudaError_t stream_launches(const Shape& s, const QPlan& pl, const QStreamParams
   constexpr bool F32 = sizeof(T) == 4;
   // 16 and 32 rows as row groups of 8, which convert the codes once each but leave
   // registers enough for eight consumer warps; 32 rows of bf16 as two groups of 16 on
-  // six. Measured at 4 requests x 8 KV heads x 16384 tokens, d = 128, us: 16 rows 39
-  // (one group of 16: 44), fp32 47 (59); 32 rows 62 (two groups of 16: 60), fp32 78 (89).
+  // six. Measured when they were chosen, at 4 requests x 8 KV heads x 16384 tokens of
+  // d = 128, us: 16 rows 39 (one group of 16: 44), fp32 47 (59); 32 rows 62 (two groups
+  // of 16: 60), fp32 78 (89). With the next unit's queries ready ahead: 36, 41, 53, 69.
   cudaError_t e;
   if (pl.rows == 8)
     e = stream_variant<D, 1, 1, F32>(pl, p, stream);
