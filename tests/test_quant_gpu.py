@@ -822,3 +822,50 @@ def test_tensors_elsewhere_are_refused():
         nosa.nosa_quant_attention(cfg, units, tab, tail, lens, q, torch.empty_like(q))
     with pytest.raises(ValueError, match="device"):
         nosa.nosa_quant_append(cfg, q[:, :, :1], q[:, :, :1], None, units, tab, tail, lens)
+
+
+def test_binding_refusals():
+    """Wrong types, shapes, strides, sizes and alignments are refused before anything runs."""
+    cfg = config(2, 4, 2, 64, "bf16")
+    U, cap, bf = 4, 3, torch.bfloat16
+    z = lambda *shape, dtype=torch.float32: torch.zeros(*shape, dtype=dtype, device="cuda")  # noqa: E731
+    units, tab = z(6, Q.unit_bytes(64), dtype=torch.uint8), z(U, cap, dtype=torch.int32)
+    tail, lens = z(U * nosa.nosa_payload_bytes(cfg), dtype=torch.uint8), z(U, dtype=torch.int32)
+    k, q, mass = z(2, 5, 2, 64, dtype=bf), z(2, 5, 4, 64, dtype=bf), z(U, cap)
+    out = torch.empty_like(q)
+    ws = z(nosa.nosa_quant_attention_workspace_bytes(cfg, cap, 5, True), dtype=torch.uint8)
+
+    def append(k=k, v=k, e=None, units=units, tab=tab, tail=tail, lens=lens, **kw):
+        nosa.nosa_quant_append(cfg, k, v, e, units, tab, tail, lens, **kw)
+
+    def attention(units=units, tab=tab, tail=tail, lens=lens, q=q, out=out, workspace=ws, **kw):
+        nosa.nosa_quant_attention(cfg, units, tab, tail, lens, q, out, workspace=workspace, **kw)
+
+    def evict(tab=tab, mass=mass, lens=lens, budget=2, recent=1, **kw):
+        nosa.nosa_quant_evict(cfg, budget, recent, tab, mass, lens, **kw)
+
+    wide = z(2, 5, 2, 72, dtype=bf)
+    bad = [
+        lambda: append(k=k.float()), lambda: append(k=k[:, :, :1]), lambda: append(v=k[:, :4]),
+        lambda: append(k=z(2, 5, 64, 2, dtype=bf).transpose(2, 3)), lambda: append(k=wide[..., 1:65]),
+        lambda: append(k=z(2, 5, 2, 68, dtype=bf)[..., :64]), lambda: append(e=z(2, 5, 4)), lambda: append(e=k[..., 0]),
+        lambda: append(units=units.view(-1)[1:]), lambda: append(units=units.view(-1)[:100]),
+        lambda: append(tail=tail[:-256]), lambda: append(lens=lens[:2]), lambda: append(lens=lens.float()),
+        lambda: append(tab=tab.long()), lambda: append(tab=tab[:2]), lambda: append(lens_out=z(U)),
+        lambda: append(n_new=z(3, dtype=torch.int32)), lambda: append(status=z(2, dtype=torch.int32)),
+        lambda: attention(q=q.float()), lambda: attention(q=z(2, 129, 4, 64, dtype=bf)), lambda: attention(out=out[:, :4]),
+        lambda: attention(out=z(2, 5, 8, 64, dtype=bf)[:, :, ::2]), lambda: attention(out=q), lambda: attention(lse=z(2, 5, 2)),
+        lambda: attention(mass=z(U, cap + 1)), lambda: attention(mass=mass, decay=2.0), lambda: attention(mass=mass, workspace=ws[:-256]),
+        lambda: attention(workspace=ws[16:]), lambda: attention(q_len=z(3, dtype=torch.int32)),
+        lambda: attention(tail=tail.float()), lambda: evict(mass=mass.double()), lambda: evict(mass=mass[:, :2]),
+        lambda: evict(budget=0, recent=0), lambda: evict(recent=3), lambda: evict(order=z(U, cap)),
+        lambda: evict(tab_out=z(U, cap + 1, dtype=torch.int32)), lambda: evict(lens_out=z(U + 1, dtype=torch.int32))]
+    for i, f in enumerate(bad):
+        with pytest.raises((ValueError, nosa.NosaError)):
+            f()
+            print("not refused:", i)
+    attention(mass=mass, lse=z(2, 5, 4))  # and what they vary from is accepted
+    append()
+    evict()
+    torch.cuda.synchronize()
+    assert lens.tolist() == [5] * U and not out.any()

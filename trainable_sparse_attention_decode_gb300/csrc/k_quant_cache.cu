@@ -295,7 +295,7 @@ cudaError_t append_variant(const Shape& s, const QAppendArgs& a, cudaStream_t st
   if (a.n <= kQB) {
     return launch_dependent(quant_tail_kernel<T, D, true>, dim3(s.U), kAppendThreads, 0, stream, a, s.Hkv, s.payload);
   } else {
-    const int most = std::min((a.n + kQB - 1) / kQB, a.max_blocks);
+    const int most = (int)std::min<long long>((a.n + kQB - 1LL) / kQB, a.max_blocks);
     const cudaError_t e =
         launch_dependent(quant_blocks_kernel<T, D>, dim3(s.U, most), kAppendThreads, 0, stream, a, s.Hkv, s.payload);
     if (e != cudaSuccess) return e;

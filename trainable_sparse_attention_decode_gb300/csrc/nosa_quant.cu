@@ -61,6 +61,7 @@ nosa_status take_strides(const char* name, const int64_t* st, int n, int heads, 
 
 nosa_status launched(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return NOSA_OK;
+  cudaGetLastError();  // (reported here)
   return refuse(NOSA_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
 }
 
