@@ -36,11 +36,11 @@
 //
 // Measured on GB300 (bytes that the call cannot do without / time, of the measured copy
 // rate of 6793 GB/s):
-//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   661 us   97 %
-//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB    99 us   86 %
+//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   669 us   96 %
+//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB   100 us   85 %
 //   8 units x 131071 tokens, 4 rows                       0.27 GB    49 us   82 %
-//   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    30 us   67 %
-//   1 unit x 2031 tokens, d = 64, fp32                    0.3 MB      9 us
+//   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    30 us   68 %
+//   1 unit x 2031 tokens, d = 64, fp32                    0.3 MB    8.4 us
 // The stream itself runs at the copy rate; what is left is fixed: 3.75 us until the
 // first unit has landed (lengths, table, unit: three dependent reads), about 4 us between
 // the first and the last CTA to end, 1.5 us for the last join inside a CTA, 3 us for the
@@ -378,6 +378,42 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
     return __all_sync(0xffffffffu, s_bad == 0 && mbar_wait_bounded(bar, (uint32_t)(phase & 1)));
   };
 
+  // Whether the consumers join their last segment's rows with the helper. Measured on
+  // GB300, us (helper alone): d = 64, 1 unit x 2031 tokens in fp32 8.3 (9.0), 64 units x 16384
+  // 29.9 (30.6), 32 rows 36 (37.5); d = 128, 32 rows over 32 units of 8200 42.2 (40.0): there
+  // the join's registers disturb the main loop.
+  constexpr bool kShareJoin = D == 64;
+  // Rows first, first + step, ... of segment k: the warps' parts become the CTA's, in slot `to`.
+  auto join_rows = [&](int k, long long to, int first, int step) {
+    const float* red = red_of(k);
+    const float2* ml = ml_of(k);
+#pragma unroll 4
+    for (int r = first; r < ROWS; r += step) {
+      const int w0 = r / WR * IS, rr = r % WR;  // the warps of this row, and their row
+      float M = ml[w0 * WR + rr].x;
+#pragma unroll
+      for (int w = 1; w < IS; ++w) M = max_nan(M, ml[(w0 + w) * WR + rr].x);
+      const float mu = finite_max(M);
+      float wt[IS], L = 0.f;
+#pragma unroll
+      for (int w = 0; w < IS; ++w) {
+        const float2 y = ml[(w0 + w) * WR + rr];
+        wt[w] = exp_from(y.x, mu);
+        L += wt[w] * y.y;
+      }
+      if (lane < D / 4) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < IS; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(red + ((w0 + w) * WR + rr) * Gm::RP + 4 * lane);
+          acc.x += wt[w] * y.x; acc.y += wt[w] * y.y; acc.z += wt[w] * y.z; acc.w += wt[w] * y.w;
+        }
+        reinterpret_cast<float4*>(p.part_acc + (to * ROWS + r) * D)[lane] = acc;
+      }
+      if (lane == 0) p.part_ml[to * ROWS + r] = make_float2(M, L);
+    }
+  };
+
   if (warp == W) {
     // ---- producer: lane s owns stage s and brings it items s, s + STAGES, ... ----
     int it = lane, u = s_unit, tile = 0, j = 0, nb = 0, idx = -1;
@@ -458,37 +494,13 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
     for (int x = 0; x < NQ && ahead.more(); ++x) prepare();
     for (int k = 0; k < prepared && ok; ++k) {
       if (!(ok = wait(&dump_full[k % ND], k / ND))) break;
-      const float* red = red_of(k);
-      const float2* ml = ml_of(k);
       long long to = slot[0];
 #pragma unroll
       for (int x = 1; x < NQ; ++x)
         if (x == k % NQ) to = slot[x];
-#pragma unroll 4
-      for (int r = 0; r < ROWS; ++r) {
-        const int w0 = r / WR * IS, rr = r % WR;  // the warps of this row, and their row
-        float M = ml[w0 * WR + rr].x;
-#pragma unroll
-        for (int w = 1; w < IS; ++w) M = max_nan(M, ml[(w0 + w) * WR + rr].x);
-        const float mu = finite_max(M);
-        float wt[IS], L = 0.f;
-#pragma unroll
-        for (int w = 0; w < IS; ++w) {
-          const float2 y = ml[(w0 + w) * WR + rr];
-          wt[w] = exp_from(y.x, mu);
-          L += wt[w] * y.y;
-        }
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (lane < D / 4) {
-#pragma unroll
-          for (int w = 0; w < IS; ++w) {
-            const float4 y = *reinterpret_cast<const float4*>(red + ((w0 + w) * WR + rr) * Gm::RP + 4 * lane);
-            acc.x += wt[w] * y.x; acc.y += wt[w] * y.y; acc.z += wt[w] * y.z; acc.w += wt[w] * y.w;
-          }
-          reinterpret_cast<float4*>(p.part_acc + (to * ROWS + r) * D)[lane] = acc;
-        }
-        if (lane == 0) p.part_ml[to * ROWS + r] = make_float2(M, L);
-      }
+      // (the last segment's consumers have nothing else to do and take most of its rows)
+      const bool last = kShareJoin && k == prepared - 1 && !ahead.more();
+      join_rows(k, to, last ? W : 0, last ? W + 1 : 1);
       __syncwarp();
       if (lane == 0) mbar_arrive(&dump_free[k % ND]);
       if (ahead.more()) prepare();  // (every warp has left segment k, whose queries were in this buffer)
@@ -739,6 +751,10 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&dump_full[k % ND]);
+    if (kShareJoin && seg.left == seg.cnt) {  // the last segment (its buffer's earlier fills have been joined)
+      if (!(ok = wait(&dump_full[k % ND], k / ND))) break;
+      join_rows(k, cta + vu, warp, W + 1);
+    }
   }
   if (!ok && lane == 0) {
     s_bad = 1;
