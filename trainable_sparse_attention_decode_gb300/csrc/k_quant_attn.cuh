@@ -39,8 +39,8 @@
 //   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   669 us   96 %
 //   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB   100 us   85 %
 //   8 units x 131071 tokens, 4 rows                       0.27 GB    49 us   82 %
-//   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    30 us   68 %
-//   1 unit x 2031 tokens, d = 64, fp32                    0.3 MB    8.4 us
+//   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    30 us   69 %
+//   1 unit x 2031 tokens, d = 64, fp32                    0.3 MB    8.0 us
 // The stream itself runs at the copy rate; what is left is fixed: 3.75 us until the
 // first unit has landed (lengths, table, unit: three dependent reads), about 4 us between
 // the first and the last CTA to end, 1.5 us for the last join inside a CTA, 3 us for the
@@ -766,18 +766,27 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::THREADS, 1) quant_strea
 // ---------------------------------------------------------------------------
 // Tail attention and the join. Grid (units x tiles, row groups of 8, z): a CTA writes
 // d / z dims of 8 rows. Before the stream has finished: the tail in fp32, its keys and
-// values in registers from one round of loads. After: every thread merges its share
+// values in registers. After: every thread merges its share
 // of the unit's parts for four dims of a row, the shares join in shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kQcRows = 8;
+// The CTA has to fit beside a stream CTA, or it starts when that has ended and the tail
+// is waited for. A stream CTA of d = 64 has ten warps, three of them on two of the SM's
+// four schedulers, which leaves 48 registers a thread here (40 where the stream's are
+// fp32): the values are then loaded after the keys are done with. Measured on GB300, us
+// (64 registers): 32 units x 1000 tokens 10.0 (14.3), 128 x 3000 17.3 (21.8), fp32 8 x 3000
+// 9.2 (15.0). At d = 128 there is room for 80
+// beside a bf16 stream, and the values come along with the keys.
+template <typename T, int D> constexpr int kQcPerSm = D == 64 ? (sizeof(T) == 4 ? 6 : 5) : 3;
 constexpr int kQcScan = 4;  // lengths of a thread
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams p, int rows, bool weights) {
+__global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kernel(QStreamParams p, int rows, bool weights) {
   constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE;
   constexpr int KC = NCH / 4;                        // 16-byte key chunks of a thread: token tid % 64
   constexpr int TG = kQcThreads / NCH, TPT = kQB / TG;  // value tokens: TPT of one 16-byte column
   constexpr int CPW = 32 / TG;                       // columns of a warp; its lanes: token group x column
+  constexpr bool kLate = D == 64;                    // values after the keys (fewer registers)
   __shared__ __align__(16) float q_s[kQcRows * D];
   __shared__ __align__(16) float o_s[kQcRows * D];   // the tail's output
   __shared__ float pd_s[4][kQcRows][kQB];            // partial logits
@@ -800,14 +809,18 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
     const uint8_t* tail = p.tail + (long long)u * p.payload;
     const int t = tid % kQB, cg = tid / kQB;
     const int col = warp * CPW + lane % CPW, t0 = lane / CPW * TPT;
-    uint4 kr[KC], vr[TPT];
+    uint4 kr[KC];
 #pragma unroll
     for (int i = 0; i < KC; ++i)
       kr[i] = t < nt ? *reinterpret_cast<const uint4*>(tail + ((size_t)(cg * KC + i) * kQB + t) * 16) : make_uint4(0, 0, 0, 0);
+    uint4 vr[TPT];
+    auto load_values = [&]() {
 #pragma unroll
-    for (int i = 0; i < TPT; ++i)
-      vr[i] = t0 + i < nt ? *reinterpret_cast<const uint4*>(tail + (size_t)kQB * D * ELT + (size_t)(t0 + i) * D * ELT + col * 16)
-                          : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < TPT; ++i)
+        vr[i] = t0 + i < nt ? *reinterpret_cast<const uint4*>(tail + (size_t)kQB * D * ELT + (size_t)(t0 + i) * D * ELT + col * 16)
+                            : make_uint4(0, 0, 0, 0);
+    };
+    if (!kLate) load_values();
     const float* es = reinterpret_cast<const float*>(tail + 2 * (size_t)kQB * D * ELT);
     const float e0 = lane < nt ? es[lane] : -INFINITY, e1 = lane + 32 < nt ? es[lane + 32] : -INFINITY;
     for (int i = tid; i < live * NCH; i += kQcThreads) {
@@ -860,6 +873,7 @@ __global__ void __launch_bounds__(kQcThreads) quant_combine_kernel(QStreamParams
       }
     }
     __syncthreads();
+    if (kLate) load_values();
 #pragma unroll 1
     for (int r = 0; r < live; ++r) {
       float acc[CE];
