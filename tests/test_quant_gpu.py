@@ -869,3 +869,58 @@ def test_binding_refusals():
     evict()
     torch.cuda.synchronize()
     assert lens.tolist() == [5] * U and not out.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 3, 8])
+def test_attention_masked_codes(dtype, d, T):
+    """Masked tokens of a block hold the codes that are no numbers: one token, several of every slice,
+    and all of a block contribute nothing. 4, 12 and 32 rows take every shape of tile."""
+    rng = np.random.default_rng(31 + T)
+    c = Cache(rng, dtype, 3, 4, 1, d, [64 * 5 + 9, 64 * 3, 64 * 40 + 1], masked=0.0)
+    ko, vo = Q.code_offsets(d)
+    gone = {c.tab[0, 1]: [17], c.tab[0, 4]: [0, 5, 10, 15, 18, 35, 52, 63], c.tab[1, 0]: list(range(B)),
+            c.tab[1, 2]: list(range(1, B)), c.tab[2, 39]: [62, 63]}
+    for i, tokens in gone.items():
+        c.images[i, 2 * B * d:2 * B * d + 4 * B].view(np.float32)[tokens] = -np.inf
+        for n, t in enumerate(tokens):
+            c.images[i, vo[t]] = 0x7F if n % 2 else 0xFF
+            c.images[i, ko[t]] = 0xFF if n % 3 else 0x7F
+    c.upload()
+    q = query(rng, 3, T, 4, d, dtype)
+    m0 = rng.random(size=c.tab.shape).astype(np.float32)
+    for _ in range(2):
+        mass = dev(m0)
+        out, lse, status = c.run(q, mass=mass)
+        assert status == 0
+        c.check(q, out, lse, mass0=m0, mass=f64(mass))
+    assert torch.equal(c.units, dev(c.images))  # the cache itself keeps its bytes
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,T", [(4, 2), (1, 70)])
+def test_attention_codes_that_are_no_numbers(dtype, hq, T):
+    """A value code that is no number in a token that is not masked reaches the rows that see that token,
+    in its dim, and no others."""
+    rng = np.random.default_rng(33)
+    d, n = 64, 192
+    c = Cache(rng, dtype, 1, hq, 1, d, [n], masked=0.0)
+    _, vo = Q.code_offsets(d)
+    last = c.tab[0, 2]
+    if T == 2:  # the first query sees masked tokens of the last block only
+        c.images[last, 2 * B * d:2 * B * d + 4 * B].view(np.float32)[:63] = -np.inf
+    c.images[last, vo[63, 7]] = 0x7F
+    c.upload()
+    q = query(rng, 1, T, hq, d, dtype)
+    out, lse, status = c.run(q)
+    assert status == 0 and not torch.isnan(lse).any()
+    sees = n - T + 1 + np.arange(T)
+    reached = sees == n
+    nan = torch.isnan(out[0]).cpu().numpy()  # [T][hq][d]
+    assert nan[reached][:, :, 7].all() and not nan[~reached].any() and not np.delete(nan, 7, axis=2).any()
+    K, V, e = c.tokens(0)
+    for t in np.flatnonzero(~reached):  # and those rows are right
+        want, wl, _, A, S = Q.attend(f64(q)[0, t], K, np.nan_to_num(V), e, np.full(hq, sees[t]))
+        assert np.all(np.abs(f64(out)[0, t] - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -10 + 2.0 ** -16 * S[:, None]) * A)
+        assert np.all(np.abs(f64(lse)[0, t] - wl) <= 2.0 ** -18 * S + 2.0 ** -18 * (1 + np.abs(wl)))
