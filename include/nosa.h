@@ -538,7 +538,9 @@ nosa_status nosa_quant_append(const nosa_config* cfg, int32_t max_blocks, int32_
  * lens - q_len[b] + t + 1 tokens of its unit. Logits are q.k / sqrt(d) + e; a token
  * with e = -inf is masked and contributes nothing whatever its key and value hold.
  * A row that sees no token gives out = 0, lse = -inf. Sums and the softmax are held
- * in fp32, the products take 11-bit (bf16) or 22-bit (fp32) operands.
+ * in fp32. The products take queries exactly (bf16) or with 22 bits (fp32), but for at
+ * most 2^-39 of the largest element of a row, and the softmax's weights with 11 bits
+ * (bf16) or 22 (fp32), but for at most 2^-39 of the largest weight of a row.
  *   q    : device [batch][n_queries][n_q_heads][head_dim] of cfg dtype
  *   out  : the same shape, contiguous (written; rows past q_len[b] are left); it must
  *          not overlap q

@@ -924,3 +924,48 @@ def test_attention_codes_that_are_no_numbers(dtype, hq, T):
         want, wl, _, A, S = Q.attend(f64(q)[0, t], K, np.nan_to_num(V), e, np.full(hq, sees[t]))
         assert np.all(np.abs(f64(out)[0, t] - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -10 + 2.0 ** -16 * S[:, None]) * A)
         assert np.all(np.abs(f64(lse)[0, t] - wl) <= 2.0 ** -18 * S + 2.0 ** -18 * (1 + np.abs(wl)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 3, 8])
+@pytest.mark.parametrize("outlier", [300.0, 30000.0])
+def test_attention_queries_with_an_outlier(dtype, d, T, outlier):
+    """One element of a query is far larger than the others and meets keys of zero: the others keep
+    their bits. An element is held to 2^-22 of itself (bf16: exactly) or to 2^-39 of the row's largest,
+    which for an outlier of 2^15 is 2^-24: summed over 128 dims of keys of about 1, over sqrt(d), below
+    2^-20, a hundredth of the 2^-18 S (S about 10) that the check allows a logit."""
+    rng = np.random.default_rng(41 + d)
+    c = Cache(rng, dtype, 2, 4, 1, d, [64 * 4 + 3, 64 * 2], masked=0.0)
+    ko, _ = Q.code_offsets(d)
+    c.images[:, ko[:, 9]] = 0
+    c.tk[:, :, 9] = 0.0
+    c.upload()
+    q = query(rng, 2, T, 4, d, dtype, scale=1.0)
+    q[..., 9] = outlier
+    q[:, :, 1, 9] *= -1
+    out, lse, status = c.run(q)
+    assert status == 0
+    c.check(q, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("top", [-140, -126, -113, -112, -108, -90, 90, 111, 126, 127.9])
+def test_attention_queries_at_the_ends_of_the_range(dtype, d, top):
+    """Rows whose largest element is 2^top, with keys that bring the logits back to about 1 where a
+    block can hold them (largest element 2^-99 to 2^120)."""
+    rng = np.random.default_rng(43)
+    key = 2.0 ** min(max(-top, -100.0), 118.0)
+    c = Cache(rng, dtype, 1, 4, 1, d, [64 * 3 + 5], masked=0.0)
+    k = rng.normal(size=(len(c.images), B, d)).clip(-3, 3) * key
+    _, v8, e, s = Q.decode(c.images, d)
+    c.images = Q.encode(k, v8 * s[:, 1, None, None], e)
+    c.tk = f64(torch.as_tensor(rng.normal(size=c.tk.shape).clip(-3, 3) * key).to(DT[dtype]))
+    c.upload()
+    x = rng.uniform(-1, 1, size=(1, 1, 4, d))
+    x[..., 3] = 1.0
+    q = dev(x * 2.0 ** top, DT[dtype])
+    out, lse, status = c.run(q)
+    assert status == 0
+    c.check(q, out, lse)

@@ -26,9 +26,10 @@
 // operand (tokens x dims, dims x tokens) and the rows as the small one: up to 8 rows
 // (the query heads of a KV head) waste nothing, and the weights of a slice reach the
 // second product with two 8 x 8 transposes. An e4m3 code is exact in fp16. Queries are
-// brought to a largest magnitude in [1, 2) by a power of two per row, so that fp16
-// holds a bf16 query exactly (what is lost lies 2^-25 below the row's largest
-// element); an fp32 query is the sum of two fp16 terms (22 bits). Weights are held in
+// brought to a largest magnitude in [2^14, 2^15) by a power of two per row, the top of
+// fp16's range, so that an outlier takes no bits from the others: a bf16 element is exact
+// down to 2^-31 of the row's largest, an fp32 one the sum of two fp16 terms (22 bits), and
+// what is lost otherwise is at most 2^-39 of the largest. Weights are held in
 // fp32 for the sums and rounded to fp16 (fp32 output: two terms) for the second
 // product, scaled by 2^14 so that weights down to 2^-28 of the largest keep their 11
 // bits. Each slice's product starts from zero and enters the fp32 output with the
@@ -277,9 +278,9 @@ __device__ __forceinline__ void qa_queries(const QStreamParams& p, int u, int ro
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // 2^ex <= mx < 2^(ex + 1), kept where both 2^ex and 2^-ex are normal numbers
-    const int ex = min(max((int)(__float_as_uint(mx) >> 23), 1), 253) - 127;
-    const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
+    // 2^(ex - 127) <= mx < 2^(ex - 126), kept where both powers below are normal numbers
+    const uint32_t ex = min(max(__float_as_uint(mx) >> 23, 15u), 254u);
+    const float down = __uint_as_float((268 - ex) << 23), up = __uint_as_float((ex - 14) << 23);
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const float x0 = f[k][0] * down, x1 = f[k][1] * down, x2 = f[k][2] * down, x3 = f[k][3] * down;
@@ -293,7 +294,7 @@ __device__ __forceinline__ void qa_queries(const QStreamParams& p, int u, int ro
       }
     }
     if (c == 0) {
-      rs_s[8 * i + g] = up * kQScale<D>;
+      rs_s[8 * i + g] = up;
       vis_s[8 * i + g] = qa_row(row0 + 8 * i + g, p.G, n, qn).sees;
     }
   }
@@ -702,7 +703,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float f = (NT == 1 ? fac[0][x] : rs_s[nt * 8 + 2 * c + x]) * ks;
+            const float f = (NT == 1 ? fac[0][x] : rs_s[nt * 8 + 2 * c + x]) * ks * kQScale<D>;  // (the power of two first)
             const int sees = NT == 1 ? vis[0][x] : vis_s[nt * 8 + 2 * c + x];
             float mx = -INFINITY;
 #pragma unroll
