@@ -969,3 +969,28 @@ def test_attention_queries_at_the_ends_of_the_range(dtype, d, top):
     out, lse, status = c.run(q)
     assert status == 0
     c.check(q, out, lse)
+
+
+@pytest.mark.parametrize("kind", ["stream", "pointer", "default"])
+def test_attention_workspace_belongs_to_the_calls_stream(kind):
+    """The workspace of a call on another stream is not memory that was freed on the current one while
+    work there still uses it."""
+    rng = np.random.default_rng(51)
+    c = Cache(rng, "bf16", 2, 8, 2, 64, [700, 64, 300, 129]).upload()
+    q = query(rng, 2, 1, 8, 64, "bf16")
+    need = nosa.nosa_quant_attention_workspace_bytes(c.cfg, c.cap, 1, False)
+    side = torch.cuda.Stream()
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    torch.cuda.synchronize()
+    current, other = (side, torch.cuda.default_stream()) if kind == "default" else (torch.cuda.current_stream(), side)
+    arg = {"stream": other, "pointer": other.cuda_stream, "default": 0}[kind]
+    with torch.cuda.stream(current):
+        used = torch.empty(need, dtype=torch.uint8, device="cuda")
+        for i in range(200):
+            used.fill_(i)
+        at = used.data_ptr()
+        del used
+        ws = nosa.nosa_quant_attention(c.cfg, c.units, c.t_tab, c.tail, c.t_lens, q, out, lse=lse, stream=arg)
+    assert ws.numel() == need and (ws.data_ptr() + need <= at or at + need <= ws.data_ptr())
+    torch.cuda.synchronize()
+    c.check(q, out, lse)

@@ -171,6 +171,19 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _workspace(nbytes, device, stream):
+    """A workspace for a call on `stream`, from the memory that the allocator keeps for that stream:
+    what it hands out there, no work that is queued on another stream still uses."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        p = _stream(stream)
+        stream = torch.cuda.ExternalStream(p, device=device) if p else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _check(status: int, handle=None):
     if status != 0:
         raise NosaError(status, nosa_last_error(handle))
@@ -517,11 +530,8 @@ def nosa_quant_attention(cfg: NosaConfig, units, block_tab, tail, lens, q, out, 
     qp, qs = _rows(q, dev, shp, dt, "q")
     up, nu, tab, tl, lp = _cache_args(units, block_tab, tail, lens, dev, d, elt, U, blocks, torch)
     if workspace is None:
-        workspace = torch.empty(
-            nosa_quant_attention_workspace_bytes(cfg, blocks, n, mass is not None),
-            dtype=torch.uint8, device=q.device)
-        if stream is not None:  # (it may be dropped before that stream has used it)
-            workspace.record_stream(torch.cuda.ExternalStream(_stream(stream), device=dev))
+        workspace = _workspace(nosa_quant_attention_workspace_bytes(cfg, blocks, n, mass is not None),
+                               q.device, stream)
     st = lib.nosa_quant_attention(
         C.byref(cfg), blocks, n, up, nu, tab, tl, lp, qp, qs,
         None if q_len is None else _arg(q_len, dev, (batch,), torch.int32, "q_len"),
