@@ -248,3 +248,27 @@ def test_cuda_core_selection_two_position_pass_natural():
     # every position's selection is checked, the attention on sampled positions
     w = synth.WORKLOADS["1b-bf16"].with_(batch=1, n_q_heads=4, n_kv_heads=1, head_dim=64, k=16, k_e=8)
     _prefill(w, 64 * 1215 + 9, attn_every=1999, select_tc=False)
+
+
+def test_workspace_of_a_forward_on_another_stream():
+    """The workspace of a call on another stream is not memory that was freed on the current one while
+    work there still uses it."""
+    w = synth.WORKLOADS["1b-bf16"].with_(batch=1)
+    L = 200
+    cfg = nosa.nosa_config(w.batch, w.n_q_heads, w.n_kv_heads, w.head_dim, w.dtype, w.k, w.k_e, L)
+    k, v, e = synth.gpu.kv(w, 0, L)
+    q = synth.gpu.queries(w, L).permute(1, 0, 2, 3).contiguous()
+    out, ref = torch.empty_like(q), torch.empty_like(q)
+    nosa.nosa_prefill_forward(cfg, q, k, v, e, ref)
+    need = nosa.nosa_prefill_workspace_bytes(cfg, L)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    used = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for i in range(200):
+        used.fill_(i)
+    at = used.data_ptr()
+    del used
+    ws = nosa.nosa_prefill_forward(cfg, q, k, v, e, out, stream=side)
+    assert ws.data_ptr() + need <= at or at + need <= ws.data_ptr()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref)

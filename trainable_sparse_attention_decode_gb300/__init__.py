@@ -309,7 +309,7 @@ def nosa_prefill_forward(cfg: NosaConfig, q, k, v, e, out, lse=None, sel=None, w
     if need == 0:
         raise NosaError(1, nosa_last_error() or "invalid configuration or length")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q.device, stream)
     _check(lib.nosa_prefill_forward(
         C.byref(cfg), L, _ptr(q, qs, dt, "q"), _ptr(k, ks, dt, "k"), _ptr(v, ks, dt, "v"),
         _ptr(e, ks[:3], torch.float32, "e", 4), _ptr(out, qs, dt, "out"),
