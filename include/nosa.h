@@ -494,7 +494,8 @@ nosa_status nosa_sparse_attention_noalloc(const nosa_config* cfg, const void* un
  * NOSA_QUANT_INDEX a table entry, length or count out of range, NOSA_QUANT_CAPACITY
  * tokens that did not fit. A table entry out of range is skipped, a length out of
  * range makes the unit empty for attention and leaves it as it was elsewhere, a count
- * is clamped.
+ * is clamped. Where a wait gave up, out and lse of the units whose blocks it concerned
+ * are NaN and their mass is as it was.
  *
  * Strides: k_strides, v_strides, q_strides are NULL (contiguous) or three host
  * values: elements between requests, tokens and heads of the array, each >= 0 and a

@@ -994,3 +994,31 @@ def test_attention_workspace_belongs_to_the_calls_stream(kind):
     assert ws.numel() == need and (ws.data_ptr() + need <= at or at + need <= ws.data_ptr())
     torch.cuda.synchronize()
     c.check(q, out, lse)
+
+
+@pytest.mark.parametrize("dtype,batch,hq,hkv,d,T,n,cap", [
+    ("bf16", 2, 8, 2, 128, 1, 700, 11), ("bf16", 2, 8, 2, 64, 1, 700, 600), ("f32", 3, 4, 1, 64, 1, 400, 7), ("f32", 1, 4, 2, 128, 3, 999, 16),
+    ("bf16", 2, 8, 2, 128, 12, 900, 15), ("f32", 2, 8, 2, 64, 8, 300, 5), ("bf16", 300, 4, 4, 64, 1, 130, 3)])
+def test_attention_wait_that_gives_up(dtype, batch, hq, hkv, d, T, n, cap, monkeypatch):
+    """Waits that give up at once (set on the host): the status says so, the rows that exist are
+    NaN (every unit has blocks), the accumulated weights stay, the kernels end, and the next call is right."""
+    rng = np.random.default_rng(61)
+    c = Cache(rng, dtype, batch, hq, hkv, d, [n - h for _ in range(batch) for h in range(hkv)], cap=cap).upload()
+    q = query(rng, batch, T, hq, d, dtype)
+    q_len = [T] * (batch - 1) + [max(1, T - 1)]
+    m0 = rng.random(size=c.tab.shape).astype(np.float32)
+    mass = dev(m0)
+    c.run(q, q_len=q_len, mass=dev(m0))
+    ws = c.workspace
+    monkeypatch.setenv("NOSA_INJECT_FAIL", "wait")
+    for _ in range(3):
+        out, lse, status = c.run(q, q_len=q_len, mass=mass, decay=0.5, workspace=ws)
+        assert status == nosa.NOSA_QUANT_WAIT
+        for b in range(batch):
+            assert torch.isnan(out[b, :q_len[b]]).all() and torch.isnan(lse[b, :q_len[b]]).all()
+            assert (out[b, q_len[b]:] == 7).all() and (lse[b, q_len[b]:] == 7).all()
+        assert np.array_equal(mass.cpu().numpy(), m0)
+    monkeypatch.delenv("NOSA_INJECT_FAIL")
+    out, lse, status = c.run(q, q_len=q_len, mass=mass, decay=0.5, workspace=ws)
+    assert status == 0
+    c.check(q, out, lse, q_len=q_len, mass0=m0, mass=f64(mass), decay=0.5)

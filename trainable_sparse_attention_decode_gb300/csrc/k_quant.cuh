@@ -88,6 +88,7 @@ struct QAttnArgs {
   float* mass;           // [U][max_blocks] or null
   float decay;
   uint8_t* ws;
+  bool give_up;  // a test's: every wait gives up at once
   int* status;
 };
 

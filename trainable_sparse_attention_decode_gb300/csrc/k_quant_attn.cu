@@ -27,7 +27,7 @@ Layout layout(const Shape& s, const QPlan& pl, int max_blocks, bool mass) {
     at = (at + bytes + 255) / 256 * 256;
     return here;
   };
-  w.base = take(vu * 8);
+  w.base = take((size_t)s.U * 8);
   w.part_ml = take(slots * pl.rows * 8);
   w.part_acc = take(slots * pl.rows * s.d * 4);
   w.rowstat = take(vu * pl.rows * 8);
@@ -80,6 +80,7 @@ cudaError_t launch_quant_attention(const Shape& s, const QAttnArgs& a, cudaStrea
   p.decay = a.decay;
   p.status = a.status;
   p.ctas = pl.ctas;
+  p.give_up = a.give_up;
   p.total = reinterpret_cast<long long*>(a.ws);
   p.base = reinterpret_cast<long long*>(a.ws + w.base);
   p.part_ml = reinterpret_cast<float2*>(a.ws + w.part_ml);

@@ -62,6 +62,7 @@ namespace nosa {
 
 constexpr int kQaMinItems = 2;    // blocks of a CTA's share, at least
 constexpr int kQcThreads = 256;   // combine
+constexpr int kQcScan = 4;        // lengths of a thread, where the combine adds them up
 constexpr float kQLog2e = 1.4426950408889634f;
 
 struct QStreamParams {
@@ -83,12 +84,13 @@ struct QStreamParams {
   float decay;
   int* status;
   int ctas;  // CTAs of the stream
+  bool give_up;  // every wait gives up at once (a test's)
   // workspace
   long long* total;   // items of the call
-  long long* base;    // [units x tiles] first item of each
-  float2* part_ml;    // [ctas + units x tiles][rows] maximum and sum of a part
+  long long* base;    // [units] full blocks of the units before, where there are many units
+  float2* part_ml;    // [ctas + units x tiles][rows] maximum and sum of a part (or qa_missing)
   float* part_acc;    // ... [rows][d] its output (not normalised)
-  float2* rowstat;    // [units x tiles][rows] final maximum and 1 / sum
+  float2* rowstat;    // [units x tiles][rows] final maximum and 1 / sum (-1: parts are missing)
   float* tail_w;      // [units x tiles][rows] weight of the tail
   float2* blk;        // [units x tiles][max_blocks][rows] maximum and sum of a block, or null (no weights asked for)
 };
@@ -145,6 +147,10 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// A part that is missing, because a wait gave up: whatever it is joined with, the sum of the
+// row is -infinity, which no other sum is.
+__device__ __forceinline__ float2 qa_missing() { return make_float2(3.402823466e38f, -INFINITY); }
+
 // CTAs that share `total` items, and the CTA that holds item x.
 __device__ __forceinline__ int qa_active(long long total, int ctas) {
   const long long want = (total + kQaMinItems - 1) / kQaMinItems;
@@ -184,7 +190,7 @@ struct QGeom {
   static constexpr int W = IS * RG;             // consumer warps; a producer and a helper come on top
   static constexpr int THREADS = 32 * (W + 2);
   // What the compiler is told of the threads: 480 hold it to 136 registers, so that the join fits
-  // beside the stream (kQcPerSm).
+  // beside the stream (kQcPerSm). fp32 takes the 144 that it may.
   static constexpr int BOUND = D == 64 && ROWS == 8 && !F32 ? 480 : THREADS;
   static constexpr int STAGES = D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 8 : 9;
   static constexpr int SL = 4;                  // slices of a block that a warp takes at once
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
       mbar_init(&dump_free[s], 1);
     }
     fence_mbar_init();
-    s_bad = 0;
+    s_bad = p.give_up;
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -430,6 +436,13 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
+  }
+  if (p.U > kQcScan * kQcThreads) {  // each unit's place by one of the CTAs
+    long long at = before;
+    for (int u = a0; u < a1; ++u) {
+      if (u % p.ctas == cta) p.base[u] = at;
+      at += max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
+    }
   }
   total *= p.tiles;
   before *= p.tiles;
@@ -453,6 +466,10 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
   // Waits (whole warp) for a phase, with a limit, unless another warp has given up.
   auto wait = [&](uint64_t* bar, int phase) {
     return __all_sync(0xffffffffu, s_bad == 0 && mbar_wait_bounded(bar, (uint32_t)(phase & 1)));
+  };
+  auto give_up = [&]() {  // (one lane)
+    s_bad = 1;
+    quant_flag(p.status, kQErrWait);
   };
 
   // Whether the consumers join their last segment's rows with the helper. Measured on
@@ -523,7 +540,6 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
           mbar_arrive_expect_tx(&full[lane], UB);
           bulk_g2s(smem + lane * UB, p.units + (long long)idx * UB, UB, &full[lane]);
         }
-        if (j == 0) p.base[(long long)u * p.tiles + tile] = g0 + it;
         ++fills;
         it += STAGES;
         pos += STAGES;
@@ -539,10 +555,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
       }
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
     }
-    if (!ok && lane == 0) {
-      s_bad = 1;
-      quant_flag(p.status, kQErrWait);
-    }
+    if (!ok && lane == 0) give_up();
     __syncthreads();
     if (s_bad != 0 && fills > 0) mbar_wait_bounded(&full[lane], (uint32_t)((fills - 1) & 1));  // drain
     return;
@@ -582,11 +595,12 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
       if (lane == 0) mbar_arrive(&dump_free[k % ND]);
       if (ahead.more()) prepare();  // (every warp has left segment k, whose queries were in this buffer)
     }
-    if (!ok && lane == 0) {
-      s_bad = 1;
-      quant_flag(p.status, kQErrWait);
-    }
+    if (!ok && lane == 0) give_up();
     __syncthreads();
+    if (s_bad != 0) {  // none of the CTA's parts counts
+      for (QWalk all(p, s_unit, g0 - s_before, items, lane); all.more(); all.next())
+        if (lane < ROWS) p.part_ml[(cta + all.vu()) * ROWS + lane] = qa_missing();
+    }
     return;
   }
 
@@ -840,10 +854,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
       join_rows(k, cta + vu, warp, W + 1);
     }
   }
-  if (!ok && lane == 0) {
-    s_bad = 1;
-    quant_flag(p.status, kQErrWait);
-  }
+  if (!ok && lane == 0) give_up();
   __syncthreads();
 }
 
@@ -862,7 +873,6 @@ constexpr int kQcRows = 8;
 // 9.2 (15.0). At d = 128 there is room for 80
 // beside a bf16 stream, and the values come along with the keys.
 template <typename T, int D> constexpr int kQcPerSm = D == 64 ? (sizeof(T) == 4 ? 6 : 5) : 3;
-constexpr int kQcScan = 4;  // lengths of a thread
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kernel(QStreamParams p, int rows, bool weights) {
@@ -1017,7 +1027,7 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
   if (nb > 0) {
     if (!few) {
       total = __ldcg(p.total);
-      first = __ldcg(p.base + vu);
+      first = __ldcg(p.base + u) * p.tiles + (long long)tile * nb;
     }
     const int active = qa_active(total, p.ctas);
     c0 = qa_cta_of(first, total, active);
@@ -1066,7 +1076,8 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
   }
   if (on && grp == 0) {
     if (nt > 0) merge(make_float2(m_s[r], l_s[r]), *reinterpret_cast<const float4*>(o_s + r * D + d0 + 4 * x));
-    const float mu = finite_max(m), inv = l == 0.f ? 0.f : 1.f / l;
+    const bool missing = l == -INFINITY;
+    const float mu = finite_max(m), inv = missing ? __uint_as_float(0x7FC00000u) : l == 0.f ? 0.f : 1.f / l;
     const QRow w = qa_row(r0 + r, p.G, n, qn);
     const long long row = ((long long)b * p.T + w.t) * p.Hq + h * p.G + w.g;
     T* dst = reinterpret_cast<T*>(p.out) + row * D + d0 + 4 * x;
@@ -1081,10 +1092,10 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
       if (p.blk != nullptr) {
         const float tw = nt > 0 ? l_s[r] * exp_from(m_s[r], mu) * inv : 0.f;
         if (weights) {
-          st_s[r] = make_float2(mu, inv);
+          st_s[r] = make_float2(mu, missing ? -1.f : inv);
           tw_s[r] = tw;
         } else if (blockIdx.z == 0) {
-          p.rowstat[(long long)vu * rows + rt + r] = make_float2(mu, inv);
+          p.rowstat[(long long)vu * rows + rt + r] = make_float2(mu, missing ? -1.f : inv);
           p.tail_w[(long long)vu * rows + rt + r] = tw;
         }
       }
@@ -1095,12 +1106,14 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
     p.tail_w[(long long)vu * rows + rt + tid] = 0.f;
   }
   if (weights) {
-    // All of the unit's rows are here: the accumulated weights too. Eight lanes have a
-    // block's rows; CTA z of the unit takes every gridDim.z-th run of 32 blocks.
+    // All of the unit's rows are here: the accumulated weights too (unless parts are
+    // missing). Eight lanes have a block's rows; CTA z of the unit takes every gridDim.z-th
+    // run of 32 blocks.
     __syncthreads();
     const int row = tid % kQcRows, step = kQcThreads / kQcRows * gridDim.z;
     const float2 st = row < live ? st_s[row] : make_float2(0.f, 0.f);
     const float tw = row < live ? tw_s[row] : 0.f;
+    if (__any_sync(0xffffffffu, st.y == -1.f)) return;  // (a warp has all rows)
     float* mass = p.mass + (long long)u * p.max_blocks;
     const float2* note = p.blk + (long long)u * p.max_blocks * kQcRows + row;
     for (int j0 = blockIdx.z * (kQcThreads / kQcRows) + tid / kQcRows; j0 - tid / kQcRows < p.max_blocks; j0 += 8 * step) {
@@ -1152,10 +1165,12 @@ __global__ void __launch_bounds__(kQcThreads) quant_weights_kernel(QStreamParams
   }
   griddep_wait();
   griddep_launch_dependents();
+  bool missing = false;
   for (int tile = 0; tile < p.tiles; ++tile) {
     const long long vu = (long long)u * p.tiles + tile;
     const bool on = tile * ROWS + r < p.T * p.G;
     const float2 st = on ? __ldcg(p.rowstat + vu * ROWS + r) : make_float2(0.f, 0.f);
+    missing |= st.y == -1.f;
     float2 ml[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -1169,6 +1184,7 @@ __global__ void __launch_bounds__(kQcThreads) quant_weights_kernel(QStreamParams
       if (j == nb && nt > 0) w[i] += __ldcg(p.tail_w + vu * ROWS + r);
     }
   }
+  if (__any_sync(0xffffffffu, missing)) return;  // the unit's weights stay as they are
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int j = first + i * PW;

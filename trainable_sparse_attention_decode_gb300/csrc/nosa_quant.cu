@@ -3,6 +3,8 @@
 #include "nosa.h"
 #include "k_quant.cuh"
 
+#include <cstdlib>
+#include <cstring>
 #include <string>
 
 namespace nosa {
@@ -57,6 +59,13 @@ nosa_status take_strides(const char* name, const int64_t* st, int n, int heads, 
     if (st[i] < 0 || st[i] % (16 / s.elt) != 0)
       return invalid(std::string(name) + ": strides must be >= 0 and multiples of 16 bytes");
   return NOSA_OK;
+}
+
+// NOSA_INJECT_FAIL=wait: the attention's waits give up at once (a test hook, read at every
+// call; no GPU fault is involved).
+bool inject_wait() {
+  const char* g = std::getenv("NOSA_INJECT_FAIL");
+  return g != nullptr && std::strcmp(g, "wait") == 0;
 }
 
 nosa_status launched(cudaError_t e, const char* what) {
@@ -153,6 +162,7 @@ nosa_status nosa_quant_attention(const nosa_config* cfg, int32_t max_blocks, int
   a.mass = mass;
   a.decay = decay;
   a.ws = static_cast<uint8_t*>(workspace);
+  a.give_up = inject_wait();
   a.status = status;
   return launched(launch_quant_attention(s, a, static_cast<cudaStream_t>(stream)), "8-bit cache attention");
 }
