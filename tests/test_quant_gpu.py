@@ -1022,3 +1022,43 @@ def test_attention_wait_that_gives_up(dtype, batch, hq, hkv, d, T, n, cap, monke
     out, lse, status = c.run(q, q_len=q_len, mass=mass, decay=0.5, workspace=ws)
     assert status == 0
     c.check(q, out, lse, q_len=q_len, mass0=m0, mass=f64(mass), decay=0.5)
+
+
+@pytest.mark.parametrize("dtype,batch,hq,hkv,d,cap", [("bf16", 64, 16, 8, 64, 4), ("f32", 40, 8, 8, 128, 4), ("bf16", 160, 24, 8, 128, 200),
+                                                      ("f32", 300, 4, 4, 64, 140)])
+def test_calls_behind_each_other_read_what_the_last_one_wrote(dtype, batch, hq, hkv, d, cap):
+    """Steps of append, attention and eviction over many units, whose lengths share cache lines: queued
+    without a pause and with the GPU waited for after every call, the bits are the same."""
+    rng = np.random.default_rng(71)
+    U = batch * hkv
+    cfg = config(batch, hq, hkv, d, dtype)
+    steps = 24
+    ins = [(query(rng, batch, 1, hkv, d, dtype, 1.0), query(rng, batch, 1, hkv, d, dtype, 1.0), query(rng, batch, 1, hq, d, dtype)) for _ in range(steps)]
+    prompt = query(rng, batch, 3 * B, hkv, d, dtype, 1.0)
+    n_new = dev(rng.integers(1, 3 * B - 1, size=batch).astype(np.int32))
+
+    def loop(pause):
+        done = torch.cuda.synchronize if pause else lambda: None
+        units = torch.zeros(U * 4, Q.unit_bytes(d), dtype=torch.uint8, device="cuda")
+        tab = torch.zeros(U, cap, dtype=torch.int32, device="cuda")
+        tab[:, :4] = torch.arange(U * 4, dtype=torch.int32, device="cuda").view(U, 4)
+        tail = torch.zeros(U * nosa.nosa_payload_bytes(cfg), dtype=torch.uint8, device="cuda")
+        lens, mass = torch.zeros(U, dtype=torch.int32, device="cuda"), torch.zeros(U, cap, device="cuda")
+        ws = torch.zeros(nosa.nosa_quant_attention_workspace_bytes(cfg, cap, 1, True), dtype=torch.uint8, device="cuda")
+        outs = [(torch.empty_like(ins[0][2]), torch.empty(batch, 1, hq, device="cuda")) for _ in range(steps)]
+        torch.cuda.synchronize()
+        nosa.nosa_quant_append(cfg, prompt, prompt, None, units, tab, tail, lens, n_new=n_new)
+        done()
+        for (k, v, q), (out, lse) in zip(ins, outs):
+            nosa.nosa_quant_append(cfg, k, v, None, units, tab, tail, lens)
+            done()
+            nosa.nosa_quant_attention(cfg, units, tab, tail, lens, q, out, lse=lse, mass=mass, decay=0.9, workspace=ws)
+            done()
+            nosa.nosa_quant_evict(cfg, 2, 1, tab, mass, lens)
+            done()
+        torch.cuda.synchronize()
+        return [x for pair in outs for x in pair] + [mass, lens, tail, units]
+
+    want = loop(True)
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(want, loop(False)))

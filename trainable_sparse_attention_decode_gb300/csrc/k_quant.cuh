@@ -103,16 +103,19 @@ __device__ __forceinline__ void quant_flag(int* status, int bit) {
   if (status != nullptr) atomicOr(status, bit);
 }
 // Tokens of unit u: lens[u], or -1 (flagged by `flag`) where it is not a length of this cache.
+// EARLY: read before the kernel's own griddep_wait (see launch_dependent).
+template <bool EARLY = false>
 __device__ __forceinline__ int quant_len(const int32_t* lens, int u, int max_blocks, int* status, bool flag) {
-  const int n = lens[u];
+  const int n = EARLY ? __ldcg(lens + u) : lens[u];
   if (n >= 0 && n <= kQB * max_blocks) return n;
   if (flag) quant_flag(status, kQErrIndex);
   return -1;
 }
 // Valid new tokens of request b out of n.
+template <bool EARLY = false>
 __device__ __forceinline__ int quant_count(const int32_t* count, int b, int n, int* status, bool flag) {
   if (count == nullptr) return n;
-  const int c = count[b];
+  const int c = EARLY ? __ldcg(count + b) : count[b];
   if (c >= 0 && c <= n) return c;
   if (flag) quant_flag(status, kQErrIndex);
   return c < 0 ? 0 : n;
@@ -123,7 +126,12 @@ __device__ __forceinline__ int quant_count(const int32_t* count, int b, int n, i
 // calls griddep_wait before it ends: where a kernel has ended, all before it have.
 // The first kernel of a call waits before it reads anything and only then lets its
 // successor start (griddep_launch_dependents), so that a successor inside the call may
-// read, before its own wait, what was there before the call.
+// read, before its own wait, what was there before the call: a wait returns when all that
+// came before has been performed in the device's memory, that is, in L2, and no CTA of the
+// successor starts before every CTA of the first kernel has come past its wait. Only a
+// copy that an earlier kernel left in the SM's L1 could be older, so such reads go past L1
+// (__ldcg). Nothing that the call itself writes is read early, but for a weight by the one
+// thread that then writes it.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg{};

@@ -894,8 +894,8 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
   const int vu = blockIdx.x, u = vu / p.tiles, tile = vu % p.tiles, b = u / p.Hkv, h = u % p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool flag = tid == 0 && blockIdx.y == 0 && blockIdx.z == 0;
-  const int n = max(0, quant_len(p.lens, u, p.max_blocks, p.status, flag));
-  const int qn = quant_count(p.q_len, b, p.T, p.status, flag);
+  const int n = max(0, quant_len<true>(p.lens, u, p.max_blocks, p.status, flag));
+  const int qn = quant_count<true>(p.q_len, b, p.T, p.status, flag);
   const int nb = n / kQB, nt = n % kQB;
   const int rt = blockIdx.y * kQcRows, r0 = tile * rows + rt;        // first row, in the tile and in the request
   const int live = min(kQcRows, max(0, qn * p.G - r0));              // rows that exist
@@ -906,22 +906,22 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
     uint4 kr[KC];
 #pragma unroll
     for (int i = 0; i < KC; ++i)
-      kr[i] = t < nt ? *reinterpret_cast<const uint4*>(tail + ((size_t)(cg * KC + i) * kQB + t) * 16) : make_uint4(0, 0, 0, 0);
+      kr[i] = t < nt ? __ldcg(reinterpret_cast<const uint4*>(tail + ((size_t)(cg * KC + i) * kQB + t) * 16)) : make_uint4(0, 0, 0, 0);
     uint4 vr[TPT];
     auto load_values = [&]() {
 #pragma unroll
       for (int i = 0; i < TPT; ++i)
-        vr[i] = t0 + i < nt ? *reinterpret_cast<const uint4*>(tail + (size_t)kQB * D * ELT + (size_t)(t0 + i) * D * ELT + col * 16)
+        vr[i] = t0 + i < nt ? __ldcg(reinterpret_cast<const uint4*>(tail + (size_t)kQB * D * ELT + (size_t)(t0 + i) * D * ELT + col * 16))
                             : make_uint4(0, 0, 0, 0);
     };
     if (!kLate) load_values();
     const float* es = reinterpret_cast<const float*>(tail + 2 * (size_t)kQB * D * ELT);
-    const float e0 = lane < nt ? es[lane] : -INFINITY, e1 = lane + 32 < nt ? es[lane + 32] : -INFINITY;
+    const float e0 = lane < nt ? __ldcg(es + lane) : -INFINITY, e1 = lane + 32 < nt ? __ldcg(es + lane + 32) : -INFINITY;
     for (int i = tid; i < live * NCH; i += kQcThreads) {
       const int r = i / NCH, x = i % NCH;
       const QRow w = qa_row(r0 + r, p.G, n, qn);
       const T* src = reinterpret_cast<const T*>(p.q) + b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + x * CE;
-      const uint4 y = *reinterpret_cast<const uint4*>(src);
+      const uint4 y = __ldcg(reinterpret_cast<const uint4*>(src));
       const T* e = reinterpret_cast<const T*>(&y);
 #pragma unroll
       for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = to_f32(e[k]) * kQScale<D>;
@@ -1002,7 +1002,7 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
 #pragma unroll
     for (int k = 0; k < kQcScan; ++k) {
       const int i = tid + k * kQcThreads;
-      const int c = i < p.U ? max(0, quant_len(p.lens, i, p.max_blocks, nullptr, false)) / kQB : 0;
+      const int c = i < p.U ? max(0, quant_len<true>(p.lens, i, p.max_blocks, nullptr, false)) / kQB : 0;
       all += c;
       if (i < u) ahead += c;
     }
@@ -1153,14 +1153,14 @@ template <int ROWS>
 __global__ void __launch_bounds__(kQcThreads) quant_weights_kernel(QStreamParams p) {
   constexpr int PW = 32 / ROWS;  // blocks at once
   const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane % ROWS;
-  const int n = max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)), nb = n / kQB, nt = n % kQB;
+  const int n = max(0, quant_len<true>(p.lens, u, p.max_blocks, nullptr, false)), nb = n / kQB, nt = n % kQB;
   const int first = blockIdx.y * weights_per_cta<ROWS>() + warp * PW * 4 + lane / ROWS;
   float* mass = p.mass + (long long)u * p.max_blocks;
   float old[4], w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int j = first + i * PW;
-    old[i] = r == 0 && j < p.max_blocks && p.decay != 0.f ? mass[j] * p.decay : 0.f;
+    old[i] = r == 0 && j < p.max_blocks && p.decay != 0.f ? __ldcg(mass + j) * p.decay : 0.f;
     w[i] = 0.f;
   }
   griddep_wait();

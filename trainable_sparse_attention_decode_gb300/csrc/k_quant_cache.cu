@@ -222,10 +222,11 @@ struct BlockQuant {
 struct UnitAppend {
   int n0, add;
 };
+template <bool EARLY>
 __device__ __forceinline__ UnitAppend unit_append(const QAppendArgs& p, int Hkv, int u, bool flag) {
   UnitAppend r;
-  r.n0 = quant_len(p.lens, u, p.max_blocks, p.status, flag);
-  r.add = quant_count(p.n_new, u / Hkv, p.n, p.status, flag);
+  r.n0 = quant_len<EARLY>(p.lens, u, p.max_blocks, p.status, flag);
+  r.add = quant_count<EARLY>(p.n_new, u / Hkv, p.n, p.status, flag);
   if (r.n0 < 0) {
     r.n0 = r.add = 0;
   } else if (r.n0 > kQB * p.max_blocks - r.add) {
@@ -244,7 +245,7 @@ quant_blocks_kernel(QAppendArgs p, int Hkv, long long payload) {
   griddep_wait();
   griddep_launch_dependents();
   const int u = blockIdx.x, j = blockIdx.y;
-  const UnitAppend a = unit_append(p, Hkv, u, false);
+  const UnitAppend a = unit_append<false>(p, Hkv, u, false);
   if (j >= (a.n0 % kQB + a.add) / kQB) return;
   BlockQuant<T, D> q(p, Hkv, u, a.n0, p.tail + u * payload);
   q.load(j);
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kAppendThreads) quant_tail_kernel(QAppendArgs 
   const int u = blockIdx.x, b = u / Hkv, h = u % Hkv, tid = threadIdx.x;
   if (BLOCK) griddep_wait();  // (the call's first launch)
   griddep_launch_dependents();
-  const UnitAppend a = unit_append(p, Hkv, u, tid == 0);
+  const UnitAppend a = unit_append<!BLOCK>(p, Hkv, u, tid == 0);
   uint8_t* tail = p.tail + u * payload;
   const int old = a.n0 % kQB, done = (old + a.add) / kQB;
   if constexpr (BLOCK) {
