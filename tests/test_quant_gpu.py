@@ -1062,3 +1062,29 @@ def test_calls_behind_each_other_read_what_the_last_one_wrote(dtype, batch, hq, 
     want = loop(True)
     for _ in range(3):
         assert all(torch.equal(x, y) for x, y in zip(want, loop(False)))
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d,T,n", [("bf16", 8, 8, 64, 1, 70), ("bf16", 16, 4, 128, 1, 900), ("f32", 8, 2, 64, 4, 300), ("f32", 8, 4, 128, 1, 64)])
+def test_attention_queries_written_by_the_call_before(dtype, hq, hkv, d, T, n):
+    """Each call's queries are the outputs of the call before it, in two buffers that are written again
+    and again: queued without a pause and with one, the bits are the same."""
+    rng = np.random.default_rng(73)
+    c = Cache(rng, dtype, 20, hq, hkv, d, [n] * (20 * hkv)).upload()
+    first = query(rng, 20, T, hq, d, dtype)
+    ws = torch.empty(nosa.nosa_quant_attention_workspace_bytes(c.cfg, c.cap, T), dtype=torch.uint8, device="cuda")
+
+    def chain(pause):
+        a, b, seen = first.clone(), torch.empty_like(first), []
+        for i in range(40):
+            nosa.nosa_quant_attention(c.cfg, c.units, c.t_tab, c.tail, c.t_lens, a, b, workspace=ws)
+            if pause:
+                torch.cuda.synchronize()
+            a, b = b, a
+            if i % 8 == 7:
+                seen.append(a.clone())
+        torch.cuda.synchronize()
+        return seen
+
+    want = chain(True)
+    for _ in range(5):
+        assert all(torch.equal(x, y) for x, y in zip(want, chain(False)))

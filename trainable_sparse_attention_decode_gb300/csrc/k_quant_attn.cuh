@@ -263,7 +263,8 @@ __device__ __forceinline__ void qa_queries(const QStreamParams& p, int u, int ro
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       raw[i][k] = Raw{};
-      if (w.t < qn) raw[i][k] = __ldg(reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.q) + (src + 16 * k) * (F32 ? 4 : 2)));
+      // (not the read-only path: the kernel may be resident while its predecessor writes q)
+      if (w.t < qn) raw[i][k] = *reinterpret_cast<const Raw*>(static_cast<const uint8_t*>(p.q) + (src + 16 * k) * (F32 ? 4 : 2));
     }
   }
 #pragma unroll
