@@ -1088,3 +1088,46 @@ def test_attention_queries_written_by_the_call_before(dtype, hq, hkv, d, T, n):
     want = chain(True)
     for _ in range(5):
         assert all(torch.equal(x, y) for x, y in zip(want, chain(False)))
+
+
+def test_first_evictions_of_two_threads():
+    """A process in which threads with tables of different widths evict first, at once: the widest table
+    is evicted from afterwards."""
+    import subprocess
+    import sys
+    code = """
+import sys, threading
+sys.path[:0] = [%r, %r]
+import numpy as np, torch
+import test_quant_gpu as t
+nosa = t.nosa
+widths = [6000, 16384, 5200, 9000, 12000, 7000, 16000, 5100]
+cfg = t.config(1, 1, 1, 64, "bf16")
+def arrays(cap):
+    rng = np.random.default_rng(cap)
+    mass = rng.random((1, cap)).astype(np.float32)
+    return mass, t.dev(np.arange(cap, dtype=np.int32)[None]), t.dev(mass), t.dev(np.array([64 * cap], np.int32))
+ins = [arrays(cap) for cap in widths]
+torch.cuda.synchronize()
+gate, bad = threading.Barrier(len(widths)), []
+def first(mass, tab, m, n):
+    gate.wait()
+    try:
+        nosa.nosa_quant_evict(cfg, 16, 4, tab, m, n)
+    except Exception as e:
+        bad.append(e)
+threads = [threading.Thread(target=first, args=x) for x in ins]
+[x.start() for x in threads]
+[x.join() for x in threads]
+mass, tab, m, n = arrays(16384)
+nosa.nosa_quant_evict(cfg, 16, 4, tab, m, n)
+torch.cuda.synchronize()
+assert not bad, bad
+for (mass, tab, m, n), cap in zip(ins + [(mass, tab, m, n)], widths + [16384]):
+    wt, wm, wn, _ = t.Q.evict(np.arange(cap), mass[0], 64 * cap, 16, 4)
+    assert n.item() == wn and np.array_equal(tab[0].cpu().numpy(), wt) and np.array_equal(m[0].cpu().numpy(), wm)
+print("ok")
+""" % (ROOT, os.path.join(ROOT, "tests"))
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr

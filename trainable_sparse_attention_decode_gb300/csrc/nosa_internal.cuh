@@ -13,6 +13,7 @@
 #include <stddef.h>
 
 #include <atomic>
+#include <mutex>
 
 namespace nosa {
 
@@ -325,6 +326,10 @@ struct DeviceGuard {
 inline cudaError_t raise_smem_limit(const void* func, size_t bytes, std::atomic<int>* cache) {
   int dev = 0;
   cudaGetDevice(&dev);
+  if (dev < 64 && cache[dev].load(std::memory_order_relaxed) >= (int)bytes) return cudaSuccess;
+  // One thread raises at a time: a smaller limit must not be set after a larger one.
+  static std::mutex mutex;
+  const std::lock_guard<std::mutex> lock(mutex);
   if (dev < 64 && cache[dev].load(std::memory_order_relaxed) >= (int)bytes) return cudaSuccess;
   const cudaError_t e =
       cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
