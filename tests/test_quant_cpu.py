@@ -154,3 +154,32 @@ def test_oracle_evict_keeps_the_heaviest():
         assert sum(mass[order[:keep - recent]]) == best
         assert list(order[keep - recent:keep]) == list(range(full - recent, full))
         assert m[keep] == mass[full] and not m[keep + 1:full + 1].any()
+
+
+@pytest.mark.parametrize("bad", [None, 4096, np.zeros((2, 1, 2, 128), np.float32), [1, 2], "x"])
+def test_binding_refuses_what_is_no_tensor(bad):
+    """A tensor that is missing, and pointers, arrays and lists in its place: a ValueError."""
+    cfg, U, z = _cfg(), 4, torch.zeros
+    k, q = z(2, 1, 2, 128, dtype=torch.bfloat16), z(2, 1, 8, 128, dtype=torch.bfloat16)
+    cache = dict(units=z(8, 16672, dtype=torch.uint8), block_tab=z(U, 4, dtype=torch.int32),
+                 tail=z(U, nosa.nosa_payload_bytes(cfg), dtype=torch.uint8), lens=z(U, dtype=torch.int32))
+    calls = [(nosa.nosa_quant_append, dict(k=k, v=k, **cache), dict(e=None)),
+             (nosa.nosa_quant_attention, dict(q=q, out=torch.empty_like(q), **cache), {}),
+             (nosa.nosa_quant_evict, dict(block_tab=cache["block_tab"], mass=z(U, 4), lens=cache["lens"]),
+              dict(budget=2, n_recent=1))]
+    for f, tensors, others in calls:
+        for name in tensors:
+            with pytest.raises(ValueError):  # (or the tensors before it are, which are the CPU's)
+                f(cfg, **{**tensors, name: bad}, **others)
+    if bad is not None:
+        with pytest.raises(ValueError):
+            nosa.nosa_quant_append(cfg, **calls[0][1], e=bad)
+
+
+def test_binding_refuses_tensors_of_other_ranks():
+    cfg, U, z = _cfg(), 4, torch.zeros
+    with pytest.raises(ValueError, match="block_tab"):
+        nosa.nosa_quant_evict(cfg, 2, 1, z(U, dtype=torch.int32), z(U, 4), z(U, dtype=torch.int32))
+    q = z(8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q must have 4"):
+        nosa.nosa_quant_attention(cfg, z(8), z(U, 4, dtype=torch.int32), z(8), z(U), q, q)

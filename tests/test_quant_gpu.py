@@ -1131,3 +1131,21 @@ print("ok")
     for _ in range(3):
         r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
         assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("bad", [None, 4096, np.zeros((2, 1, 2, 64), np.float32)])
+def test_binding_names_what_is_no_tensor(bad):
+    cfg = config(2, 4, 2, 64, "bf16")
+    z = lambda *shape, dtype=torch.float32: torch.zeros(*shape, dtype=dtype, device="cuda")  # noqa: E731
+    k, q = z(2, 1, 2, 64, dtype=torch.bfloat16), z(2, 1, 4, 64, dtype=torch.bfloat16)
+    cache = dict(units=z(6, Q.unit_bytes(64), dtype=torch.uint8), block_tab=z(4, 3, dtype=torch.int32),
+                 tail=z(4 * nosa.nosa_payload_bytes(cfg), dtype=torch.uint8), lens=z(4, dtype=torch.int32))
+    calls = [(nosa.nosa_quant_append, dict(k=k, v=k, **cache), dict(e=None)),
+             (nosa.nosa_quant_attention, dict(q=q, out=torch.empty_like(q), **cache), {}),
+             (nosa.nosa_quant_evict, dict(block_tab=cache["block_tab"], mass=z(4, 3), lens=cache["lens"]), dict(budget=2, n_recent=1))]
+    for f, tensors, others in calls:
+        for name in tensors:
+            with pytest.raises(ValueError, match=f"{name} (is required|must)"):
+                f(cfg, **{**tensors, name: bad}, **others)
+        f(cfg, **tensors, **others)  # and as it should be it runs
+    torch.cuda.synchronize()

@@ -453,6 +453,19 @@ def _refuse(t, device, shape, dtype, what, align):
     return _ptr(t, shape, dtype, what, align)
 
 
+def _not_tensors(required, optional, dims):
+    """Why a call whose arguments lack a tensor's attributes or dimensions is refused."""
+    torch = _torch()
+    for what, t in {**required, **optional}.items():
+        if t is None and what in required:
+            raise ValueError(f"{what} is required")
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise ValueError(f"{what} must be a CUDA tensor")
+    for what, n in dims.items():
+        if required[what].ndim != n:
+            raise ValueError(f"{what} must have {n} dimensions")
+
+
 def _rows(t, device, shape, dtype, what):
     """Pointer and strides (None where contiguous) of [batch][n][heads][d] rows."""
     if t.is_contiguous():
@@ -492,23 +505,28 @@ def nosa_quant_append(cfg: NosaConfig, k, v, e, units, block_tab, tail, lens, le
     The new lengths go to lens_out (lens itself by default); n_new [batch] int32 gives the
     valid tokens of each request."""
     torch = _torch()
-    dev, batch, hkv, d = cfg.device, cfg.batch, cfg.n_kv_heads, cfg.head_dim
-    dt, elt = (torch.float32, 4) if cfg.dtype == NOSA_F32 else (torch.bfloat16, 2)
-    n, blocks, U = k.shape[1], block_tab.shape[1], batch * hkv
-    shp = (batch, n, hkv, d)
-    kp, ks = _rows(k, dev, shp, dt, "k")
-    vp, vs = _rows(v, dev, shp, dt, "v")
-    up, nu, tab, tl, lp = _cache_args(units, block_tab, tail, lens, dev, d, elt, U, blocks, torch)
-    st = lib.nosa_quant_append(
-        C.byref(cfg), blocks, n, kp, ks, vp, vs,
-        None if e is None else _arg(e, dev, shp[:3], torch.float32, "e"),
-        None if n_new is None else _arg(n_new, dev, (batch,), torch.int32, "n_new"),
-        up, nu, tab, tl, lp,
-        lp if lens_out is None else _arg(lens_out, dev, (U,), torch.int32, "lens_out"),
-        None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
-        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
-    if st:
-        _check(st)
+    try:
+        dev, batch, hkv, d = cfg.device, cfg.batch, cfg.n_kv_heads, cfg.head_dim
+        dt, elt = (torch.float32, 4) if cfg.dtype == NOSA_F32 else (torch.bfloat16, 2)
+        n, blocks, U = k.shape[1], block_tab.shape[1], batch * hkv
+        shp = (batch, n, hkv, d)
+        kp, ks = _rows(k, dev, shp, dt, "k")
+        vp, vs = _rows(v, dev, shp, dt, "v")
+        up, nu, tab, tl, lp = _cache_args(units, block_tab, tail, lens, dev, d, elt, U, blocks, torch)
+        st = lib.nosa_quant_append(
+            C.byref(cfg), blocks, n, kp, ks, vp, vs,
+            None if e is None else _arg(e, dev, shp[:3], torch.float32, "e"),
+            None if n_new is None else _arg(n_new, dev, (batch,), torch.int32, "n_new"),
+            up, nu, tab, tl, lp,
+            lp if lens_out is None else _arg(lens_out, dev, (U,), torch.int32, "lens_out"),
+            None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        if st:
+            _check(st)
+    except (AttributeError, IndexError):
+        _not_tensors(dict(k=k, v=v, units=units, block_tab=block_tab, tail=tail, lens=lens),
+                     dict(e=e, lens_out=lens_out, n_new=n_new, status=status), dict(k=4, v=4, block_tab=2))
+        raise
 
 
 def nosa_quant_attention_workspace_bytes(cfg: NosaConfig, max_blocks: int, n_queries: int = 1,
@@ -523,27 +541,33 @@ def nosa_quant_attention(cfg: NosaConfig, units, block_tab, tail, lens, q, out, 
     cache; writes out (and lse [batch][n][Hq]) and, given mass [U][max_blocks], accumulates the
     blocks' attention weight. Returns the workspace (allocated here when not passed)."""
     torch = _torch()
-    dev, batch, d = cfg.device, cfg.batch, cfg.head_dim
-    dt, elt = (torch.float32, 4) if cfg.dtype == NOSA_F32 else (torch.bfloat16, 2)
-    n, blocks, U = q.shape[1], block_tab.shape[1], batch * cfg.n_kv_heads
-    shp = (batch, n, cfg.n_q_heads, d)
-    qp, qs = _rows(q, dev, shp, dt, "q")
-    up, nu, tab, tl, lp = _cache_args(units, block_tab, tail, lens, dev, d, elt, U, blocks, torch)
-    if workspace is None:
-        workspace = _workspace(nosa_quant_attention_workspace_bytes(cfg, blocks, n, mass is not None),
-                               q.device, stream)
-    st = lib.nosa_quant_attention(
-        C.byref(cfg), blocks, n, up, nu, tab, tl, lp, qp, qs,
-        None if q_len is None else _arg(q_len, dev, (batch,), torch.int32, "q_len"),
-        _arg(out, dev, shp, dt, "out", 16),
-        None if lse is None else _arg(lse, dev, shp[:3], torch.float32, "lse"),
-        None if mass is None else _arg(mass, dev, (U, blocks), torch.float32, "mass"), decay,
-        _buffer(workspace, dev, torch.uint8, "workspace", 256), workspace.numel(),
-        None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
-        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
-    if st:
-        _check(st)
-    return workspace
+    try:
+        dev, batch, d = cfg.device, cfg.batch, cfg.head_dim
+        dt, elt = (torch.float32, 4) if cfg.dtype == NOSA_F32 else (torch.bfloat16, 2)
+        n, blocks, U = q.shape[1], block_tab.shape[1], batch * cfg.n_kv_heads
+        shp = (batch, n, cfg.n_q_heads, d)
+        qp, qs = _rows(q, dev, shp, dt, "q")
+        up, nu, tab, tl, lp = _cache_args(units, block_tab, tail, lens, dev, d, elt, U, blocks, torch)
+        if workspace is None:
+            workspace = _workspace(nosa_quant_attention_workspace_bytes(cfg, blocks, n, mass is not None),
+                                   q.device, stream)
+        st = lib.nosa_quant_attention(
+            C.byref(cfg), blocks, n, up, nu, tab, tl, lp, qp, qs,
+            None if q_len is None else _arg(q_len, dev, (batch,), torch.int32, "q_len"),
+            _arg(out, dev, shp, dt, "out", 16),
+            None if lse is None else _arg(lse, dev, shp[:3], torch.float32, "lse"),
+            None if mass is None else _arg(mass, dev, (U, blocks), torch.float32, "mass"), decay,
+            _buffer(workspace, dev, torch.uint8, "workspace", 256), workspace.numel(),
+            None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        if st:
+            _check(st)
+        return workspace
+    except (AttributeError, IndexError):
+        _not_tensors(dict(q=q, out=out, units=units, block_tab=block_tab, tail=tail, lens=lens),
+                     dict(lse=lse, mass=mass, q_len=q_len, workspace=workspace, status=status),
+                     dict(q=4, block_tab=2))
+        raise
 
 
 def nosa_quant_evict(cfg: NosaConfig, budget, n_recent, block_tab, mass, lens, tab_out=None,
@@ -551,18 +575,24 @@ def nosa_quant_evict(cfg: NosaConfig, budget, n_recent, block_tab, mass, lens, t
     """Evicts the blocks of least accumulated weight from every unit with more than `budget` full
     blocks (its newest n_recent stay). Works in place unless outputs are given."""
     torch = _torch()
-    dev, U, blocks = cfg.device, cfg.batch * cfg.n_kv_heads, block_tab.shape[1]
-    shp, i32, f32 = (U, blocks), torch.int32, torch.float32
-    tp = _arg(block_tab, dev, shp, i32, "block_tab")
-    mp = _arg(mass, dev, shp, f32, "mass")
-    lp = _arg(lens, dev, (U,), i32, "lens")
-    st = lib.nosa_quant_evict(
-        C.byref(cfg), blocks, budget, n_recent, tp, mp, lp,
-        tp if tab_out is None else _arg(tab_out, dev, shp, i32, "tab_out"),
-        mp if mass_out is None else _arg(mass_out, dev, shp, f32, "mass_out"),
-        lp if lens_out is None else _arg(lens_out, dev, (U,), i32, "lens_out"),
-        None if order is None else _arg(order, dev, shp, i32, "order"),
-        None if status is None else _arg(status, dev, (1,), i32, "status"),
-        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
-    if st:
-        _check(st)
+    try:
+        dev, U, blocks = cfg.device, cfg.batch * cfg.n_kv_heads, block_tab.shape[1]
+        shp, i32, f32 = (U, blocks), torch.int32, torch.float32
+        tp = _arg(block_tab, dev, shp, i32, "block_tab")
+        mp = _arg(mass, dev, shp, f32, "mass")
+        lp = _arg(lens, dev, (U,), i32, "lens")
+        st = lib.nosa_quant_evict(
+            C.byref(cfg), blocks, budget, n_recent, tp, mp, lp,
+            tp if tab_out is None else _arg(tab_out, dev, shp, i32, "tab_out"),
+            mp if mass_out is None else _arg(mass_out, dev, shp, f32, "mass_out"),
+            lp if lens_out is None else _arg(lens_out, dev, (U,), i32, "lens_out"),
+            None if order is None else _arg(order, dev, shp, i32, "order"),
+            None if status is None else _arg(status, dev, (1,), i32, "status"),
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        if st:
+            _check(st)
+    except (AttributeError, IndexError):
+        _not_tensors(dict(block_tab=block_tab, mass=mass, lens=lens),
+                     dict(tab_out=tab_out, mass_out=mass_out, lens_out=lens_out, order=order, status=status),
+                     dict(block_tab=2))
+        raise
