@@ -1149,3 +1149,104 @@ def test_binding_names_what_is_no_tensor(bad):
                 f(cfg, **{**tensors, name: bad}, **others)
         f(cfg, **tensors, **others)  # and as it should be it runs
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype,batch,hq,hkv,d,lens,T", [
+    ("f32", 2, 8, 2, 128, [333, 64], 3), ("f32", 1, 8, 1, 128, [1000], 2), ("f32", 2, 16, 16, 128, [190, 5], 9), ("f32", 1, 6, 2, 128, [700], 5),
+    ("bf16", 1, 16, 2, 128, [2000], 5), ("bf16", 1, 6, 1, 64, [300], 8)])
+@pytest.mark.parametrize("with_mass", [False, True])
+def test_attention_rows_between_the_tiles(dtype, batch, hq, hkv, d, lens, T, with_mass):
+    """9 to 16 rows in fp32 with d = 128, and row counts just above a tile."""
+    rng = np.random.default_rng(81)
+    c = Cache(rng, dtype, batch, hq, hkv, d, [max(0, n - h) for n in lens for h in range(hkv)]).upload()
+    q = query(rng, batch, T, hq, d, dtype)
+    m0 = rng.random(size=c.tab.shape).astype(np.float32)
+    mass = dev(m0) if with_mass else None
+    out, lse, status = c.run(q, mass=mass, decay=0.5)
+    assert status == 0
+    c.check(q, out, lse, mass0=m0, mass=f64(mass) if with_mass else None, decay=0.5)
+
+
+@pytest.mark.parametrize("hq,T", [(4, 7), (8, 3)])
+def test_attention_long_rings_fp32_16_rows(hq, T):
+    rng = np.random.default_rng(83)
+    hkv, d = 2, 128
+    c = Cache(rng, "f32", 2, hq, hkv, d, [64 * 50] * 4)
+    c.lens = np.array([64 * 1300 + 9, 64 * 700, 64 * 2000 + 63, 40], np.int32)
+    c.cap = 2001
+    c.tab = rng.integers(0, len(c.images), size=(4, c.cap)).astype(np.int32)
+    c.upload()
+    q = query(rng, 2, T, hq, d, "f32")
+    m0 = rng.random(size=c.tab.shape).astype(np.float32)
+    mass = dev(m0)
+    out, lse, status = c.run(q, mass=mass, decay=0.5)
+    assert status == 0
+    c.check(q, out, lse, mass0=m0, mass=f64(mass), decay=0.5)
+    for _ in range(5):
+        m1 = dev(m0)
+        again = c.run(q, mass=m1, decay=0.5, workspace=c.workspace)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and torch.equal(mass, m1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,q_len", [(12, [12, 1, 0, 5]), (9, [2, 4, 9, 8]), (33, [1, 33, 0, 17])])
+def test_attention_tiles_without_rows(dtype, T, q_len):
+    """Several tiles of rows, of which a request's queries fill some or none."""
+    rng = np.random.default_rng(85)
+    c = Cache(rng, dtype, 4, 8, 1, 64, [500, 129, 70, 64]).upload()
+    q = query(rng, 4, T, 8, 64, dtype)
+    m0 = rng.random(size=c.tab.shape).astype(np.float32)
+    mass = dev(m0)
+    out, lse, status = c.run(q, q_len=q_len, mass=mass, decay=0.75)
+    assert status == 0
+    c.check(q, out, lse, q_len=q_len, mass0=m0, mass=f64(mass), decay=0.75)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strides_of_zero(dtype):
+    """Queries, keys and values that are the same for all requests, tokens or heads."""
+    rng = np.random.default_rng(87)
+    batch, hq, hkv, d, T = 3, 4, 2, 64, 5
+    c = Cache(rng, dtype, batch, hq, hkv, d, [200, 65, 128, 7, 300, 64]).upload()
+    for shape in ((1, T, hq, d), (batch, 1, hq, d), (batch, T, 1, d), (1, 1, 1, d)):
+        q = dev(rng.normal(size=shape), DT[dtype]).expand(batch, T, hq, d)
+        out = torch.empty(batch, T, hq, d, dtype=DT[dtype], device="cuda")
+        lse = torch.empty(batch, T, hq, device="cuda")
+        nosa.nosa_quant_attention(c.cfg, c.units, c.t_tab, c.tail, c.t_lens, q, out, lse=lse)
+        c.check(q, out, lse)
+    for n in (9, 66):
+        for shape in ((1, n, hkv, d), (batch, 1, hkv, d), (batch, n, 1, d)):
+            k = dev(rng.normal(size=shape), DT[dtype]).expand(batch, n, hkv, d)
+            res = []
+            for x in (k, k.contiguous()):
+                units = torch.zeros(12, Q.unit_bytes(d), dtype=torch.uint8, device="cuda")
+                tail = torch.zeros(6 * nosa.nosa_payload_bytes(c.cfg), dtype=torch.uint8, device="cuda")
+                lens = torch.full((6,), 60, dtype=torch.int32, device="cuda")
+                nosa.nosa_quant_append(c.cfg, x, x, None, units, dev(np.arange(12).reshape(6, 2)[:, ::-1].astype(np.int32)), tail, lens)
+                res.append((units, tail, lens))
+            assert all(torch.equal(x, y) for x, y in zip(*res)) and res[0][2].tolist() == [60 + n] * 6
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 128)])
+def test_attention_the_longest_table(dtype, d):
+    """16384 blocks and no tail: one block named by every entry, so that the output is the block's and
+    every entry weighs the same."""
+    rng = np.random.default_rng(89)
+    cap = 16384
+    c = Cache(rng, dtype, 1, 4, 2, d, [64, 64], cap=cap)
+    one = c.tokens(0), c.tokens(1)
+    c.tab = np.repeat(c.tab[:, :1], cap, axis=1)
+    c.lens = np.full(2, cap * B, np.int32)
+    c.upload()
+    q = query(rng, 1, 1, 4, d, dtype)
+    mass = torch.zeros(c.tab.shape, device="cuda")
+    out, lse, status = c.run(q, mass=mass, decay=0.0)
+    assert status == 0
+    rel = (cap * B / 16 + 16) * 2.0 ** -23  # the additions' bound, as in Cache.check
+    for u in range(2):
+        K, V, e = one[u]
+        want, wl, _, A, S = Q.attend(f64(q)[0, 0, 2 * u:2 * u + 2], K, V, e, np.full(2, B))
+        dl = 2.0 ** -18 * S
+        assert np.all(np.abs(f64(out)[0, 0, 2 * u:2 * u + 2] - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -10 + 2 * rel + 4 * dl[:, None]) * A)
+        assert np.all(np.abs(f64(lse)[0, 0, 2 * u:2 * u + 2] - wl - np.log(cap)) <= 3 * dl + 2 * rel)
+        assert np.all(np.abs(f64(mass)[u] * cap / 2 - 1) <= 4 * dl.max() + 2 * rel)
