@@ -539,9 +539,11 @@ nosa_status nosa_quant_append(const nosa_config* cfg, int32_t max_blocks, int32_
  * lens - q_len[b] + t + 1 tokens of its unit. Logits are q.k / sqrt(d) + e; a token
  * with e = -inf is masked and contributes nothing whatever its key and value hold.
  * A row that sees no token gives out = 0, lse = -inf. Sums and the softmax are held
- * in fp32. The products take queries exactly (bf16) or with 22 bits (fp32), but for at
- * most 2^-39 of the largest element of a row, and the softmax's weights with 11 bits
- * (bf16) or 22 (fp32), but for at most 2^-39 of the largest weight of a row.
+ * in fp32, its exponentials to 2^-21 of a row's largest. The products take queries
+ * exactly (bf16) or with 22 bits (fp32), but for at most 2^-39 of the largest element of
+ * a row, and the softmax's weights with 11 bits (bf16) or 22 (fp32), but for at most
+ * 2^-39 of the largest weight of a row. Values are summed with the row's largest weight
+ * as 1 before the sum is divided, and that sum has to stay in fp32's range.
  *   q    : device [batch][n_queries][n_q_heads][head_dim] of cfg dtype
  *   out  : the same shape, contiguous (written; rows past q_len[b] are left); it must
  *          not overlap q
@@ -551,7 +553,10 @@ nosa_status nosa_quant_append(const nosa_config* cfg, int32_t max_blocks, int32_
  *          the query heads of the KV head; 0 <= decay <= 1 (0 overwrites).
  *   workspace : device, nosa_quant_attention_workspace_bytes(...) bytes, 256-byte
  *          aligned; scratch that calls on one stream (or graphs that do not overlap)
- *          may share. The size is that of cfg's device.
+ *          may share. The size is that of cfg's device. With mass it is mainly 8 bytes
+ *          for each entry of block_tab and each row (n_queries * n_q_heads / n_kv_heads,
+ *          rounded up to 8, 16 or a multiple of 32): 1 GB for 256 units, 1024 blocks and
+ *          512 rows.
  */
 size_t nosa_quant_attention_workspace_bytes(const nosa_config* cfg, int32_t max_blocks,
                                             int32_t n_queries, int32_t with_mass);

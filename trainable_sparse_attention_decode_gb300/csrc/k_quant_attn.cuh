@@ -20,7 +20,7 @@
 //             still runs, then joins the unit's parts.
 //   weights : with accumulated weights, what the stream noted for each block is added
 //             up relative to the rows' final sums: by the join where one CTA has all
-//             rows of a unit (up to 8), else by a launch of its own.
+//             rows of a unit (up to 8) and the table is short, else by a launch of its own.
 //
 // The products take the tensor cores' 16 x 8 x 16 shape with the codes as the large
 // operand (tokens x dims, dims x tokens) and the rows as the small one: up to 8 rows
@@ -32,21 +32,21 @@
 // what is lost otherwise is at most 2^-39 of the largest. Weights are held in
 // fp32 for the sums and rounded to fp16 (fp32 output: two terms) for the second
 // product, scaled by 2^14 so that weights down to 2^-28 of the largest keep their 11
-// bits. Each slice's product starts from zero and enters the fp32 output with the
+// bits. Each block's product starts from zero and enters the fp32 output with the
 // block's value scale, so neither scale ever multiplies an operand.
 //
 // Measured on GB300 (bytes that the call cannot do without / time, of the measured copy
 // rate of 6793 GB/s):
-//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   669 us   96 %
+//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   668 us   96 %
 //   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB   100 us   85 %
-//   8 units x 131071 tokens, 4 rows                       0.27 GB    49 us   82 %
+//   8 units x 131071 tokens, 4 rows                       0.27 GB    50 us   81 %
 //   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    30 us   69 %
-//   1 unit x 2031 tokens, d = 64, fp32                    0.3 MB    8.0 us
+//   1 unit x 2031 tokens, d = 64, fp32                    0.3 MB    8.1 us
 // The stream itself runs at the copy rate; what is left is fixed: 3.75 us until the
 // first unit has landed (lengths, table, unit: three dependent reads), about 4 us between
 // the first and the last CTA to end, 1.5 us for the last join inside a CTA, 3 us for the
 // join launch after it and 2.5 us for the weights'. With 32 rows (8 drafted tokens of
-// 4 heads, 32 units of 8200 tokens: 40 us; 128 rows over 16 units of 16384 tokens: 98 us)
+// 4 heads, 32 units of 8200 tokens: 41 us; 128 rows over 16 units of 16384 tokens: 99 us)
 // the products' instructions bound it: about 1300 of a warp and block at 1.7 a cycle, six
 // consumer warps being all that the outputs' registers leave room for.
 #pragma once
@@ -871,8 +871,8 @@ constexpr int kQcRows = 8;
 // four schedulers, which leaves 48 registers a thread here (40 where the stream's are
 // fp32): the values are then loaded after the keys are done with. Measured on GB300, us
 // (64 registers): 32 units x 1000 tokens 10.0 (14.3), 128 x 3000 17.3 (21.8), fp32 8 x 3000
-// 9.2 (15.0). At d = 128 there is room for 80
-// beside a bf16 stream, and the values come along with the keys.
+// 9.2 (15.0). (At 40 registers 20 bytes spill, outside the loops.) At d = 128 there is room for
+// 80 beside a bf16 stream, and the values come along with the keys.
 template <typename T, int D> constexpr int kQcPerSm = D == 64 ? (sizeof(T) == 4 ? 6 : 5) : 3;
 
 template <typename T, int D>

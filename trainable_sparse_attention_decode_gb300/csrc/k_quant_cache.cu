@@ -4,7 +4,7 @@
 // prompt (GB300: 4 x 8192 tokens of 8 heads of 128 in bf16, 203 MB, 35.4 us = 85 % of the
 // measured copy rate; what is left is the lengths' read ahead of the block's and the
 // CTAs' barriers), latency a token (32 requests of 8 heads, every fourth completing a
-// block: 4.4 us) and an eviction (256 units: one of 129 blocks 4.7 us, 1024 blocks down
+// block: 4.8 us) and an eviction (256 units: one of 129 blocks 4.7 us, 1024 blocks down
 // to 64 7.2 us).
 #include "k_quant.cuh"
 
