@@ -487,7 +487,9 @@ nosa_status nosa_sparse_attention_noalloc(const nosa_config* cfg, const void* un
  *   bytes [128 d, +256)   : fp32 eviction logits of the 64 tokens
  *   then fp32 key scale, fp32 value scale, zeros to a multiple of 32 bytes.
  * A code is an e4m3 number (4 exponent bits, 3 mantissa bits, largest 448) and
- * stands for code * scale.
+ * stands for code * scale. (0x7F and 0xFF, which are no numbers and which
+ * nosa_quant_append never writes, count as NaN in a token that is not masked. In a
+ * masked one they count for nothing, but cost the attention time.)
  *
  * Device status: calls take `status`, a device int32 word or NULL, and OR bits into
  * it (they never clear it): NOSA_QUANT_WAIT a bounded wait in a kernel gave up,

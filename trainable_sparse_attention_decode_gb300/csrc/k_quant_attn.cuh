@@ -321,18 +321,32 @@ __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0
   constexpr int DL = D / 32;  // dims of a lane
   const int b = u / p.Hkv, h = u % p.Hkv, lane = threadIdx.x & 31;
   const int n = max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)), qn = quant_count(p.q_len, b, p.T, nullptr, false);
+  auto block = [&](int j) -> const uint8_t* {  // null: the table names no unit
+    const int idx = p.tab[(long long)u * p.max_blocks + j];
+    return idx < 0 || (long long)idx >= p.n_units ? nullptr : p.units + (long long)idx * quant_unit_bytes(D);
+  };
 #pragma unroll 1
   for (int r = 0; r < WR; ++r) {
     const QRow w = qa_row(first + r, p.G, n, qn);
     const float mu = finite_max(ml[r].x);
     if (w.sees == 0 || isnan(mu)) continue;
+    bool due = false;  // a scale is NaN, and the row sees a token of its block
+#pragma unroll 1
+    for (int j = j0 + lane * IS; j < j1; j += 32 * IS) {
+      const uint8_t* unit = block(j);
+      if (unit == nullptr) continue;
+      const float* es = reinterpret_cast<const float*>(unit + quant_e_off(D));
+      if (!isnan(es[kQB + 1])) continue;
+#pragma unroll 1
+      for (int t = 0; t < kQB; ++t) due |= es[t] != -INFINITY && j * kQB + t < w.sees;
+    }
+    if (__any_sync(0xffffffffu, due)) continue;
     const T* q = static_cast<const T*>(p.q) + b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h;
     float acc[DL] = {};
 #pragma unroll 1
     for (int j = j0; j < j1; j += IS) {
-      const int idx = p.tab[(long long)u * p.max_blocks + j];
-      if (idx < 0 || (long long)idx >= p.n_units) continue;
-      const uint8_t* unit = p.units + (long long)idx * quant_unit_bytes(D);
+      const uint8_t* unit = block(j);
+      if (unit == nullptr) continue;
       const float* es = reinterpret_cast<const float*>(unit + quant_e_off(D));
       float wt[2];  // the lane's tokens lane and lane + 32; -1: masked or not seen
 #pragma unroll
@@ -370,7 +384,6 @@ __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0
       if (!any) continue;
 #pragma unroll
       for (int x = 0; x < DL; ++x) acc[x] += sum[x] * es[kQB + 1];
-      if (isnan(es[kQB + 1])) break;
     }
 #pragma unroll
     for (int x = 0; x < DL; ++x) {
