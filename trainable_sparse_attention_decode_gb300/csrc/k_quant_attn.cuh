@@ -46,7 +46,7 @@
 // first unit has landed (lengths, table, unit: three dependent reads), about 4 us between
 // the first and the last CTA to end, 1.5 us for the last join inside a CTA, 3 us for the
 // join launch after it and 2.5 us for the weights'. With 32 rows (8 drafted tokens of
-// 4 heads, 32 units of 8200 tokens: 41 us; 128 rows over 16 units of 16384 tokens: 99 us)
+// 4 heads, 32 units of 8200 tokens: 41 us; 128 rows over 16 units of 16384 tokens: 98 us)
 // the products' instructions bound it: about 1300 of a warp and block at 1.7 a cycle, six
 // consumer warps being all that the outputs' registers leave room for.
 #pragma once
@@ -393,6 +393,15 @@ __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0
   }
 }
 
+// First items of a thread's units, where the join does not add them up itself (out of line: 32 rows
+// over 32 units of 8200 tokens 40.7 us, with the loop in the kernel 41.1).
+static __device__ __noinline__ void qa_places(const QStreamParams& p, int a0, int a1, long long at) {
+  for (int u = a0; u < a1; ++u) {
+    p.base[u] = at;
+    at += max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
+  }
+}
+
 template <int D, int NT, int RG, bool F32>
 __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_kernel(QStreamParams p) {
   using Gm = QGeom<D, NT, RG, F32>;
@@ -451,13 +460,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  if (p.U > kQcScan * kQcThreads) {  // each unit's place by one of the CTAs
-    long long at = before;
-    for (int u = a0; u < a1; ++u) {
-      if (u % p.ctas == cta) p.base[u] = at;
-      at += max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
-    }
-  }
+  if (p.U > kQcScan * kQcThreads && tid % p.ctas == cta) qa_places(p, a0, a1, before);  // (a thread's by one of the CTAs)
   total *= p.tiles;
   before *= p.tiles;
   if (cta == 0 && tid == 0) *p.total = total;
