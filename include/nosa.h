@@ -585,6 +585,134 @@ nosa_status nosa_quant_evict(const nosa_config* cfg, int32_t max_blocks, int32_t
                              const int32_t* lens, int32_t* tab_out, float* mass_out,
                              int32_t* lens_out, int32_t* order, int32_t* status, void* stream);
 
+/*
+ * Rotary positions. Pair i of a row (a query or key head of a token) turns by the angle
+ * that the position of its axis has in the table:
+ *     a' = a cos - b sin,  b' = b cos + a sin
+ * in fp32, each product and sum rounded on its own, then rounded to cfg's dtype. Dims from
+ * rot_dim on are left. (The NOSA pages have no counterpart: they start from rotated
+ * queries and keys.)
+ *   table       : device fp32 [table_len][rot_dim / 2][2], 16-byte aligned: cosine and sine
+ *                 of pair i at each position, with whatever frequencies and scaling
+ *   rot_dim     : a multiple of 16, at most head_dim
+ *   interleaved : 0: pair i is dims (i, i + rot_dim / 2); else (2 i, 2 i + 1)
+ *   n_axes      : 1 to 4 axes of positions (text; time, height and width of a video)
+ *   axes        : host [rot_dim / 2], the axis of each pair, or NULL: all 0
+ * Positions are a device int32 [n_axes][batch][n_tokens] array given with each call. One
+ * outside [0, table_len) is flagged (NOSA_QUANT_INDEX in `status`) and clamped.
+ */
+typedef struct {
+  const float* table;
+  int32_t table_len;
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t n_axes;
+  const int32_t* axes;
+} nosa_rope;
+
+/*
+ * Rotates query and key rows, in place or into other arrays: before nosa_append_kv,
+ * nosa_decode_step or nosa_prefill_forward, whose q and k it has the layout of. Async.
+ *   q, q_out : device [batch][n_tokens][n_q_heads][head_dim] of cfg dtype, or both NULL
+ *   k, k_out : device [batch][n_tokens][n_kv_heads][head_dim], or both NULL
+ *   *_strides: as for the caches (elements between requests, tokens, heads; NULL:
+ *              contiguous); an output's may not be 0 along a dimension of more than one
+ *              element
+ *   backward : nonzero: the transpose (sin negated), which takes gradients of the rotated
+ *              rows to gradients of q and k
+ *   status   : device int32 word or NULL
+ * An output is its input (with the same strides) or does not overlap any of the inputs.
+ * Only the shape fields of cfg and its dtype and device are used.
+ */
+nosa_status nosa_rotate(const nosa_config* cfg, const nosa_rope* rope, const int32_t* positions,
+                        int32_t n_tokens, const void* q, const int64_t* q_strides, void* q_out,
+                        const int64_t* q_out_strides, const void* k, const int64_t* k_strides,
+                        void* k_out, const int64_t* k_out_strides, int32_t backward,
+                        int32_t* status, void* stream);
+
+/*
+ * 4-bit block cache: as the 8-bit one (its state, status bits, strides and rules, and
+ * nosa_quant_evict serves both), with full blocks in 4 bits: 0.56 of the 8-bit unit's
+ * bytes. A code n in 0..15 stands for (step * n + zero) * scale:
+ *   keys   : a step and a zero for each channel (dim) of the block
+ *   values : a step and a zero for each token and run of 64 dims
+ * and one scale each for the block's keys and values.
+ *
+ * 4-bit unit (d = head_dim; 4832 bytes for d = 64, 9376 for d = 128). With tt = t % 16,
+ * word (m, lane, w) is the 4 bytes at 512 m + 16 lane + 4 w, nibble y its bits 4 y to 4 y + 3:
+ *   bytes [0, 32 d)    : key codes. Token t, dim x: word (x / 16, 4 (2 (tt / 4) + tt % 2) +
+ *                        x % 16 / 4, t / 16), nibble tt % 4 / 2 + 2 (x % 4 / 2) + 4 (x % 2)
+ *   bytes [32 d, +32 d): value codes. Token t, dim x: word (x / 16, 4 (x % 8) + tt / 4,
+ *                        t / 16), nibble x % 16 / 8 + 2 (t % 4 / 2) + 4 (t % 2)
+ *   bytes [64 d, +d)   : steps of the keys, one byte each: the upper byte of an fp16 number
+ *                        whose lower byte is 0; that of dim x is number
+ *                        o(x, d) = 4 (x % 16 / 4 * (d / 16) + x / 16) + x % 4
+ *   bytes [65 d, +2 d) : zeros of the keys, fp16, in the same order
+ *   bytes [67 d, +2 d) : steps of the values, fp16: that of token t and run r of 64 dims is
+ *                        number 64 r + o(t, 64)
+ *   bytes [69 d, +2 d) : zeros of the values, fp16, in the same order
+ *   bytes [71 d, +256) : fp32 eviction logits of the 64 tokens
+ *   then fp32 key scale, fp32 value scale, zeros to a multiple of 32 bytes.
+ * Steps are not negative. (What a masked token's steps, zeros and codes hold does not
+ * count, but costs the attention time where a value's step or zero is no number.)
+ */
+size_t nosa_quant4_unit_bytes(const nosa_config* cfg);
+
+/*
+ * nosa_quant_append into 4-bit units, with the keys rotated on the way (rope NULL: as they
+ * are): what enters the tail and the blocks is bit for bit what nosa_rotate makes of k.
+ * positions as above, for n_tokens tokens of each request; those past n_new are not read. A
+ * block that fills up is quantised from its tokens in cfg's dtype, masked ones (logit
+ * -inf) left out:
+ *   scale : 2^(p - 2) where 2^p <= max |x| < 2^(p + 1); 0 (and zeros everywhere) below
+ *           2^-100; NaN where an element is not finite (the block's keys or values are then
+ *           NaN, and so is what attends to it)
+ *   zero  : the group's least x / scale, rounded down to fp16
+ *   step  : (its largest - zero) / 15, rounded up to fp16 (keys: with two fraction bits)
+ *   code  : (x / scale - zero) * r, r the fp32 number nearest to 1 / step, to the nearest
+ *           integer, ties to even; 0 in tokens left out
+ * where the differences, and the product with the fp32 number nearest to 1 / 15 that the
+ * division by 15 is, are rounded to fp32. Other arguments and rules as nosa_quant_append.
+ */
+nosa_status nosa_quant4_append(const nosa_config* cfg, int32_t max_blocks, int32_t n_tokens,
+                               const void* k, const int64_t* k_strides, const void* v,
+                               const int64_t* v_strides, const float* e, const int32_t* n_new,
+                               const nosa_rope* rope, const int32_t* positions, void* units,
+                               int64_t n_units, const int32_t* block_tab, void* tail,
+                               const int32_t* lens, int32_t* lens_out, int32_t* status,
+                               void* stream);
+
+/*
+ * Reads blocks back as tokens: block i of the outputs is unit ids[i] (ids NULL: unit i),
+ * each element (step * n + zero) * scale rounded to cfg's dtype, masked tokens zeros. Async.
+ *   ids   : device int32 [n] or NULL (then n <= n_units); an id out of range is flagged and
+ *           its block of the outputs left as it was. The same id may come more than once.
+ *   k_out, v_out : device [n][64][head_dim] of cfg dtype, each may be NULL
+ *   e_out : device fp32 [n][64], the tokens' logits, or NULL
+ */
+nosa_status nosa_quant4_read(const nosa_config* cfg, const void* units, int64_t n_units,
+                             const int32_t* ids, int64_t n, void* k_out, void* v_out,
+                             float* e_out, int32_t* status, void* stream);
+
+/*
+ * nosa_quant_attention over 4-bit units, with the queries rotated on the way (rope NULL: as
+ * they are): a row's products take bit for bit what nosa_rotate makes of it. positions as
+ * above, for n_queries tokens of each request; those past q_len are not read. Logits are
+ * held as precisely as with nosa_quant_attention (the product of a bf16 query element and a
+ * key's step is exact, that of an fp32 one keeps 22 bits); a weight times the step of a
+ * value is rounded to 11 bits (bf16 calls) or 22 (fp32). Other arguments and rules as
+ * nosa_quant_attention.
+ */
+size_t nosa_quant4_attention_workspace_bytes(const nosa_config* cfg, int32_t max_blocks,
+                                             int32_t n_queries, int32_t with_mass);
+nosa_status nosa_quant4_attention(const nosa_config* cfg, int32_t max_blocks, int32_t n_queries,
+                                  const void* units, int64_t n_units, const int32_t* block_tab,
+                                  const void* tail, const int32_t* lens, const void* q,
+                                  const int64_t* q_strides, const int32_t* q_len,
+                                  const nosa_rope* rope, const int32_t* positions, void* out,
+                                  float* lse, float* mass, float decay, void* workspace,
+                                  size_t workspace_bytes, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

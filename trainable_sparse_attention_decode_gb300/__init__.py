@@ -27,7 +27,9 @@ __all__ = [
     "nosa_prefill_forward", "nosa_prefill_device_error", "nosa_prefill_timing",
     "nosa_numa_choose", "NOSA_QUANT_WAIT", "NOSA_QUANT_INDEX", "NOSA_QUANT_CAPACITY",
     "nosa_quant_unit_bytes", "nosa_quant_append", "nosa_quant_attention_workspace_bytes",
-    "nosa_quant_attention", "nosa_quant_evict",
+    "nosa_quant_attention", "nosa_quant_evict", "NosaRope", "nosa_rope", "nosa_rotate",
+    "nosa_quant4_unit_bytes", "nosa_quant4_append", "nosa_quant4_read",
+    "nosa_quant4_attention_workspace_bytes", "nosa_quant4_attention",
 ]
 
 NOSA_F32, NOSA_BF16 = 0, 1
@@ -67,6 +69,11 @@ class NosaStats(C.Structure):
                 ("host_numa_node", C.c_int32),
                 ("t_us", C.c_double * 8), ("t_count", C.c_int64), ("launches", C.c_int64),
                 ("host_store_kind", C.c_int32), ("host_store_pinned", C.c_int32)]
+
+
+class _Rope(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("table_len", C.c_int32), ("rot_dim", C.c_int32),
+                ("interleaved", C.c_int32), ("n_axes", C.c_int32), ("axes", C.POINTER(C.c_int32))]
 
 
 def _load():
@@ -112,6 +119,17 @@ def _load():
                                            VP, VP, VP, VP, VP, C.c_float, VP, SZ, VP, VP]),
         "nosa_quant_evict": (C.c_int, [P(NosaConfig), I32, I32, I32, VP, VP, VP, VP, VP, VP, VP,
                                        VP, VP]),
+        "nosa_rotate": (C.c_int, [P(NosaConfig), P(_Rope), VP, I32, VP, VP, VP, VP, VP, VP, VP, VP,
+                                  I32, VP, VP]),
+        "nosa_quant4_unit_bytes": (SZ, [P(NosaConfig)]),
+        "nosa_quant4_append": (C.c_int, [P(NosaConfig), I32, I32, VP, VP, VP, VP, VP, VP, P(_Rope), VP,
+                                         VP, C.c_int64, VP, VP, VP, VP, VP, VP]),
+        "nosa_quant4_read": (C.c_int, [P(NosaConfig), VP, C.c_int64, VP, C.c_int64, VP, VP, VP, VP,
+                                       VP]),
+        "nosa_quant4_attention_workspace_bytes": (SZ, [P(NosaConfig), I32, I32, I32]),
+        "nosa_quant4_attention": (C.c_int, [P(NosaConfig), I32, I32, VP, C.c_int64, VP, VP, VP, VP,
+                                            VP, VP, P(_Rope), VP, VP, VP, VP, C.c_float, VP, SZ, VP,
+                                            VP]),
     }
     for name, (res, args) in sigs.items():
         f = getattr(L, name)
@@ -480,10 +498,11 @@ def _rows(t, device, shape, dtype, what):
             (C.c_int64 * 3)(*(s if n > 1 else 0 for s, n in zip(st[:3], shape))))
 
 
-def _cache_args(units, block_tab, tail, lens, device, d, elt, U, blocks, torch):
+def _cache_args(units, block_tab, tail, lens, device, d, elt, U, blocks, torch, bits=8):
     """(units, number of units, block_tab, tail, lens) of a cache, checked."""
     u8, i32 = torch.uint8, torch.int32
-    size = (128 * d + 295) // 32 * 32                 # nosa_quant_unit_bytes
+    # nosa_quant_unit_bytes, nosa_quant4_unit_bytes
+    size = (128 * d + 295) // 32 * 32 if bits == 8 else (71 * d + 295) // 32 * 32
     n = units.numel()
     if n % size:
         raise ValueError(f"units must hold whole units of {size} bytes")
@@ -595,4 +614,193 @@ def nosa_quant_evict(cfg: NosaConfig, budget, n_recent, block_tab, mass, lens, t
         _not_tensors(dict(block_tab=block_tab, mass=mass, lens=lens),
                      dict(tab_out=tab_out, mass_out=mass_out, lens_out=lens_out, order=order, status=status),
                      dict(block_tab=2))
+        raise
+
+
+# ---------------------------------------------------------------------------
+# rotary positions and the 4-bit block cache
+# ---------------------------------------------------------------------------
+class NosaRope:
+    """A rotation: its table and how rows pair up. It keeps the table alive."""
+
+    def __init__(self, table, axes, interleaved):
+        torch = _torch()
+        if not isinstance(table, torch.Tensor) or table.ndim != 3 or table.shape[2] != 2:
+            raise ValueError("table must be a [positions][rot_dim / 2][2] CUDA tensor")
+        self.table, self.device = table, table.get_device()
+        self.pairs = table.shape[1]
+        axes = [0] * self.pairs if axes is None else [int(a) for a in axes]
+        if len(axes) != self.pairs:
+            raise ValueError(f"axes must have {self.pairs} entries, one for each pair")
+        self.n_axes = max(axes, default=0) + 1
+        self._axes = (C.c_int32 * len(axes))(*axes)
+        self.c = _Rope(_ptr(table, None, torch.float32, "table"), table.shape[0], 2 * self.pairs,
+                       1 if interleaved else 0, self.n_axes, self._axes)
+        self.ref = C.byref(self.c)
+
+
+def nosa_rope(table, axes=None, interleaved=False) -> NosaRope:
+    """A rotation from table [positions][rot_dim / 2][2] fp32 (cosine and sine of each pair), the
+    axis of each pair (None: one axis), and the pairing: halves, or neighbours if interleaved."""
+    return NosaRope(table, axes, interleaved)
+
+
+def _turn(rope, positions, device, batch, n, torch):
+    """(reference to the C struct, pointer to the positions) of a call's rotation, or two Nones."""
+    if rope is None:
+        if positions is not None:
+            raise ValueError("positions without a rope")
+        return None, None
+    if not isinstance(rope, NosaRope):
+        raise ValueError("rope must be made by nosa_rope")
+    if rope.device != device:
+        raise ValueError(f"the rope's table is on cuda:{rope.device}, the configuration's device is cuda:{device}")
+    if positions is None:
+        raise ValueError("positions is required")
+    shape = (batch, n) if rope.n_axes == 1 and positions.ndim == 2 else (rope.n_axes, batch, n)
+    return rope.ref, _arg(positions, device, shape, torch.int32, "positions")
+
+
+def nosa_rotate(cfg: NosaConfig, rope: NosaRope, positions, q, k=None, q_out=None, k_out=None, backward=False,
+                status=None, stream=None):
+    """Rotates q [batch][n][Hq][d] and k [batch][n][Hkv][d] (either may be None; rows may be strided)
+    by positions [axes][batch][n] int32 ([batch][n] for one axis), in place unless outputs are given.
+    backward: the transpose, for gradients."""
+    torch = _torch()
+    try:
+        dev, batch, d = cfg.device, cfg.batch, cfg.head_dim
+        dt = torch.float32 if cfg.dtype == NOSA_F32 else torch.bfloat16
+        if q is None and k is None:
+            raise ValueError("q or k is required")
+        if rope is None:
+            raise ValueError("rope is required")
+        if (q is None and q_out is not None) or (k is None and k_out is not None):
+            raise ValueError("an output without its input")
+        n = (k if q is None else q).shape[1]
+        ref, pos = _turn(rope, positions, dev, batch, n, torch)
+        args = []
+        for x, y, heads, what in ((q, q_out, cfg.n_q_heads, "q"), (k, k_out, cfg.n_kv_heads, "k")):
+            if x is None:
+                args += (None, None, None, None)
+                continue
+            shp = (batch, n, heads, d)
+            xp = _rows(x, dev, shp, dt, what)
+            args += xp
+            args += xp if y is None or y is x else _rows(y, dev, shp, dt, what + "_out")
+        st = lib.nosa_rotate(
+            C.byref(cfg), ref, pos, n, *args, 1 if backward else 0,
+            None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        if st:
+            _check(st)
+    except (AttributeError, IndexError):
+        req = {w: x for w, x in (("q", q), ("k", k)) if x is not None}
+        _not_tensors(dict(req, positions=positions), dict(q_out=q_out, k_out=k_out, status=status), {w: 4 for w in req})
+        raise
+
+
+def nosa_quant4_unit_bytes(cfg: NosaConfig) -> int:
+    return int(lib.nosa_quant4_unit_bytes(C.byref(cfg)))
+
+
+def nosa_quant4_append(cfg: NosaConfig, k, v, e, units, block_tab, tail, lens, lens_out=None, n_new=None,
+                       rope=None, positions=None, status=None, stream=None):
+    """nosa_quant_append for a cache of 4-bit units; with rope and positions [axes][batch][n] int32 the
+    keys are rotated on the way."""
+    torch = _torch()
+    try:
+        dev, batch, hkv, d = cfg.device, cfg.batch, cfg.n_kv_heads, cfg.head_dim
+        dt, elt = (torch.float32, 4) if cfg.dtype == NOSA_F32 else (torch.bfloat16, 2)
+        n, blocks, U = k.shape[1], block_tab.shape[1], batch * hkv
+        shp = (batch, n, hkv, d)
+        kp, ks = _rows(k, dev, shp, dt, "k")
+        vp, vs = _rows(v, dev, shp, dt, "v")
+        ref, pos = _turn(rope, positions, dev, batch, n, torch)
+        up, nu, tab, tl, lp = _cache_args(units, block_tab, tail, lens, dev, d, elt, U, blocks, torch, 4)
+        st = lib.nosa_quant4_append(
+            C.byref(cfg), blocks, n, kp, ks, vp, vs,
+            None if e is None else _arg(e, dev, shp[:3], torch.float32, "e"),
+            None if n_new is None else _arg(n_new, dev, (batch,), torch.int32, "n_new"),
+            ref, pos, up, nu, tab, tl, lp,
+            lp if lens_out is None else _arg(lens_out, dev, (U,), torch.int32, "lens_out"),
+            None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        if st:
+            _check(st)
+    except (AttributeError, IndexError):
+        _not_tensors(dict(k=k, v=v, units=units, block_tab=block_tab, tail=tail, lens=lens),
+                     dict(e=e, lens_out=lens_out, n_new=n_new, positions=positions, status=status),
+                     dict(k=4, v=4, block_tab=2))
+        raise
+
+
+def nosa_quant4_read(cfg: NosaConfig, units, k_out=None, v_out=None, e_out=None, ids=None, status=None, stream=None):
+    """Reads 4-bit units back as tokens: block i of k_out, v_out [n][64][d] (and e_out [n][64] fp32) is
+    unit ids[i] (int32; None: unit i). Each output may be None."""
+    torch = _torch()
+    outs = dict(k_out=k_out, v_out=v_out, e_out=e_out)
+    try:
+        dev, d = cfg.device, cfg.head_dim
+        dt = torch.float32 if cfg.dtype == NOSA_F32 else torch.bfloat16
+        size = (71 * d + 295) // 32 * 32  # nosa_quant4_unit_bytes
+        count = units.numel()
+        if count % size:
+            raise ValueError(f"units must hold whole units of {size} bytes")
+        given = [x for x in outs.values() if x is not None]
+        if not given:
+            raise ValueError("k_out, v_out or e_out is required")
+        n = given[0].shape[0] if ids is None else ids.shape[0]
+        st = lib.nosa_quant4_read(
+            C.byref(cfg), _buffer(units, dev, torch.uint8, "units", 16), count // size,
+            None if ids is None else _arg(ids, dev, (n,), torch.int32, "ids"), n,
+            None if k_out is None else _arg(k_out, dev, (n, 64, d), dt, "k_out", 16),
+            None if v_out is None else _arg(v_out, dev, (n, 64, d), dt, "v_out", 16),
+            None if e_out is None else _arg(e_out, dev, (n, 64), torch.float32, "e_out"),
+            None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        if st:
+            _check(st)
+    except (AttributeError, IndexError):
+        _not_tensors(dict(units=units), dict(outs, ids=ids, status=status), {})
+        raise
+
+
+def nosa_quant4_attention_workspace_bytes(cfg: NosaConfig, max_blocks: int, n_queries: int = 1,
+                                          with_mass: bool = False) -> int:
+    return int(lib.nosa_quant4_attention_workspace_bytes(C.byref(cfg), max_blocks, n_queries,
+                                                         1 if with_mass else 0))
+
+
+def nosa_quant4_attention(cfg: NosaConfig, units, block_tab, tail, lens, q, out, lse=None, mass=None, decay=1.0,
+                          q_len=None, rope=None, positions=None, workspace=None, status=None, stream=None):
+    """nosa_quant_attention over a cache of 4-bit units; with rope and positions [axes][batch][n] int32
+    the queries are rotated on the way. Returns the workspace (allocated here when not passed)."""
+    torch = _torch()
+    try:
+        dev, batch, d = cfg.device, cfg.batch, cfg.head_dim
+        dt, elt = (torch.float32, 4) if cfg.dtype == NOSA_F32 else (torch.bfloat16, 2)
+        n, blocks, U = q.shape[1], block_tab.shape[1], batch * cfg.n_kv_heads
+        shp = (batch, n, cfg.n_q_heads, d)
+        qp, qs = _rows(q, dev, shp, dt, "q")
+        ref, pos = _turn(rope, positions, dev, batch, n, torch)
+        up, nu, tab, tl, lp = _cache_args(units, block_tab, tail, lens, dev, d, elt, U, blocks, torch, 4)
+        if workspace is None:
+            workspace = _workspace(nosa_quant4_attention_workspace_bytes(cfg, blocks, n, mass is not None),
+                                   q.device, stream)
+        st = lib.nosa_quant4_attention(
+            C.byref(cfg), blocks, n, up, nu, tab, tl, lp, qp, qs,
+            None if q_len is None else _arg(q_len, dev, (batch,), torch.int32, "q_len"), ref, pos,
+            _arg(out, dev, shp, dt, "out", 16),
+            None if lse is None else _arg(lse, dev, shp[:3], torch.float32, "lse"),
+            None if mass is None else _arg(mass, dev, (U, blocks), torch.float32, "mass"), decay,
+            _buffer(workspace, dev, torch.uint8, "workspace", 256), workspace.numel(),
+            None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
+            torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+        if st:
+            _check(st)
+        return workspace
+    except (AttributeError, IndexError):
+        _not_tensors(dict(q=q, out=out, units=units, block_tab=block_tab, tail=tail, lens=lens),
+                     dict(lse=lse, mass=mass, q_len=q_len, positions=positions, workspace=workspace, status=status),
+                     dict(q=4, block_tab=2))
         raise
