@@ -21,6 +21,8 @@
 #include "k_quant.cuh"
 #include "k_rope.cuh"
 
+#include <cuda_fp16.h>
+
 namespace nosa {
 
 __host__ __device__ constexpr int quant4_kstep_off(int d) { return 64 * d; }   // e5m2 bytes [d]
@@ -60,12 +62,32 @@ struct Q4ReadArgs {
 };
 cudaError_t launch_quant4_append(const Shape& s, const Q4AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_quant4_read(const Shape& s, const Q4ReadArgs& a, cudaStream_t stream);
-size_t quant4_attn_workspace(const Shape& s, int max_blocks, int T, bool mass);
 cudaError_t launch_quant4_attention(const Shape& s, const QAttnArgs& a, const RopeArgs& rope, cudaStream_t stream);
 
 #ifdef __CUDACC__
-#include <cuda_fp16.h>
 __device__ __forceinline__ float half_bits(uint32_t b) { return __half2float(__ushort_as_half((unsigned short)b)); }
+
+// Keys (token t, dims x .. x + 3) and values (tokens t .. t + 3, dim x) of a unit, without
+// the block's scale; x (t) a multiple of 4.
+template <int D>
+__device__ __forceinline__ void quant4_keys(const uint8_t* unit, int t, int x, float* f) {
+  const int bit = quant4_k_bit(t, x), o = quant4_order(x, D);  // (nibbles 0, 4, 2, 6 from there)
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(unit + bit / 32 * 4) >> (bit % 32);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f[i] = fmaf(half_bits(unit[quant4_kstep_off(D) + o + i] << 8), (float)(w >> (16 * (i % 2) + 8 * (i / 2)) & 15),
+                half_bits(reinterpret_cast<const unsigned short*>(unit + quant4_kzero_off(D))[o + i]));
+}
+template <int D>
+__device__ __forceinline__ void quant4_values(const uint8_t* unit, int t, int x, float* f) {
+  const int bit = quant4_v_bit(t, x), o = x / 64 * kQB + quant4_order(t, kQB);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(unit + 32 * D + bit / 32 * 4) >> (bit % 32);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f[i] = fmaf(half_bits(reinterpret_cast<const unsigned short*>(unit + quant4_vstep_off(D))[o + i]),
+                (float)(w >> (16 * (i % 2) + 8 * (i / 2)) & 15),
+                half_bits(reinterpret_cast<const unsigned short*>(unit + quant4_vzero_off(D))[o + i]));
+}
 #endif
 
 }  // namespace nosa

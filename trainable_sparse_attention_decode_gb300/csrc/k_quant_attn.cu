@@ -1,4 +1,4 @@
-// Plan, workspace and dispatch of the attention over the 8-bit block cache.
+// Plan, workspace and dispatch of the attention over the 8-bit and 4-bit block caches.
 #include "k_quant_attn.cuh"
 
 namespace nosa {
@@ -54,8 +54,7 @@ size_t quant_attn_workspace(const Shape& s, int max_blocks, int T, bool mass) {
   return layout(s, quant_attn_plan(s, T), max_blocks, mass).total;
 }
 
-cudaError_t launch_quant_attention(const Shape& s, const QAttnArgs& a, cudaStream_t stream) {
-  const QPlan pl = quant_attn_plan(s, a.T);
+static QStreamParams stream_params(const Shape& s, const QPlan& pl, const QAttnArgs& a) {
   const Layout w = layout(s, pl, a.max_blocks, a.mass != nullptr);
   QStreamParams p{};
   p.units = a.units;
@@ -88,7 +87,20 @@ cudaError_t launch_quant_attention(const Shape& s, const QAttnArgs& a, cudaStrea
   p.rowstat = reinterpret_cast<float2*>(a.ws + w.rowstat);
   p.tail_w = reinterpret_cast<float*>(a.ws + w.tail_w);
   p.blk = a.mass != nullptr ? reinterpret_cast<float2*>(a.ws + w.blk) : nullptr;
+  return p;
+}
+
+cudaError_t launch_quant_attention(const Shape& s, const QAttnArgs& a, cudaStream_t stream) {
+  const QPlan pl = quant_attn_plan(s, a.T);
+  const QStreamParams p = stream_params(s, pl, a);
   return s.dtype == 0 ? launch_quant_stream_f32(s, pl, p, stream) : launch_quant_stream_bf16(s, pl, p, stream);
+}
+
+cudaError_t launch_quant4_attention(const Shape& s, const QAttnArgs& a, const RopeArgs& rope, cudaStream_t stream) {
+  const QPlan pl = quant_attn_plan(s, a.T);
+  QStreamParams p = stream_params(s, pl, a);
+  p.rope = rope;
+  return s.dtype == 0 ? launch_quant4_stream_f32(s, pl, p, stream) : launch_quant4_stream_bf16(s, pl, p, stream);
 }
 
 }  // namespace nosa

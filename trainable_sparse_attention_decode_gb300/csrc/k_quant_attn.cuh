@@ -51,7 +51,7 @@
 // consumer warps being all that the outputs' registers leave room for.
 #pragma once
 
-#include "k_quant.cuh"
+#include "k_quant4.cuh"
 
 #include <cuda_fp16.h>
 
@@ -75,6 +75,7 @@ struct QStreamParams {
   QStrides qs;
   int T;
   const int32_t* q_len;
+  RopeArgs rope;  // turns the queries (4-bit cache)
   int U, Hkv, Hq, G, tiles;
   const uint8_t* tail;
   long long payload;
@@ -94,6 +95,10 @@ struct QStreamParams {
   float* tail_w;      // [units x tiles][rows] weight of the tail
   float2* blk;        // [units x tiles][max_blocks][rows] maximum and sum of a block, or null (no weights asked for)
 };
+
+// Units of the two caches.
+template <int D, int BITS> constexpr int kQUnitBytes = BITS == 8 ? quant_unit_bytes(D) : quant4_unit_bytes(D);
+template <int D, int BITS> constexpr int kQLogits = BITS == 8 ? quant_e_off(D) : quant4_e_off(D);
 
 // 1 / sqrt(d)
 template <int D> constexpr float kQScale = D == 64 ? 0.125f : 0.08838834764831845f;
@@ -129,6 +134,23 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
+// A word of eight 4-bit codes as the four A operand registers of a 16 x 16 x 8 tile, without a
+// conversion: n as the subnormal fp16 number 2^-24 n in the tile's rows 0..7, 2^-20 n in 8..15.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t* a) {
+  const uint32_t x = w >> 8;
+  a[0] = w & 0x000F000Fu;
+  a[1] = w & 0x00F000F0u;
+  a[2] = x & 0x000F000Fu;
+  a[3] = x & 0x00F000F0u;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t word_of(uint4 v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+// Four of a unit's steps of keys (bytes of a word) as fp16: two registers.
+__device__ __forceinline__ uint2 steps_f16(uint32_t w) { return make_uint2(__byte_perm(w, 0, 0x1404), __byte_perm(w, 0, 0x3424)); }
+
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -178,25 +200,26 @@ __device__ __forceinline__ QRow qa_row(int r, int G, int n, int qn) {
 // same readers. Copies may land out of order, and a barrier's parity tells a phase only
 // from its neighbours, so a warp may wait for a stage's next fill only after it has seen
 // the fill before.
-template <int D, int NT, int RG, bool F32>
+template <int D, int NT, int RG, bool F32, int BITS = 8>
 struct QGeom {
-  static constexpr int ROWS = 8 * NT * RG, KS = D / 16, UB = quant_unit_bytes(D);
+  static constexpr int ROWS = 8 * NT * RG, KS = D / 16, UB = kQUnitBytes<D, BITS>;
   // Eight warps in all leave each one 255 registers, which 16 rows of output need; more
   // leave 168. Slots and ring for 8 rows, d = 128, measured at 256 units x 65536 tokens, us:
   // 4 slots and 8 stages 677, 3 and 9 671, 5 and 10 694, 3 and 6 721, 6 and 6 745, 2 and 8
   // 907 (two warps cannot keep up); the first leaves shared memory for the join's CTAs to
   // wait on the same SMs. d = 64 (64 units x 16384), 8 and 16 33.6, 4 and 16 33.9, 8 and 8 41.
-  static constexpr int IS = NT == 2 ? 6 / RG : RG > 1 ? 8 / RG : D == 128 ? 4 : 8;
+  static constexpr int IS = NT == 2 ? 6 / RG : RG > 1 ? 8 / RG : D == 128 && BITS == 8 ? 4 : 8;
   static constexpr int W = IS * RG;             // consumer warps; a producer and a helper come on top
   static constexpr int THREADS = 32 * (W + 2);
   // What the compiler is told of the threads: 480 hold it to 136 registers, so that the join fits
   // beside the stream (kQcPerSm). fp32 takes the 144 that it may.
   static constexpr int BOUND = D == 64 && ROWS == 8 && !F32 ? 480 : THREADS;
-  static constexpr int STAGES = D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 8 : 9;
+  static constexpr int STAGES = BITS == 4 ? (NT * RG == 1 ? 16 : 12) : D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 8 : 9;
   static constexpr int SL = 4;                  // slices of a block that a warp takes at once
-  static constexpr int NQ = 2, ND = NT * RG == 1 ? 2 : 1;  // buffers for queries and for the warps' parts
+  static constexpr int NQ = 2, ND = NT * RG == 1 && !(BITS == 4 && D == 128) ? 2 : 1;  // buffers for queries and for the warps' parts
   static constexpr int RP = D + 4;              // padded row of a part
-  static constexpr int Q_BYTES = NT * RG * KS * 32 * (F32 ? 16 : 8);
+  static constexpr int QB = !F32 ? 8 : BITS == 8 ? 16 : 24;  // bytes of a lane's four query elements
+  static constexpr int Q_BYTES = NT * RG * KS * 32 * QB;
   static constexpr int RED_BYTES = W * 8 * NT * RP * 4, ML_BYTES = W * 8 * NT * 8;
   static constexpr int Q_OFF = STAGES * UB;
   static constexpr int RED_OFF = Q_OFF + NQ * Q_BYTES;
@@ -249,7 +272,7 @@ struct QWalk {
 
 // Queries of GROUPS x 8 rows (whole warp) as B operands, and the rows' factors; all
 // loads come first, so that they cost one round trip.
-template <int D, int GROUPS, bool F32>
+template <int D, int GROUPS, bool F32, int BITS>
 __device__ __forceinline__ void qa_queries(const QStreamParams& p, int u, int row0, int n, int qn, uint8_t* q_s, float* rs_s,
                                            int* vis_s, int lane) {
   constexpr int KS = D / 16;
@@ -280,6 +303,13 @@ __device__ __forceinline__ void qa_queries(const QStreamParams& p, int u, int ro
       } else {
         f[k][0] = bf16_lo(x.x); f[k][1] = bf16_hi(x.x); f[k][2] = bf16_lo(x.y); f[k][3] = bf16_hi(x.y);
       }
+      if constexpr (BITS == 4) {
+        using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+        const QRow w = qa_row(row0 + 8 * i + g, p.G, n, qn);
+        if (p.rope.pairs > 0 && w.t < qn)
+          rope_turn_vec<T, 4, false>(p.rope, static_cast<const T*>(p.q) + b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h,
+                                     (long long)b * p.T + w.t, 16 * k + 4 * c, f[k]);
+      }
 #pragma unroll
       for (int y = 0; y < 4; ++y) mx = fmaxf(mx, fabsf(f[k][y]));
     }
@@ -292,7 +322,22 @@ __device__ __forceinline__ void qa_queries(const QStreamParams& p, int u, int ro
     for (int k = 0; k < KS; ++k) {
       const float x0 = f[k][0] * down, x1 = f[k][1] * down, x2 = f[k][2] * down, x3 = f[k][3] * down;
       const uint32_t h0 = f16x2(x0, x1), h1 = f16x2(x2, x3);
-      if constexpr (F32) {
+      if constexpr (F32 && BITS == 4) {  // three terms of 8 bits, whose products with a step are exact
+        const float x[4] = {x0, x1, x2, x3};
+        float r[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) r[y] = x[y];
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+          float a[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            a[y] = term == 2 ? r[y] : __uint_as_float(__float_as_uint(r[y]) & 0xFFFF0000u);
+            r[y] -= a[y];
+          }
+          reinterpret_cast<uint2*>(q_s)[((i * KS + k) * 3 + term) * 32 + lane] = make_uint2(f16x2(a[0], a[1]), f16x2(a[2], a[3]));
+        }
+      } else if constexpr (F32) {
         const float2 y0 = f32x2(h0), y1 = f32x2(h1);
         reinterpret_cast<uint4*>(q_s)[(i * KS + k) * 32 + lane] =
             make_uint4(h0, h1, f16x2(x0 - y0.x, x1 - y0.y), f16x2(x2 - y1.x, x3 - y1.y));
@@ -315,7 +360,7 @@ __device__ __forceinline__ void qa_queries(const QStreamParams& p, int u, int ro
 // The products pay nothing for this. Clearing the codes of masked tokens on the way, with a
 // mask per word, was measured: 256 units x 65536 tokens 674 us (668 without), 32 rows 41.3
 // (40.0), 128 rows 101 (97.5), fp32 32 rows 74.0 (69.3).
-template <int D, int WR, int RP, int IS, bool F32>
+template <int D, int WR, int RP, int IS, bool F32, int BITS>
 __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0, int j1, int first, float* red, const float2* ml) {
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   constexpr int DL = D / 32;  // dims of a lane
@@ -323,7 +368,7 @@ __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0
   const int n = max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)), qn = quant_count(p.q_len, b, p.T, nullptr, false);
   auto block = [&](int j) -> const uint8_t* {  // null: the table names no unit
     const int idx = p.tab[(long long)u * p.max_blocks + j];
-    return idx < 0 || (long long)idx >= p.n_units ? nullptr : p.units + (long long)idx * quant_unit_bytes(D);
+    return idx < 0 || (long long)idx >= p.n_units ? nullptr : p.units + (long long)idx * kQUnitBytes<D, BITS>;
   };
 #pragma unroll 1
   for (int r = 0; r < WR; ++r) {
@@ -335,7 +380,7 @@ __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0
     for (int j = j0 + lane * IS; j < j1; j += 32 * IS) {
       const uint8_t* unit = block(j);
       if (unit == nullptr) continue;
-      const float* es = reinterpret_cast<const float*>(unit + quant_e_off(D));
+      const float* es = reinterpret_cast<const float*>(unit + kQLogits<D, BITS>);
       if (!isnan(es[kQB + 1])) continue;
 #pragma unroll 1
       for (int t = 0; t < kQB; ++t) due |= es[t] != -INFINITY && j * kQB + t < w.sees;
@@ -347,7 +392,7 @@ __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0
     for (int j = j0; j < j1; j += IS) {
       const uint8_t* unit = block(j);
       if (unit == nullptr) continue;
-      const float* es = reinterpret_cast<const float*>(unit + quant_e_off(D));
+      const float* es = reinterpret_cast<const float*>(unit + kQLogits<D, BITS>);
       float wt[2];  // the lane's tokens lane and lane + 32; -1: masked or not seen
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -355,9 +400,19 @@ __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0
         float l = 0.f;
 #pragma unroll 8
         for (int x = 0; x < D; x += 4) {
-          const uint32_t k = *reinterpret_cast<const uint32_t*>(unit + quant_k_off(t, x, D));
-          const float2 k0 = f32x2(e4m3x2_f16x2(k)), k1 = f32x2(e4m3x2_f16x2(k >> 16));
-          l += to_f32(q[x]) * k0.x + to_f32(q[x + 1]) * k0.y + to_f32(q[x + 2]) * k1.x + to_f32(q[x + 3]) * k1.y;
+          float k[4], qv[4];
+          if constexpr (BITS == 8) {
+            const uint32_t y = *reinterpret_cast<const uint32_t*>(unit + quant_k_off(t, x, D));
+            const float2 k0 = f32x2(e4m3x2_f16x2(y)), k1 = f32x2(e4m3x2_f16x2(y >> 16));
+            k[0] = k0.x; k[1] = k0.y; k[2] = k1.x; k[3] = k1.y;
+          } else {
+            quant4_keys<D>(unit, t, x, k);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qv[i] = to_f32(q[x + i]);
+          if constexpr (BITS == 4)
+            if (p.rope.pairs > 0) rope_turn_vec<T, 4, false>(p.rope, q, (long long)b * p.T + w.t, x, qv);
+          l += qv[0] * k[0] + qv[1] * k[1] + qv[2] * k[2] + qv[3] * k[3];
         }
         wt[y] = es[t] == -INFINITY || j * kQB + t >= w.sees ? -1.f : exp_from(l * kQScale<D> * es[kQB] + es[t], mu);
       }
@@ -368,9 +423,13 @@ __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0
         float v[DL][4];
 #pragma unroll
         for (int x = 0; x < DL; ++x) {
-          const uint32_t k = *reinterpret_cast<const uint32_t*>(unit + quant_v_off(t, lane * DL + x, D));
-          const float2 v0 = f32x2(e4m3x2_f16x2(k)), v1 = f32x2(e4m3x2_f16x2(k >> 16));
-          v[x][0] = v0.x; v[x][1] = v0.y; v[x][2] = v1.x; v[x][3] = v1.y;
+          if constexpr (BITS == 8) {
+            const uint32_t k = *reinterpret_cast<const uint32_t*>(unit + quant_v_off(t, lane * DL + x, D));
+            const float2 v0 = f32x2(e4m3x2_f16x2(k)), v1 = f32x2(e4m3x2_f16x2(k >> 16));
+            v[x][0] = v0.x; v[x][1] = v0.y; v[x][2] = v1.x; v[x][3] = v1.y;
+          } else {
+            quant4_values<D>(unit, t, lane * DL + x, v[x]);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -402,9 +461,9 @@ static __device__ __noinline__ void qa_places(const QStreamParams& p, int a0, in
   }
 }
 
-template <int D, int NT, int RG, bool F32>
-__global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_kernel(QStreamParams p) {
-  using Gm = QGeom<D, NT, RG, F32>;
+template <int D, int NT, int RG, bool F32, int BITS>
+__global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_stream_kernel(QStreamParams p) {
+  using Gm = QGeom<D, NT, RG, F32, BITS>;
   constexpr int KS = Gm::KS, ROWS = Gm::ROWS, STAGES = Gm::STAGES, UB = Gm::UB, SL = Gm::SL, W = Gm::W, IS = Gm::IS;
   constexpr int NQ = Gm::NQ, ND = Gm::ND, WR = 8 * NT, kThreads = Gm::THREADS;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -588,7 +647,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
       constexpr int GR = F32 ? 1 : ROWS / 8;  // row groups at once: 32 rows of bf16 take 64 registers
 #pragma unroll 1
       for (int r = 0; r < ROWS; r += 8 * GR)
-        qa_queries<D, GR, F32>(p, ahead.u, ahead.tile * ROWS + r, ahead.tokens, qn, q_of(prepared) + r * KS * 4 * (F32 ? 16 : 8),
+        qa_queries<D, GR, F32, BITS>(p, ahead.u, ahead.tile * ROWS + r, ahead.tokens, qn, q_of(prepared) + r * KS * 4 * Gm::QB,
                                rs_of(prepared) + r, vis_of(prepared) + r, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[prepared % NQ]);
@@ -630,7 +689,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
   for (int k = 0; seg.more(); ++k, it0 += seg.cnt, seg.next()) {
     if (!(ok = wait(&q_full[k % NQ], k / NQ))) break;
     const long long vu = seg.vu();
-    const uint8_t* q_s = q_of(k) + rg * NT * KS * 32 * (F32 ? 16 : 8);
+    const uint8_t* q_s = q_of(k) + rg * NT * KS * 32 * Gm::QB;
     const float* rs_s = rs_of(k) + rg * WR;
     const int* vis_s = vis_of(k) + rg * WR;
     float o[NT][KS][4], m_run[NT][2], l_run[NT][2], fac[1][2];
@@ -666,7 +725,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
       if (!(ok = wait(&full[s], it / STAGES))) break;
       const bool null_unit = null_s[s] != 0;
       const uint8_t* unit = smem + s * UB;
-      const float* es = reinterpret_cast<const float*>(unit + quant_e_off(D));
+      const float* es = reinterpret_cast<const float*>(unit + kQLogits<D, BITS>);
       const float ks = es[kQB], vs = es[kQB + 1] * 0x1p-14f;
       const bool edge = j * kQB + kQB > least;
       float blk_l[NT][2];
@@ -682,37 +741,82 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int w = 0; w < SL; ++w) sc[nt][w][0] = sc[nt][w][1] = sc[nt][w][2] = sc[nt][w][3] = 0.f;
+        float qz[BITS == 4 ? NT : 1][4];  // the queries' products with the zeros, in every row alike
+        if constexpr (BITS == 8) {
 #pragma unroll
-        for (int jj = 0; jj < KS / 2; ++jj) {
-          uint4 v[SL];
+          for (int jj = 0; jj < KS / 2; ++jj) {
+            uint4 v[SL];
 #pragma unroll
-          for (int w = 0; w < SL; ++w) v[w] = kw[w * 2 * D + jj * 32];
+            for (int w = 0; w < SL; ++w) v[w] = kw[w * 2 * D + jj * 32];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int kk = 2 * jj + y;
-            uint32_t qb[NT][F32 ? 4 : 2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (F32) {
-                const uint4 x = reinterpret_cast<const uint4*>(q_s)[(nt * KS + kk) * 32 + lane];
-                qb[nt][0] = x.x; qb[nt][1] = x.y; qb[nt][2] = x.z; qb[nt][3] = x.w;
-              } else if constexpr (NT == 1) {
-                qb[nt][0] = qr[kk][0];
-                qb[nt][1] = qr[kk][1];
-              } else {
-                const uint2 x = reinterpret_cast<const uint2*>(q_s)[(nt * KS + kk) * 32 + lane];
-                qb[nt][0] = x.x;
-                qb[nt][1] = x.y;
-              }
-            }
-#pragma unroll
-            for (int w = 0; w < SL; ++w) {
-              const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
-              const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
+            for (int y = 0; y < 2; ++y) {
+              const int kk = 2 * jj + y;
+              uint32_t qb[NT][F32 ? 4 : 2];
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                if constexpr (F32) mma16816(sc[nt][w], a, qb[nt][2], qb[nt][3]);
-                mma16816(sc[nt][w], a, qb[nt][0], qb[nt][1]);
+                if constexpr (F32) {
+                  const uint4 x = reinterpret_cast<const uint4*>(q_s)[(nt * KS + kk) * 32 + lane];
+                  qb[nt][0] = x.x; qb[nt][1] = x.y; qb[nt][2] = x.z; qb[nt][3] = x.w;
+                } else if constexpr (NT == 1) {
+                  qb[nt][0] = qr[kk][0];
+                  qb[nt][1] = qr[kk][1];
+                } else {
+                  const uint2 x = reinterpret_cast<const uint2*>(q_s)[(nt * KS + kk) * 32 + lane];
+                  qb[nt][0] = x.x;
+                  qb[nt][1] = x.y;
+                }
+              }
+#pragma unroll
+              for (int w = 0; w < SL; ++w) {
+                const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
+                const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if constexpr (F32) mma16816(sc[nt][w], a, qb[nt][2], qb[nt][3]);
+                  mma16816(sc[nt][w], a, qb[nt][0], qb[nt][1]);
+                }
+              }
+            }
+          }
+        } else {
+          // sum over dims of q_x step_x n_x, the queries times the steps as operands, and of q_x zero_x
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) qz[nt][0] = qz[nt][1] = qz[nt][2] = qz[nt][3] = 0.f;
+          constexpr int TERMS = F32 ? 3 : 1;
+          const uint4* kc = reinterpret_cast<const uint4*>(unit) + lane;
+          const uint4* ksteps = reinterpret_cast<const uint4*>(unit + quant4_kstep_off(D) + c * KS * 4);
+          const uint4* kzeros = reinterpret_cast<const uint4*>(unit + quant4_kzero_off(D) + c * KS * 8);
+#pragma unroll
+          for (int k4 = 0; k4 < KS / 4; ++k4) {
+            const uint4 st4 = ksteps[k4], z4[2] = {kzeros[2 * k4], kzeros[2 * k4 + 1]};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int kk = 4 * k4 + y;
+              const uint4 v = kc[kk * 32];
+              const uint2 st = steps_f16(word_of(st4, y));
+              const uint32_t z0 = word_of(z4[y / 2], 2 * (y % 2)), z1 = word_of(z4[y / 2], 2 * (y % 2) + 1), za[4] = {z0, z0, z1, z1};
+              uint32_t qs[NT][TERMS][2];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = TERMS - 1; x >= 0; --x) {
+                  uint2 q;
+                  if constexpr (NT == 1 && !F32)
+                    q = make_uint2(qr[kk][0], qr[kk][1]);
+                  else
+                    q = reinterpret_cast<const uint2*>(q_s)[((nt * KS + kk) * TERMS + x) * 32 + lane];
+                  mma16816(qz[nt], za, q.x, q.y);
+                  qs[nt][x][0] = mul_f16x2(q.x, st.x);
+                  qs[nt][x][1] = mul_f16x2(q.y, st.y);
+                }
+#pragma unroll
+              for (int w = 0; w < SL; ++w) {
+                uint32_t a[4];
+                codes_f16(word_of(v, w), a);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int x = TERMS - 1; x >= 0; --x) mma16816(sc[nt][w], a, qs[nt][x][0], qs[nt][x][1]);
               }
             }
           }
@@ -742,7 +846,11 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 float& l = sc[nt][w][2 * y + x];
-                l = l * f + ev[w][y];
+                if constexpr (BITS == 8) {
+                  l = l * f + ev[w][y];
+                } else {  // (the codes' rows are 2^-24 and 2^-20 of what they stand for)
+                  l = l * (f * (y ? 0x1p20f : 0x1p24f)) + (qz[nt][x] * f + ev[w][y]);
+                }
                 if (ev[w][y] == -INFINITY || (edge && pos + 16 * w + 2 * y >= sees)) l = -INFINITY;
                 mx = max_nan(mx, l);
               }
@@ -784,34 +892,95 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
             }
         }
         // ---- o = o * corr + scale * (V^T P) ----
-        const uint4* vw = kw + D;  // 16 D bytes on
+        if constexpr (BITS == 8) {
+          const uint4* vw = kw + D;  // 16 D bytes on
 #pragma unroll
-        for (int jj = 0; jj < KS / 2; ++jj) {
-          uint4 v[SL];
+          for (int jj = 0; jj < KS / 2; ++jj) {
+            uint4 v[SL];
 #pragma unroll
-          for (int w = 0; w < SL; ++w) v[w] = vw[w * 2 * D + jj * 32];
+            for (int w = 0; w < SL; ++w) v[w] = vw[w * 2 * D + jj * 32];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float t[NT][4];
+            for (int y = 0; y < 2; ++y) {
+              float t[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
+              for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
 #pragma unroll
-            for (int w = 0; w < SL; ++w) {
-              const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
-              const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
+              for (int w = 0; w < SL; ++w) {
+                const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
+                const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                if constexpr (F32) mma16816(t[nt], a, pl[nt][w][0], pl[nt][w][1]);
-                mma16816(t[nt], a, pb[nt][w][0], pb[nt][w][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                  if constexpr (F32) mma16816(t[nt], a, pl[nt][w][0], pl[nt][w][1]);
+                  mma16816(t[nt], a, pb[nt][w][0], pb[nt][w][1]);
+                }
               }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  float& oo = o[nt][2 * jj + y][x];
+                  oo = oo * corr[nt][x & 1] + t[nt][x] * vsc[nt][x & 1];
+                }
+            }
+          }
+        } else {
+          const uint4* vc = reinterpret_cast<const uint4*>(unit + 32 * D) + lane;
+#pragma unroll
+          for (int r = 0; r < D / 64; ++r) {  // runs of 64 dims
+            const uint4* vsteps = reinterpret_cast<const uint4*>(unit + quant4_vstep_off(D) + r * 128 + c * 32);
+            const uint4* vzeros = reinterpret_cast<const uint4*>(unit + quant4_vzero_off(D) + r * 128 + c * 32);
+            const uint4 s4[2] = {vsteps[0], vsteps[1]}, z4[2] = {vzeros[0], vzeros[1]};
+            uint32_t ps[NT][SL][2], pt[F32 ? NT : 1][SL][2];  // weights times steps
+            float base[NT][2];                                // ... with the zeros
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float tz[4] = {};
+#pragma unroll
+              for (int w = 0; w < SL; ++w) {
+                const uint32_t z0 = word_of(z4[w / 2], 2 * (w % 2)), z1 = word_of(z4[w / 2], 2 * (w % 2) + 1), za[4] = {z0, z0, z1, z1};
+                if constexpr (F32) mma16816(tz, za, pl[nt][w][0], pl[nt][w][1]);
+                mma16816(tz, za, pb[nt][w][0], pb[nt][w][1]);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t st = word_of(s4[w / 2], 2 * (w % 2) + y);
+                  if constexpr (F32) {
+                    const float2 hi = f32x2(pb[nt][w][y]), lo = f32x2(pl[nt][w][y]), t = f32x2(st);
+                    const float x0 = (hi.x + lo.x) * t.x, x1 = (hi.y + lo.y) * t.y;
+                    ps[nt][w][y] = f16x2(x0, x1);
+                    const float2 r2 = f32x2(ps[nt][w][y]);
+                    pt[nt][w][y] = f16x2(x0 - r2.x, x1 - r2.y);
+                  } else {
+                    ps[nt][w][y] = mul_f16x2(pb[nt][w][y], st);
+                  }
+                }
+              }
+              base[nt][0] = tz[0] * vsc[nt][0];
+              base[nt][1] = tz[1] * vsc[nt][1];
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int m = 4 * r; m < 4 * r + 4; ++m) {
+              const uint4 v = vc[m * 32];
+              float t[NT][4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                float& oo = o[nt][2 * jj + y][x];
-                oo = oo * corr[nt][x & 1] + t[nt][x] * vsc[nt][x & 1];
+              for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
+#pragma unroll
+              for (int w = 0; w < SL; ++w) {
+                uint32_t a[4];
+                codes_f16(word_of(v, w), a);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if constexpr (F32) mma16816(t[nt], a, pt[nt][w][0], pt[nt][w][1]);
+                  mma16816(t[nt], a, ps[nt][w][0], ps[nt][w][1]);
+                }
               }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  float& oo = o[nt][m][x];
+                  oo = oo * corr[nt][x & 1] + base[nt][x & 1] + t[nt][x] * (vsc[nt][x & 1] * (x < 2 ? 0x1p24f : 0x1p20f));
+                }
+            }
           }
         }
       }
@@ -863,7 +1032,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32>::BOUND, 1) quant_stream_
     }
     __syncwarp();
     if (__any_sync(0xffffffffu, isnan(nan)))
-      qa_part_again<D, WR, Gm::RP, IS, F32>(p, seg.u, seg.j0 + (is + IS - it0 % IS) % IS, seg.j0 + seg.cnt, seg.tile * ROWS + rg * WR, red, ml);
+      qa_part_again<D, WR, Gm::RP, IS, F32, BITS>(p, seg.u, seg.j0 + (is + IS - it0 % IS) % IS, seg.j0 + seg.cnt, seg.tile * ROWS + rg * WR, red, ml);
     __syncwarp();
     if (lane == 0) mbar_arrive(&dump_full[k % ND]);
     if (kShareJoin && seg.left == seg.cnt) {  // the last segment (its buffer's earlier fills have been joined)
@@ -891,7 +1060,7 @@ constexpr int kQcRows = 8;
 // 80 beside a bf16 stream, and the values come along with the keys.
 template <typename T, int D> constexpr int kQcPerSm = D == 64 ? (sizeof(T) == 4 ? 6 : 5) : 3;
 
-template <typename T, int D>
+template <typename T, int D, int BITS>
 __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kernel(QStreamParams p, int rows, bool weights) {
   constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE;
   constexpr int KC = NCH / 4;                        // 16-byte key chunks of a thread: token tid % 64
@@ -940,8 +1109,17 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
       const T* src = reinterpret_cast<const T*>(p.q) + b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + x * CE;
       const uint4 y = __ldcg(reinterpret_cast<const uint4*>(src));
       const T* e = reinterpret_cast<const T*>(&y);
+      if constexpr (BITS == 8) {
 #pragma unroll
-      for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = to_f32(e[k]) * kQScale<D>;
+        for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = to_f32(e[k]) * kQScale<D>;
+      } else {
+        float f[CE];
+#pragma unroll
+        for (int k = 0; k < CE; ++k) f[k] = to_f32(e[k]);
+        if (p.rope.pairs > 0) rope_turn_vec<T, CE, true>(p.rope, src - x * CE, (long long)b * p.T + w.t, x * CE, f);
+#pragma unroll
+        for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = f[k] * kQScale<D>;
+      }
     }
     __syncthreads();
 #pragma unroll
@@ -1220,18 +1398,20 @@ struct QPlan {
 QPlan quant_attn_plan(const Shape& s, int T);
 cudaError_t launch_quant_stream_bf16(const Shape& s, const QPlan& pl, const QStreamParams& p, cudaStream_t stream);
 cudaError_t launch_quant_stream_f32(const Shape& s, const QPlan& pl, const QStreamParams& p, cudaStream_t stream);
+cudaError_t launch_quant4_stream_bf16(const Shape& s, const QPlan& pl, const QStreamParams& p, cudaStream_t stream);
+cudaError_t launch_quant4_stream_f32(const Shape& s, const QPlan& pl, const QStreamParams& p, cudaStream_t stream);
 
 #ifdef __CUDACC__
-template <int D, int NT, int RG, bool F32>
+template <int D, int NT, int RG, bool F32, int BITS>
 cudaError_t stream_variant(const QPlan& pl, const QStreamParams& p, cudaStream_t stream) {
-  using Gm = QGeom<D, NT, RG, F32>;
+  using Gm = QGeom<D, NT, RG, F32, BITS>;
   static std::atomic<int> lim[64];
-  const cudaError_t e = raise_smem_limit((const void*)quant_stream_kernel<D, NT, RG, F32>, Gm::SMEM, lim);
+  const cudaError_t e = raise_smem_limit((const void*)quant_stream_kernel<D, NT, RG, F32, BITS>, Gm::SMEM, lim);
   if (e != cudaSuccess) return e;
-  return launch_dependent(quant_stream_kernel<D, NT, RG, F32>, dim3(pl.ctas), Gm::THREADS, Gm::SMEM, stream, p);
+  return launch_dependent(quant_stream_kernel<D, NT, RG, F32, BITS>, dim3(pl.ctas), Gm::THREADS, Gm::SMEM, stream, p);
 }
 
-template <typename T, int D>
+template <typename T, int D, int BITS = 8>
 cudaError_t stream_launches(const Shape& s, const QPlan& pl, const QStreamParams& p, cudaStream_t stream) {
   constexpr bool F32 = sizeof(T) == 4;
   // 16 and 32 rows as row groups of 8, which convert the codes once each but leave
@@ -1241,13 +1421,13 @@ cudaError_t stream_launches(const Shape& s, const QPlan& pl, const QStreamParams
   // of 16: 60), fp32 78 (89). With the next unit's queries ready ahead: 36, 41, 53, 69.
   cudaError_t e;
   if (pl.rows == 8)
-    e = stream_variant<D, 1, 1, F32>(pl, p, stream);
+    e = stream_variant<D, 1, 1, F32, BITS>(pl, p, stream);
   else if (pl.rows == 16)
-    e = stream_variant<D, 1, 2, F32>(pl, p, stream);
+    e = stream_variant<D, 1, 2, F32, BITS>(pl, p, stream);
   else if constexpr (F32)
-    e = stream_variant<D, 1, 4, F32>(pl, p, stream);
+    e = stream_variant<D, 1, 4, F32, BITS>(pl, p, stream);
   else
-    e = stream_variant<D, 2, 2, F32>(pl, p, stream);
+    e = stream_variant<D, 2, 2, F32, BITS>(pl, p, stream);
   if (e != cudaSuccess) return e;
   // few units have many parts each: more CTAs share the join
   const int vu = s.U * pl.tiles, y = pl.rows / kQcRows, z = vu * y <= 16 ? 4 : vu * y <= 32 ? 2 : 1;
@@ -1257,7 +1437,7 @@ cudaError_t stream_launches(const Shape& s, const QPlan& pl, const QStreamParams
   // 54.3, 256 96.7 / 95.5, 512 105.4 / 100.0 (ragged); four CTAs a unit at 16 units: 375
   // blocks 27.1 / 27.6.
   const bool joined = p.mass != nullptr && pl.rows == kQcRows && p.max_blocks <= 128 * z;
-  e = launch_dependent(quant_combine_kernel<T, D>, dim3(vu, y, z), kQcThreads, 0, stream, p, pl.rows, joined);
+  e = launch_dependent(quant_combine_kernel<T, D, BITS>, dim3(vu, y, z), kQcThreads, 0, stream, p, pl.rows, joined);
   if (e != cudaSuccess || p.mass == nullptr || joined) return e;
   auto weights = [&](auto kernel, int per) {
     return launch_dependent(kernel, dim3(s.U, (p.max_blocks + per - 1) / per), kQcThreads, 0, stream, p);
