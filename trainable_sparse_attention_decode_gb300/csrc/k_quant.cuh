@@ -89,6 +89,7 @@ struct QAttnArgs {
   float decay;
   uint8_t* ws;
   bool give_up;  // a test's: every wait gives up at once
+  bool turned;   // q was written by the launch before (see quant_stream_kernel)
   int* status;
 };
 

@@ -62,6 +62,7 @@ struct Q4ReadArgs {
 };
 cudaError_t launch_quant4_append(const Shape& s, const Q4AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_quant4_read(const Shape& s, const Q4ReadArgs& a, cudaStream_t stream);
+size_t quant4_attn_workspace(const Shape& s, int max_blocks, int T, bool mass);
 cudaError_t launch_quant4_attention(const Shape& s, const QAttnArgs& a, const RopeArgs& rope, cudaStream_t stream);
 
 #ifdef __CUDACC__

@@ -66,6 +66,7 @@ static QStreamParams stream_params(const Shape& s, const QPlan& pl, const QAttnA
   p.qs = a.qs;
   p.T = a.T;
   p.q_len = a.q_len;
+  p.turned = a.turned;
   p.U = s.U;
   p.Hkv = s.Hkv;
   p.Hq = s.Hq;
@@ -96,11 +97,37 @@ cudaError_t launch_quant_attention(const Shape& s, const QAttnArgs& a, cudaStrea
   return s.dtype == 0 ? launch_quant_stream_f32(s, pl, p, stream) : launch_quant_stream_bf16(s, pl, p, stream);
 }
 
-cudaError_t launch_quant4_attention(const Shape& s, const QAttnArgs& a, const RopeArgs& rope, cudaStream_t stream) {
-  const QPlan pl = quant_attn_plan(s, a.T);
-  QStreamParams p = stream_params(s, pl, a);
-  p.rope = rope;
+// The queries are turned first, into the workspace: in the stream's helper warp and in the join the
+// rotation cost 9 to 16 us a call (8 units x 131071 tokens; 32 rows), by their registers most of it.
+cudaError_t launch_quant4_attention(const Shape& s, const QAttnArgs& args, const RopeArgs& rope, cudaStream_t stream) {
+  const QPlan pl = quant_attn_plan(s, args.T);
+  QAttnArgs a = args;
+  if (rope.pairs > 0) {
+    RotateArgs r{};
+    r.rope = rope;
+    r.in[0] = a.q;
+    r.in_b[0] = a.qs.b;
+    r.in_t[0] = a.qs.t;
+    r.in_h[0] = a.qs.h;
+    a.qs = QStrides{(long long)a.T * s.Hq * s.d, (long long)s.Hq * s.d, s.d};
+    a.q = r.out[0] = a.ws + quant_attn_workspace(s, a.max_blocks, a.T, a.mass != nullptr);
+    a.turned = true;
+    r.out_b[0] = a.qs.b;
+    r.out_t[0] = a.qs.t;
+    r.out_h[0] = a.qs.h;
+    r.heads[0] = s.Hq;
+    r.n = a.T;
+    r.count = a.q_len;
+    r.rows = (long long)s.batch * a.T;
+    const cudaError_t e = launch_rotate(s, r, stream);
+    if (e != cudaSuccess) return e;
+  }
+  const QStreamParams p = stream_params(s, pl, a);
   return s.dtype == 0 ? launch_quant4_stream_f32(s, pl, p, stream) : launch_quant4_stream_bf16(s, pl, p, stream);
+}
+
+size_t quant4_attn_workspace(const Shape& s, int max_blocks, int T, bool mass) {
+  return quant_attn_workspace(s, max_blocks, T, mass) + (size_t)s.batch * T * s.Hq * s.d * s.elt;
 }
 
 }  // namespace nosa

@@ -75,7 +75,7 @@ struct QStreamParams {
   QStrides qs;
   int T;
   const int32_t* q_len;
-  RopeArgs rope;  // turns the queries (4-bit cache)
+  bool turned;  // q is the work of the call's first launch (4-bit cache)
   int U, Hkv, Hq, G, tiles;
   const uint8_t* tail;
   long long payload;
@@ -110,6 +110,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
 // exp(x - m) for the base-2 exponential; x = -inf gives 0 for every finite m.
 __device__ __forceinline__ float exp_from(float x, float m) { return exp2f((x - m) * kQLog2e); }
@@ -134,14 +139,21 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
-// A word of eight 4-bit codes as the four A operand registers of a 16 x 16 x 8 tile, without a
-// conversion: n as the subnormal fp16 number 2^-24 n in the tile's rows 0..7, 2^-20 n in 8..15.
+// A word of eight 4-bit codes as the four A operand registers of a 16 x 16 tile, without a
+// conversion: fp16 numbers below 2^-13 are 2^-24 times their bits, so rows 0..7 of the tile hold
+// 2^-24 n and rows 8..15 2^-24 (n + 16 n') with the code n of the row 8 before: codes_split takes
+// the product of the one off the other's. (Masking n' out costs a fifth operation, and these
+// run at half rate.)
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t* a) {
-  const uint32_t x = w >> 8;
   a[0] = w & 0x000F000Fu;
-  a[1] = w & 0x00F000F0u;
-  a[2] = x & 0x000F000Fu;
-  a[3] = x & 0x00F000F0u;
+  a[1] = w & 0x00FF00FFu;
+  a[3] = __byte_perm(w, 0, 0x4341);
+  a[2] = a[3] & 0x000F000Fu;
+}
+// A product of such a tile: rows 0..7 as 2^-24 of what the codes stand for, 8..15 as 2^-20.
+__device__ __forceinline__ void codes_split(float* d) {
+  d[2] -= d[0];
+  d[3] -= d[1];
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
@@ -234,6 +246,7 @@ struct QGeom {
 };
 
 // A CTA's share as segments: consecutive blocks of one (unit, tile).
+template <bool EARLY>
 struct QWalk {
   const QStreamParams& p;
   int u, tile, j0, cnt, left, lane, have, len, tokens;
@@ -249,7 +262,7 @@ struct QWalk {
   __device__ __forceinline__ int fetch() {  // tokens of unit u; 32 lengths at a time (whole warp)
     if (have < 0 || u >= have + 32) {
       have = u;
-      len = u + lane < p.U ? max(0, quant_len(p.lens, u + lane, p.max_blocks, nullptr, false)) : 0;
+      len = u + lane < p.U ? max(0, quant_len<EARLY>(p.lens, u + lane, p.max_blocks, nullptr, false)) : 0;
     }
     return __shfl_sync(0xffffffffu, len, u - have);
   }
@@ -302,13 +315,6 @@ __device__ __forceinline__ void qa_queries(const QStreamParams& p, int u, int ro
         f[k][2] = __uint_as_float(x.z); f[k][3] = __uint_as_float(x.w);
       } else {
         f[k][0] = bf16_lo(x.x); f[k][1] = bf16_hi(x.x); f[k][2] = bf16_lo(x.y); f[k][3] = bf16_hi(x.y);
-      }
-      if constexpr (BITS == 4) {
-        using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
-        const QRow w = qa_row(row0 + 8 * i + g, p.G, n, qn);
-        if (p.rope.pairs > 0 && w.t < qn)
-          rope_turn_vec<T, 4, false>(p.rope, static_cast<const T*>(p.q) + b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h,
-                                     (long long)b * p.T + w.t, 16 * k + 4 * c, f[k]);
       }
 #pragma unroll
       for (int y = 0; y < 4; ++y) mx = fmaxf(mx, fabsf(f[k][y]));
@@ -410,8 +416,6 @@ __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) qv[i] = to_f32(q[x + i]);
-          if constexpr (BITS == 4)
-            if (p.rope.pairs > 0) rope_turn_vec<T, 4, false>(p.rope, q, (long long)b * p.T + w.t, x, qv);
           l += qv[0] * k[0] + qv[1] * k[1] + qv[2] * k[2] + qv[3] * k[3];
         }
         wt[y] = es[t] == -INFINITY || j * kQB + t >= w.sees ? -1.f : exp_from(l * kQScale<D> * es[kQB] + es[t], mu);
@@ -454,10 +458,11 @@ __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0
 
 // First items of a thread's units, where the join does not add them up itself (out of line: 32 rows
 // over 32 units of 8200 tokens 40.7 us, with the loop in the kernel 41.1).
-static __device__ __noinline__ void qa_places(const QStreamParams& p, int a0, int a1, long long at) {
+template <bool EARLY>
+__device__ __noinline__ void qa_places(const QStreamParams& p, int a0, int a1, long long at) {
   for (int u = a0; u < a1; ++u) {
     p.base[u] = at;
-    at += max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
+    at += max(0, quant_len<EARLY>(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
   }
 }
 
@@ -498,13 +503,19 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
     fence_mbar_init();
     s_bad = p.give_up;
   }
-  griddep_wait();
-  griddep_launch_dependents();
+  // Behind the rotation of the queries, which has waited for all before it, only who reads those
+  // waits; what the others read was there before the call (see launch_dependent) and is read past L1.
+  constexpr bool kEarly = BITS == 4;
+  const bool later = kEarly && p.turned;
+  if (!later) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   // ---- the share: prefix sums of the units' full blocks ----
   const int per = (p.U + kThreads - 1) / kThreads;
   const int a0 = min(p.U, tid * per), a1 = min(p.U, a0 + per);
   long long mine = 0;
-  for (int u = a0; u < a1; ++u) mine += max(0, quant_len(p.lens, u, p.max_blocks, p.status, cta == 0)) / kQB;
+  for (int u = a0; u < a1; ++u) mine += max(0, quant_len<kEarly>(p.lens, u, p.max_blocks, p.status, cta == 0)) / kQB;
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -519,17 +530,23 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  if (p.U > kQcScan * kQcThreads && tid % p.ctas == cta) qa_places(p, a0, a1, before);  // (a thread's by one of the CTAs)
+  if (p.U > kQcScan * kQcThreads && tid % p.ctas == cta) qa_places<kEarly>(p, a0, a1, before);  // (a thread's by one of the CTAs)
   total *= p.tiles;
   before *= p.tiles;
   if (cta == 0 && tid == 0) *p.total = total;
   const int active = qa_active(total, p.ctas);
-  if (cta >= active) return;  // (the whole CTA)
+  if (cta >= active) {  // (the whole CTA)
+    if (later) {
+      griddep_wait();
+      griddep_launch_dependents();
+    }
+    return;
+  }
   const long long g0 = (long long)cta * total / active, g1 = (long long)(cta + 1) * total / active;
   if (before <= g0 && g0 < before + mine * p.tiles) {  // exactly one thread: the unit that holds item g0
     int u = a0;
     for (;; ++u) {
-      const long long n = (long long)max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)) / kQB * p.tiles;
+      const long long n = (long long)max(0, quant_len<kEarly>(p.lens, u, p.max_blocks, nullptr, false)) / kQB * p.tiles;
       if (g0 < before + n) break;
       before += n;
     }
@@ -591,14 +608,14 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
     auto seek = [&]() {                  // (u, tile, j) of the item, and its table entry
       if (it >= items) return;
       for (;;) {
-        nb = max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
+        nb = max(0, quant_len<kEarly>(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
         if (pos < (long long)nb * p.tiles) break;
         pos -= (long long)nb * p.tiles;
         ++u;
       }
       tile = (int)pos / nb;
       j = (int)pos - tile * nb;
-      idx = p.tab[(long long)u * p.max_blocks + j];
+      idx = kEarly ? __ldcg(p.tab + (long long)u * p.max_blocks + j) : p.tab[(long long)u * p.max_blocks + j];
     };
     if (lane >= STAGES) it = items;
     seek();
@@ -639,11 +656,15 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 
   if (warp == W + 1) {
     // ---- helper: prepares the queries of coming segments, joins the warps' parts ----
-    QWalk ahead(p, s_unit, g0 - s_before, items, lane);
+    if (later) {
+      griddep_wait();
+      griddep_launch_dependents();
+    }
+    QWalk<kEarly> ahead(p, s_unit, g0 - s_before, items, lane);
     long long slot[NQ];
     int prepared = 0;
     auto prepare = [&]() {
-      const int b = ahead.u / p.Hkv, qn = quant_count(p.q_len, b, p.T, p.status, lane == 0);
+      const int b = ahead.u / p.Hkv, qn = quant_count<kEarly>(p.q_len, b, p.T, p.status, lane == 0);
       constexpr int GR = F32 ? 1 : ROWS / 8;  // row groups at once: 32 rows of bf16 take 64 registers
 #pragma unroll 1
       for (int r = 0; r < ROWS; r += 8 * GR)
@@ -674,7 +695,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
     if (!ok && lane == 0) give_up();
     __syncthreads();
     if (s_bad != 0) {  // none of the CTA's parts counts
-      for (QWalk all(p, s_unit, g0 - s_before, items, lane); all.more(); all.next())
+      for (QWalk<kEarly> all(p, s_unit, g0 - s_before, items, lane); all.more(); all.next())
         if (lane < ROWS) p.part_ml[(cta + all.vu()) * ROWS + lane] = qa_missing();
     }
     return;
@@ -684,7 +705,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
   const int g = lane >> 2, c = lane & 3;
   const int tok = 4 * (g >> 1) + (g & 1);  // this lane's tokens of a slice: tok and tok + 2
   const int is = warp % IS, rg = warp / IS;
-  QWalk seg(p, s_unit, g0 - s_before, items, lane);
+  QWalk<kEarly> seg(p, s_unit, g0 - s_before, items, lane);
   int it0 = 0;  // first item of the segment
   for (int k = 0; seg.more(); ++k, it0 += seg.cnt, seg.next()) {
     if (!(ok = wait(&q_full[k % NQ], k / NQ))) break;
@@ -731,258 +752,289 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
       float blk_l[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) blk_l[nt][0] = blk_l[nt][1] = 0.f;
+      auto block = [&](auto edge_tag) {
+        constexpr bool EDGE = decltype(edge_tag)::value;
 #pragma unroll
-      for (int s0 = 0; s0 < 4; s0 += SL) {
-        if (null_unit) break;
-        const uint4* kw = reinterpret_cast<const uint4*>(unit) + s0 * 2 * D + lane;
-        // ---- logits ----
-        float sc[NT][SL][4];
+        for (int s0 = 0; s0 < 4; s0 += SL) {
+          if (BITS == 8 && null_unit) break;
+          const uint4* kw = reinterpret_cast<const uint4*>(unit) + s0 * 2 * D + lane;
+          // ---- logits ----
+          float sc[NT][SL][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int w = 0; w < SL; ++w) sc[nt][w][0] = sc[nt][w][1] = sc[nt][w][2] = sc[nt][w][3] = 0.f;
-        float qz[BITS == 4 ? NT : 1][4];  // the queries' products with the zeros, in every row alike
-        if constexpr (BITS == 8) {
+            for (int w = 0; w < SL; ++w) sc[nt][w][0] = sc[nt][w][1] = sc[nt][w][2] = sc[nt][w][3] = 0.f;
+          float qz[BITS == 4 ? NT : 1][4];  // the queries' products with the zeros, in every row alike
+          if constexpr (BITS == 8) {
 #pragma unroll
-          for (int jj = 0; jj < KS / 2; ++jj) {
-            uint4 v[SL];
+            for (int jj = 0; jj < KS / 2; ++jj) {
+              uint4 v[SL];
 #pragma unroll
-            for (int w = 0; w < SL; ++w) v[w] = kw[w * 2 * D + jj * 32];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int kk = 2 * jj + y;
-              uint32_t qb[NT][F32 ? 4 : 2];
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                if constexpr (F32) {
-                  const uint4 x = reinterpret_cast<const uint4*>(q_s)[(nt * KS + kk) * 32 + lane];
-                  qb[nt][0] = x.x; qb[nt][1] = x.y; qb[nt][2] = x.z; qb[nt][3] = x.w;
-                } else if constexpr (NT == 1) {
-                  qb[nt][0] = qr[kk][0];
-                  qb[nt][1] = qr[kk][1];
-                } else {
-                  const uint2 x = reinterpret_cast<const uint2*>(q_s)[(nt * KS + kk) * 32 + lane];
-                  qb[nt][0] = x.x;
-                  qb[nt][1] = x.y;
-                }
-              }
-#pragma unroll
-              for (int w = 0; w < SL; ++w) {
-                const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
-                const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  if constexpr (F32) mma16816(sc[nt][w], a, qb[nt][2], qb[nt][3]);
-                  mma16816(sc[nt][w], a, qb[nt][0], qb[nt][1]);
-                }
-              }
-            }
-          }
-        } else {
-          // sum over dims of q_x step_x n_x, the queries times the steps as operands, and of q_x zero_x
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) qz[nt][0] = qz[nt][1] = qz[nt][2] = qz[nt][3] = 0.f;
-          constexpr int TERMS = F32 ? 3 : 1;
-          const uint4* kc = reinterpret_cast<const uint4*>(unit) + lane;
-          const uint4* ksteps = reinterpret_cast<const uint4*>(unit + quant4_kstep_off(D) + c * KS * 4);
-          const uint4* kzeros = reinterpret_cast<const uint4*>(unit + quant4_kzero_off(D) + c * KS * 8);
-#pragma unroll
-          for (int k4 = 0; k4 < KS / 4; ++k4) {
-            const uint4 st4 = ksteps[k4], z4[2] = {kzeros[2 * k4], kzeros[2 * k4 + 1]};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int kk = 4 * k4 + y;
-              const uint4 v = kc[kk * 32];
-              const uint2 st = steps_f16(word_of(st4, y));
-              const uint32_t z0 = word_of(z4[y / 2], 2 * (y % 2)), z1 = word_of(z4[y / 2], 2 * (y % 2) + 1), za[4] = {z0, z0, z1, z1};
-              uint32_t qs[NT][TERMS][2];
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int x = TERMS - 1; x >= 0; --x) {
-                  uint2 q;
-                  if constexpr (NT == 1 && !F32)
-                    q = make_uint2(qr[kk][0], qr[kk][1]);
-                  else
-                    q = reinterpret_cast<const uint2*>(q_s)[((nt * KS + kk) * TERMS + x) * 32 + lane];
-                  mma16816(qz[nt], za, q.x, q.y);
-                  qs[nt][x][0] = mul_f16x2(q.x, st.x);
-                  qs[nt][x][1] = mul_f16x2(q.y, st.y);
-                }
-#pragma unroll
-              for (int w = 0; w < SL; ++w) {
-                uint32_t a[4];
-                codes_f16(word_of(v, w), a);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int x = TERMS - 1; x >= 0; --x) mma16816(sc[nt][w], a, qs[nt][x][0], qs[nt][x][1]);
-              }
-            }
-          }
-        }
-        // ---- softmax over the 16 SL tokens ----
-        // (Warp-wide branches around the masks or the rescaling, and packed pairs, were all
-        // slower: they keep the next products' loads from moving up. 256 units x 65536
-        // tokens, us: as it is 669, masks behind a branch 675, packed 723.)
-        float ev[SL][2];
-#pragma unroll
-        for (int w = 0; w < SL; ++w) {
-          ev[w][0] = es[16 * (s0 + w) + tok];
-          ev[w][1] = es[16 * (s0 + w) + tok + 2];
-        }
-        const int pos = j * kQB + 16 * s0 + tok;
-        float corr[NT][2], vsc[NT][2];
-        uint32_t pb[NT][SL][2], pl[F32 ? NT : 1][SL][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float f = (NT == 1 ? fac[0][x] : rs_s[nt * 8 + 2 * c + x]) * ks * kQScale<D>;  // (the power of two first)
-            const int sees = NT == 1 ? vis[0][x] : vis_s[nt * 8 + 2 * c + x];
-            float mx = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < SL; ++w)
+              for (int w = 0; w < SL; ++w) v[w] = kw[w * 2 * D + jj * 32];
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
-                float& l = sc[nt][w][2 * y + x];
-                if constexpr (BITS == 8) {
-                  l = l * f + ev[w][y];
-                } else {  // (the codes' rows are 2^-24 and 2^-20 of what they stand for)
-                  l = l * (f * (y ? 0x1p20f : 0x1p24f)) + (qz[nt][x] * f + ev[w][y]);
-                }
-                if (ev[w][y] == -INFINITY || (edge && pos + 16 * w + 2 * y >= sees)) l = -INFINITY;
-                mx = max_nan(mx, l);
-              }
-            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mn = max_nan(m_run[nt][x], mx), mu = finite_max(mn);
-            corr[nt][x] = exp_from(m_run[nt][x], mu);
-            vsc[nt][x] = mx == -INFINITY ? 0.f : vs;  // (nothing visible: whatever the scale)
-            m_run[nt][x] = mn;
-            float sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < SL; ++w)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                float& l = sc[nt][w][2 * y + x];
-                // times 2^14: for bf16 in the exponent, which costs 2^-21.5 of a weight
-                if constexpr (F32) {
-                  l = ex2((l - mu) * kQLog2e) * 16384.f;
-                } else {
-                  l = ex2(fmaf(l - mu, kQLog2e, 14.f));
-                }
-                sum += l;
-              }
-            l_run[nt][x] = l_run[nt][x] * corr[nt][x] + sum;
-            blk_l[nt][x] = blk_l[nt][x] * corr[nt][x] + sum;
-          }
-#pragma unroll
-          for (int w = 0; w < SL; ++w)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float x0 = sc[nt][w][2 * y], x1 = sc[nt][w][2 * y + 1];
-              const uint32_t hh = f16x2(x0, x1);
-              pb[nt][w][y] = transpose8x8(hh);
-              if constexpr (F32) {
-                const float2 r = f32x2(hh);
-                pl[nt][w][y] = transpose8x8(f16x2(x0 - r.x, x1 - r.y));
-              }
-            }
-        }
-        // ---- o = o * corr + scale * (V^T P) ----
-        if constexpr (BITS == 8) {
-          const uint4* vw = kw + D;  // 16 D bytes on
-#pragma unroll
-          for (int jj = 0; jj < KS / 2; ++jj) {
-            uint4 v[SL];
-#pragma unroll
-            for (int w = 0; w < SL; ++w) v[w] = vw[w * 2 * D + jj * 32];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float t[NT][4];
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
-#pragma unroll
-              for (int w = 0; w < SL; ++w) {
-                const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
-                const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
+                const int kk = 2 * jj + y;
+                uint32_t qb[NT][F32 ? 4 : 2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  if constexpr (F32) mma16816(t[nt], a, pl[nt][w][0], pl[nt][w][1]);
-                  mma16816(t[nt], a, pb[nt][w][0], pb[nt][w][1]);
-                }
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  float& oo = o[nt][2 * jj + y][x];
-                  oo = oo * corr[nt][x & 1] + t[nt][x] * vsc[nt][x & 1];
-                }
-            }
-          }
-        } else {
-          const uint4* vc = reinterpret_cast<const uint4*>(unit + 32 * D) + lane;
-#pragma unroll
-          for (int r = 0; r < D / 64; ++r) {  // runs of 64 dims
-            const uint4* vsteps = reinterpret_cast<const uint4*>(unit + quant4_vstep_off(D) + r * 128 + c * 32);
-            const uint4* vzeros = reinterpret_cast<const uint4*>(unit + quant4_vzero_off(D) + r * 128 + c * 32);
-            const uint4 s4[2] = {vsteps[0], vsteps[1]}, z4[2] = {vzeros[0], vzeros[1]};
-            uint32_t ps[NT][SL][2], pt[F32 ? NT : 1][SL][2];  // weights times steps
-            float base[NT][2];                                // ... with the zeros
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float tz[4] = {};
-#pragma unroll
-              for (int w = 0; w < SL; ++w) {
-                const uint32_t z0 = word_of(z4[w / 2], 2 * (w % 2)), z1 = word_of(z4[w / 2], 2 * (w % 2) + 1), za[4] = {z0, z0, z1, z1};
-                if constexpr (F32) mma16816(tz, za, pl[nt][w][0], pl[nt][w][1]);
-                mma16816(tz, za, pb[nt][w][0], pb[nt][w][1]);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const uint32_t st = word_of(s4[w / 2], 2 * (w % 2) + y);
                   if constexpr (F32) {
-                    const float2 hi = f32x2(pb[nt][w][y]), lo = f32x2(pl[nt][w][y]), t = f32x2(st);
-                    const float x0 = (hi.x + lo.x) * t.x, x1 = (hi.y + lo.y) * t.y;
-                    ps[nt][w][y] = f16x2(x0, x1);
-                    const float2 r2 = f32x2(ps[nt][w][y]);
-                    pt[nt][w][y] = f16x2(x0 - r2.x, x1 - r2.y);
+                    const uint4 x = reinterpret_cast<const uint4*>(q_s)[(nt * KS + kk) * 32 + lane];
+                    qb[nt][0] = x.x; qb[nt][1] = x.y; qb[nt][2] = x.z; qb[nt][3] = x.w;
+                  } else if constexpr (NT == 1) {
+                    qb[nt][0] = qr[kk][0];
+                    qb[nt][1] = qr[kk][1];
                   } else {
-                    ps[nt][w][y] = mul_f16x2(pb[nt][w][y], st);
+                    const uint2 x = reinterpret_cast<const uint2*>(q_s)[(nt * KS + kk) * 32 + lane];
+                    qb[nt][0] = x.x;
+                    qb[nt][1] = x.y;
+                  }
+                }
+#pragma unroll
+                for (int w = 0; w < SL; ++w) {
+                  const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
+                  const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (F32) mma16816(sc[nt][w], a, qb[nt][2], qb[nt][3]);
+                    mma16816(sc[nt][w], a, qb[nt][0], qb[nt][1]);
                   }
                 }
               }
-              base[nt][0] = tz[0] * vsc[nt][0];
-              base[nt][1] = tz[1] * vsc[nt][1];
             }
+          } else {
+            // sum over dims of q_x step_x n_x, the queries times the steps as operands, and of q_x zero_x
 #pragma unroll
-            for (int m = 4 * r; m < 4 * r + 4; ++m) {
-              const uint4 v = vc[m * 32];
-              float t[NT][4];
+            for (int nt = 0; nt < NT; ++nt) qz[nt][0] = qz[nt][1] = qz[nt][2] = qz[nt][3] = 0.f;
+            constexpr int TERMS = F32 ? 3 : 1;
+            const uint4* kc = reinterpret_cast<const uint4*>(unit) + lane;
+            const uint4* ksteps = reinterpret_cast<const uint4*>(unit + quant4_kstep_off(D) + c * KS * 4);
+            const uint4* kzeros = reinterpret_cast<const uint4*>(unit + quant4_kzero_off(D) + c * KS * 8);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
+            for (int k4 = 0; k4 < KS / 4; ++k4) {
+              const uint4 st4 = ksteps[k4], z4[2] = {kzeros[2 * k4], kzeros[2 * k4 + 1]};
 #pragma unroll
-              for (int w = 0; w < SL; ++w) {
-                uint32_t a[4];
-                codes_f16(word_of(v, w), a);
+              for (int y = 0; y < 4; ++y) {
+                const int kk = 4 * k4 + y;
+                const uint4 v = kc[kk * 32];
+                const uint2 st = steps_f16(word_of(st4, y));
+                const uint32_t z0 = word_of(z4[y / 2], 2 * (y % 2)), z1 = word_of(z4[y / 2], 2 * (y % 2) + 1), za[4] = {z0, z0, z1, z1};
+                uint32_t qs[NT][TERMS][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  if constexpr (F32) mma16816(t[nt], a, pt[nt][w][0], pt[nt][w][1]);
-                  mma16816(t[nt], a, ps[nt][w][0], ps[nt][w][1]);
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int x = TERMS - 1; x >= 0; --x) {
+                    uint2 q;
+                    if constexpr (NT == 1 && !F32)
+                      q = make_uint2(qr[kk][0], qr[kk][1]);
+                    else
+                      q = reinterpret_cast<const uint2*>(q_s)[((nt * KS + kk) * TERMS + x) * 32 + lane];
+                    mma16816(qz[nt], za, q.x, q.y);
+                    qs[nt][x][0] = mul_f16x2(q.x, st.x);
+                    qs[nt][x][1] = mul_f16x2(q.y, st.y);
+                  }
+#pragma unroll
+                for (int w = 0; w < SL; ++w) {
+                  uint32_t a[4];
+                  codes_f16(word_of(v, w), a);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = TERMS - 1; x >= 0; --x) mma16816(sc[nt][w], a, qs[nt][x][0], qs[nt][x][1]);
                 }
               }
+            }
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  float& oo = o[nt][m][x];
-                  oo = oo * corr[nt][x & 1] + base[nt][x & 1] + t[nt][x] * (vsc[nt][x & 1] * (x < 2 ? 0x1p24f : 0x1p20f));
+              for (int w = 0; w < SL; ++w) codes_split(sc[nt][w]);
+          }
+          // ---- softmax over the 16 SL tokens ----
+          // (Warp-wide branches around the masks or the rescaling, and packed pairs, were all
+          // slower: they keep the next products' loads from moving up. 256 units x 65536
+          // tokens, us: as it is 669, masks behind a branch 675, packed 723.)
+          float ev[SL][2];
+#pragma unroll
+          for (int w = 0; w < SL; ++w) {
+            ev[w][0] = es[16 * (s0 + w) + tok];
+            ev[w][1] = es[16 * (s0 + w) + tok + 2];
+          }
+          const int pos = j * kQB + 16 * s0 + tok;
+          float corr[NT][2], vsc[NT][2];
+          uint32_t pb[NT][SL][2], pl[F32 ? NT : 1][SL][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float f = (NT == 1 ? fac[0][x] : rs_s[nt * 8 + 2 * c + x]) * ks * kQScale<D>;  // (the power of two first)
+              const int sees = NT == 1 ? vis[0][x] : vis_s[nt * 8 + 2 * c + x];
+              float mx = -INFINITY;
+              if constexpr (BITS == 8) {
+#pragma unroll
+                for (int w = 0; w < SL; ++w)
+#pragma unroll
+                  for (int y = 0; y < 2; ++y) {
+                    float& l = sc[nt][w][2 * y + x];
+                    l = l * f + ev[w][y];
+                    if (ev[w][y] == -INFINITY || (edge && pos + 16 * w + 2 * y >= sees)) l = -INFINITY;
+                    mx = max_nan(mx, l);
+                  }
+              } else {
+#pragma unroll
+                for (int w = 0; w < SL; ++w) {
+#pragma unroll
+                  for (int y = 0; y < 2; ++y) {
+                    float& l = sc[nt][w][2 * y + x];
+                    l = l * (f * (y ? 0x1p20f : 0x1p24f)) + (qz[nt][x] * f + ev[w][y]);
+                    if (EDGE && (ev[w][y] == -INFINITY || pos + 16 * w + 2 * y >= sees)) l = -INFINITY;
+                  }
+                  mx = max3_nan(mx, sc[nt][w][x], sc[nt][w][2 + x]);
                 }
+              }
+              mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const float mn = max_nan(m_run[nt][x], mx), mu = finite_max(mn);
+              corr[nt][x] = exp_from(m_run[nt][x], mu);
+              vsc[nt][x] = mx == -INFINITY ? 0.f : vs;  // (nothing visible: whatever the scale)
+              m_run[nt][x] = mn;
+              float sum = 0.f;
+#pragma unroll
+              for (int w = 0; w < SL; ++w)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  float& l = sc[nt][w][2 * y + x];
+                  // times 2^14: for bf16 in the exponent, which costs 2^-21.5 of a weight
+                  if constexpr (F32) {
+                    l = ex2((l - mu) * kQLog2e) * 16384.f;
+                  } else {
+                    l = ex2(fmaf(l - mu, kQLog2e, 14.f));
+                  }
+                  sum += l;
+                }
+              l_run[nt][x] = l_run[nt][x] * corr[nt][x] + sum;
+              blk_l[nt][x] = SL == 4 && BITS == 4 ? sum : blk_l[nt][x] * corr[nt][x] + sum;
+            }
+#pragma unroll
+            for (int w = 0; w < SL; ++w)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float x0 = sc[nt][w][2 * y], x1 = sc[nt][w][2 * y + 1];
+                const uint32_t hh = f16x2(x0, x1);
+                pb[nt][w][y] = transpose8x8(hh);
+                if constexpr (F32) {
+                  const float2 r = f32x2(hh);
+                  pl[nt][w][y] = transpose8x8(f16x2(x0 - r.x, x1 - r.y));
+                }
+              }
+          }
+          // ---- o = o * corr + scale * (V^T P) ----
+          if constexpr (BITS == 8) {
+            const uint4* vw = kw + D;  // 16 D bytes on
+#pragma unroll
+            for (int jj = 0; jj < KS / 2; ++jj) {
+              uint4 v[SL];
+#pragma unroll
+              for (int w = 0; w < SL; ++w) v[w] = vw[w * 2 * D + jj * 32];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                float t[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
+#pragma unroll
+                for (int w = 0; w < SL; ++w) {
+                  const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
+                  const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (F32) mma16816(t[nt], a, pl[nt][w][0], pl[nt][w][1]);
+                    mma16816(t[nt], a, pb[nt][w][0], pb[nt][w][1]);
+                  }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    float& oo = o[nt][2 * jj + y][x];
+                    oo = oo * corr[nt][x & 1] + t[nt][x] * vsc[nt][x & 1];
+                  }
+              }
+            }
+          } else {
+            const uint4* vc = reinterpret_cast<const uint4*>(unit + 32 * D) + lane;
+#pragma unroll
+            for (int r = 0; r < D / 64; ++r) {  // runs of 64 dims
+              const uint4* vsteps = reinterpret_cast<const uint4*>(unit + quant4_vstep_off(D) + r * 128 + c * 32);
+              const uint4* vzeros = reinterpret_cast<const uint4*>(unit + quant4_vzero_off(D) + r * 128 + c * 32);
+              const uint4 s4[2] = {vsteps[0], vsteps[1]}, z4[2] = {vzeros[0], vzeros[1]};
+              uint32_t ps[NT][SL][2], pt[F32 ? NT : 1][SL][2];  // weights times steps
+              float base[NT][2];                                // ... with the zeros
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float tz[4] = {};
+#pragma unroll
+                for (int w = 0; w < SL; ++w) {
+                  const uint32_t z0 = word_of(z4[w / 2], 2 * (w % 2)), z1 = word_of(z4[w / 2], 2 * (w % 2) + 1), za[4] = {z0, z0, z1, z1};
+                  if constexpr (F32) mma16816(tz, za, pl[nt][w][0], pl[nt][w][1]);
+                  mma16816(tz, za, pb[nt][w][0], pb[nt][w][1]);
+#pragma unroll
+                  for (int y = 0; y < 2; ++y) {
+                    const uint32_t st = word_of(s4[w / 2], 2 * (w % 2) + y);
+                    if constexpr (F32) {
+                      const float2 hi = f32x2(pb[nt][w][y]), lo = f32x2(pl[nt][w][y]), t = f32x2(st);
+                      const float x0 = (hi.x + lo.x) * t.x, x1 = (hi.y + lo.y) * t.y;
+                      ps[nt][w][y] = f16x2(x0, x1);
+                      const float2 r2 = f32x2(ps[nt][w][y]);
+                      pt[nt][w][y] = f16x2(x0 - r2.x, x1 - r2.y);
+                    } else {
+                      ps[nt][w][y] = mul_f16x2(pb[nt][w][y], st);
+                    }
+                  }
+                }
+                base[nt][0] = tz[0] * vsc[nt][0];
+                base[nt][1] = tz[1] * vsc[nt][1];
+              }
+#pragma unroll
+              for (int m = 4 * r; m < 4 * r + 4; ++m) {
+                const uint4 v = vc[m * 32];
+                float t[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
+#pragma unroll
+                for (int w = 0; w < SL; ++w) {
+                  uint32_t a[4];
+                  codes_f16(word_of(v, w), a);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (F32) mma16816(t[nt], a, pt[nt][w][0], pt[nt][w][1]);
+                    mma16816(t[nt], a, ps[nt][w][0], ps[nt][w][1]);
+                  }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) codes_split(t[nt]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    float& oo = o[nt][m][x];
+                    oo = oo * corr[nt][x & 1] + base[nt][x & 1] + t[nt][x] * (vsc[nt][x & 1] * (x < 2 ? 0x1p24f : 0x1p20f));
+                  }
+              }
             }
           }
         }
+      };
+      if constexpr (BITS == 8) {
+        block(std::true_type());
+      } else if (!null_unit) {
+        // A masked token's logit is -inf by the sum, whatever its key, unless the block's steps or zeros
+        // are no numbers: then its rows are NaN by any token that is not masked, and a block without
+        // one is passed over. Rows that do not see the whole block look at every token. (A check of every
+        // token in every block: 413 us at 256 units x 65536 tokens.)
+        const bool live = es[lane] != -INFINITY || es[lane + 32] != -INFINITY;
+        if (__any_sync(0xffffffffu, edge))
+          block(std::true_type());
+        else if (__any_sync(0xffffffffu, live))
+          block(std::false_type());
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
@@ -1060,7 +1112,7 @@ constexpr int kQcRows = 8;
 // 80 beside a bf16 stream, and the values come along with the keys.
 template <typename T, int D> constexpr int kQcPerSm = D == 64 ? (sizeof(T) == 4 ? 6 : 5) : 3;
 
-template <typename T, int D, int BITS>
+template <typename T, int D>
 __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kernel(QStreamParams p, int rows, bool weights) {
   constexpr int ELT = (int)sizeof(T), CE = 16 / ELT, NCH = D / CE;
   constexpr int KC = NCH / 4;                        // 16-byte key chunks of a thread: token tid % 64
@@ -1109,17 +1161,8 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
       const T* src = reinterpret_cast<const T*>(p.q) + b * p.qs.b + w.t * p.qs.t + (h * p.G + w.g) * p.qs.h + x * CE;
       const uint4 y = __ldcg(reinterpret_cast<const uint4*>(src));
       const T* e = reinterpret_cast<const T*>(&y);
-      if constexpr (BITS == 8) {
 #pragma unroll
-        for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = to_f32(e[k]) * kQScale<D>;
-      } else {
-        float f[CE];
-#pragma unroll
-        for (int k = 0; k < CE; ++k) f[k] = to_f32(e[k]);
-        if (p.rope.pairs > 0) rope_turn_vec<T, CE, true>(p.rope, src - x * CE, (long long)b * p.T + w.t, x * CE, f);
-#pragma unroll
-        for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = f[k] * kQScale<D>;
-      }
+      for (int k = 0; k < CE; ++k) q_s[r * D + x * CE + k] = to_f32(e[k]) * kQScale<D>;
     }
     __syncthreads();
 #pragma unroll
@@ -1437,7 +1480,7 @@ cudaError_t stream_launches(const Shape& s, const QPlan& pl, const QStreamParams
   // 54.3, 256 96.7 / 95.5, 512 105.4 / 100.0 (ragged); four CTAs a unit at 16 units: 375
   // blocks 27.1 / 27.6.
   const bool joined = p.mass != nullptr && pl.rows == kQcRows && p.max_blocks <= 128 * z;
-  e = launch_dependent(quant_combine_kernel<T, D, BITS>, dim3(vu, y, z), kQcThreads, 0, stream, p, pl.rows, joined);
+  e = launch_dependent(quant_combine_kernel<T, D>, dim3(vu, y, z), kQcThreads, 0, stream, p, pl.rows, joined);
   if (e != cudaSuccess || p.mass == nullptr || joined) return e;
   auto weights = [&](auto kernel, int per) {
     return launch_dependent(kernel, dim3(s.U, (p.max_blocks + per - 1) / per), kQcThreads, 0, stream, p);

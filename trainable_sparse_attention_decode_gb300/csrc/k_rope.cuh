@@ -21,7 +21,6 @@ struct RopeArgs {
   long long axis_stride; // batch x n
   int len, pairs;        // positions of the table; pairs of a row (0: no rotation)
   int interleaved;       // pairs (2i, 2i + 1) instead of (i, i + pairs)
-  int one_axis;          // every pair's axis is 0
   uint32_t axes[kRopeMaxAxes];  // axis of pair i: bits 2 (i % 16) of word i / 16
   int* status;
 };
@@ -70,41 +69,98 @@ __device__ __forceinline__ float rope_turn(float x, float other, bool first, flo
   return first ? __fsub_rn(a, b) : __fadd_rn(a, b);
 }
 
-// The N elements x0, x0 + 1, ... of a row, f, turned in place and rounded to T (N a power of
-// two from 2 to 8, x0 a multiple of it, all of them in one half where pairs are halves).
-template <typename T, int N, bool EARLY>
-__device__ __forceinline__ void rope_turn_vec(const RopeArgs& p, const T* row, long long at, int x0, float* f) {
-  if (x0 >= 2 * p.pairs) return;
-  float g[N];  // the other ones of the pairs
-  int pair0;
-  const bool first = x0 < p.pairs;
-  if (p.interleaved) {
-    pair0 = x0 / 2;
-#pragma unroll
-    for (int k = 0; k < N; ++k) g[k] = f[k ^ 1];
-  } else {
-    pair0 = first ? x0 : x0 - p.pairs;
-    const T* src = row + (first ? x0 + p.pairs : x0 - p.pairs);
-    using V = typename std::conditional<N * sizeof(T) == 16, uint4, uint2>::type;
-    const V raw = rope_load<EARLY>(reinterpret_cast<const V*>(src));
-    const T* o = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-    for (int k = 0; k < N; ++k) g[k] = to_f32(o[k]);
-  }
-  // one position for pairs of one axis, which are two to a 16-byte load; else each its own
-  const int last = pair0 + (p.interleaved ? N / 2 : N) - 1;
-  bool one = true;
-  for (int i = pair0; i < last && !p.one_axis; ++i) one &= rope_axis(p, i) == rope_axis(p, last);
-  float2 cs[N];
-  const float2* at0 = p.table + (long long)rope_position<EARLY>(p, at, pair0) * p.pairs;
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const int i = pair0 + (p.interleaved ? k / 2 : k);
-    cs[k] = rope_load<EARLY>((one ? at0 : p.table + (long long)rope_position<EARLY>(p, at, i) * p.pairs) + i);
-  }
-#pragma unroll
-  for (int k = 0; k < N; ++k) f[k] = to_f32(from_f32<T>(rope_turn(f[k], g[k], p.interleaved ? k % 2 == 0 : first, cs[k])));
+// Chunk i of d / 16: sixteen elements of a row, two vectors of eight. Where pairs are halves,
+// a turned chunk has eight of each half; others are sixteen in a row.
+struct RopeChunk {
+  int lo, hi;  // where its vectors begin
+  bool turned;
+};
+__device__ __forceinline__ RopeChunk rope_chunk(const RopeArgs& p, int i) {
+  const bool turned = 8 * i < p.pairs;
+  const bool split = turned && !p.interleaved;
+  return {split ? 8 * i : 16 * i, split ? p.pairs + 8 * i : 16 * i + 8, turned};
 }
+
+// Cosines and sines of pairs 8 i .. 8 i + 7 of token row `at`: four 16-byte loads where the
+// pairs have one axis.
+template <bool EARLY>
+__device__ __forceinline__ void rope_angles(const RopeArgs& p, long long at, int i, float2* cs) {
+  uint32_t w = p.axes[0] >> (16 * (i & 1));
+#pragma unroll
+  for (int k = 1; k < kRopeMaxAxes; ++k)
+    if (i / 2 == k) w = p.axes[k] >> (16 * (i & 1));
+  w &= 0xFFFFu;
+  if (w == (w & 3u) * 0x5555u) {
+    const float4* src = reinterpret_cast<const float4*>(p.table + (long long)rope_position<EARLY>(p, at, 8 * i) * p.pairs + 8 * i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 x = rope_load<EARLY>(src + k);
+      cs[2 * k] = make_float2(x.x, x.y);
+      cs[2 * k + 1] = make_float2(x.z, x.w);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) cs[k] = rope_load<EARLY>(p.table + (long long)rope_position<EARLY>(p, at, 8 * i + k) * p.pairs + 8 * i + k);
+  }
+}
+// The sixteen elements of a turned chunk, unrounded.
+__device__ __forceinline__ void rope_turn_chunk(bool interleaved, const float2* cs, float* x) {
+  if (interleaved) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = x[2 * k], b = x[2 * k + 1];
+      x[2 * k] = rope_turn(a, b, true, cs[k]);
+      x[2 * k + 1] = rope_turn(b, a, false, cs[k]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = x[k], b = x[8 + k];
+      x[k] = rope_turn(a, b, true, cs[k]);
+      x[8 + k] = rope_turn(b, a, false, cs[k]);
+    }
+  }
+}
+
+// Eight elements in registers, as they are in memory.
+template <typename T> struct Vec8;
+template <> struct Vec8<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = r; }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = bf16_lo(r.x); f[1] = bf16_hi(r.x); f[2] = bf16_lo(r.y); f[3] = bf16_hi(r.y);
+    f[4] = bf16_lo(r.z); f[5] = bf16_hi(r.z); f[6] = bf16_lo(r.w); f[7] = bf16_hi(r.w);
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    r = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <> struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
 
 #endif
 
@@ -115,7 +171,8 @@ struct RotateArgs {
   long long in_b[2], in_t[2], in_h[2], out_b[2], out_t[2], out_h[2];  // elements between requests, tokens, heads
   int heads[2];
   int n, backward;
-  long long rows;      // batch x n
+  const int32_t* count;  // [batch] rows of a request that exist, or null
+  long long rows;        // batch x n
 };
 cudaError_t launch_rotate(const Shape& s, const RotateArgs& a, cudaStream_t stream);
 

@@ -28,7 +28,6 @@ nosa_status take_rope(const nosa_config& cfg, const nosa_rope* rope, const int32
   out.axis_stride = (long long)cfg.batch * n;
   out.len = rope->table_len;
   out.interleaved = rope->interleaved != 0;
-  out.one_axis = (out.axes[0] | out.axes[1] | out.axes[2] | out.axes[3]) == 0;
   out.status = status;
   return NOSA_OK;
 }
@@ -123,7 +122,7 @@ nosa_status nosa_quant4_read(const nosa_config* cfg, const void* units, int64_t 
 size_t nosa_quant4_attention_workspace_bytes(const nosa_config* cfg, int32_t max_blocks, int32_t n_queries, int32_t with_mass) {
   if (check_cache(cfg, max_blocks) != NOSA_OK || n_queries < 1 || n_queries > kQMaxQueries) return 0;
   DeviceGuard guard(cfg->device);
-  return quant_attn_workspace(quant_shape(*cfg), max_blocks, n_queries, with_mass != 0);
+  return quant4_attn_workspace(quant_shape(*cfg), max_blocks, n_queries, with_mass != 0);
 }
 
 nosa_status nosa_quant4_attention(const nosa_config* cfg, int32_t max_blocks, int32_t n_queries, const void* units,
@@ -141,7 +140,7 @@ nosa_status nosa_quant4_attention(const nosa_config* cfg, int32_t max_blocks, in
   RopeArgs r;
   if ((st = take_rope(*cfg, rope, positions, n_queries, status, r)) != NOSA_OK) return st;
   DeviceGuard guard(cfg->device);
-  if (workspace_bytes < quant_attn_workspace(s, max_blocks, n_queries, mass != nullptr))
+  if (workspace_bytes < quant4_attn_workspace(s, max_blocks, n_queries, mass != nullptr))
     return invalid("workspace too small (see nosa_quant4_attention_workspace_bytes)");
   return launched(launch_quant4_attention(s, a, r, static_cast<cudaStream_t>(stream)), "4-bit cache attention");
 }
