@@ -752,289 +752,273 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
       float blk_l[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) blk_l[nt][0] = blk_l[nt][1] = 0.f;
-      auto block = [&](auto edge_tag) {
-        constexpr bool EDGE = decltype(edge_tag)::value;
 #pragma unroll
-        for (int s0 = 0; s0 < 4; s0 += SL) {
-          if (BITS == 8 && null_unit) break;
-          const uint4* kw = reinterpret_cast<const uint4*>(unit) + s0 * 2 * D + lane;
-          // ---- logits ----
-          float sc[NT][SL][4];
+      for (int s0 = 0; s0 < 4; s0 += SL) {
+        if (null_unit) break;
+        const uint4* kw = reinterpret_cast<const uint4*>(unit) + s0 * 2 * D + lane;
+        // ---- logits ----
+        float sc[NT][SL][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int w = 0; w < SL; ++w) sc[nt][w][0] = sc[nt][w][1] = sc[nt][w][2] = sc[nt][w][3] = 0.f;
-          float qz[BITS == 4 ? NT : 1][4];  // the queries' products with the zeros, in every row alike
-          if constexpr (BITS == 8) {
+          for (int w = 0; w < SL; ++w) sc[nt][w][0] = sc[nt][w][1] = sc[nt][w][2] = sc[nt][w][3] = 0.f;
+        float qz[BITS == 4 ? NT : 1][4];  // the queries' products with the zeros, in every row alike
+        if constexpr (BITS == 8) {
 #pragma unroll
-            for (int jj = 0; jj < KS / 2; ++jj) {
-              uint4 v[SL];
+          for (int jj = 0; jj < KS / 2; ++jj) {
+            uint4 v[SL];
 #pragma unroll
-              for (int w = 0; w < SL; ++w) v[w] = kw[w * 2 * D + jj * 32];
+            for (int w = 0; w < SL; ++w) v[w] = kw[w * 2 * D + jj * 32];
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const int kk = 2 * jj + y;
-                uint32_t qb[NT][F32 ? 4 : 2];
+            for (int y = 0; y < 2; ++y) {
+              const int kk = 2 * jj + y;
+              uint32_t qb[NT][F32 ? 4 : 2];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (F32) {
+                  const uint4 x = reinterpret_cast<const uint4*>(q_s)[(nt * KS + kk) * 32 + lane];
+                  qb[nt][0] = x.x; qb[nt][1] = x.y; qb[nt][2] = x.z; qb[nt][3] = x.w;
+                } else if constexpr (NT == 1) {
+                  qb[nt][0] = qr[kk][0];
+                  qb[nt][1] = qr[kk][1];
+                } else {
+                  const uint2 x = reinterpret_cast<const uint2*>(q_s)[(nt * KS + kk) * 32 + lane];
+                  qb[nt][0] = x.x;
+                  qb[nt][1] = x.y;
+                }
+              }
+#pragma unroll
+              for (int w = 0; w < SL; ++w) {
+                const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
+                const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  if constexpr (F32) {
-                    const uint4 x = reinterpret_cast<const uint4*>(q_s)[(nt * KS + kk) * 32 + lane];
-                    qb[nt][0] = x.x; qb[nt][1] = x.y; qb[nt][2] = x.z; qb[nt][3] = x.w;
-                  } else if constexpr (NT == 1) {
-                    qb[nt][0] = qr[kk][0];
-                    qb[nt][1] = qr[kk][1];
-                  } else {
-                    const uint2 x = reinterpret_cast<const uint2*>(q_s)[(nt * KS + kk) * 32 + lane];
-                    qb[nt][0] = x.x;
-                    qb[nt][1] = x.y;
-                  }
-                }
-#pragma unroll
-                for (int w = 0; w < SL; ++w) {
-                  const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
-                  const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (F32) mma16816(sc[nt][w], a, qb[nt][2], qb[nt][3]);
-                    mma16816(sc[nt][w], a, qb[nt][0], qb[nt][1]);
-                  }
+                  if constexpr (F32) mma16816(sc[nt][w], a, qb[nt][2], qb[nt][3]);
+                  mma16816(sc[nt][w], a, qb[nt][0], qb[nt][1]);
                 }
               }
             }
-          } else {
-            // sum over dims of q_x step_x n_x, the queries times the steps as operands, and of q_x zero_x
+          }
+        } else {
+          // sum over dims of q_x step_x n_x, the queries times the steps as operands, and of q_x zero_x
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) qz[nt][0] = qz[nt][1] = qz[nt][2] = qz[nt][3] = 0.f;
-            constexpr int TERMS = F32 ? 3 : 1;
-            const uint4* kc = reinterpret_cast<const uint4*>(unit) + lane;
-            const uint4* ksteps = reinterpret_cast<const uint4*>(unit + quant4_kstep_off(D) + c * KS * 4);
-            const uint4* kzeros = reinterpret_cast<const uint4*>(unit + quant4_kzero_off(D) + c * KS * 8);
+          for (int nt = 0; nt < NT; ++nt) qz[nt][0] = qz[nt][1] = qz[nt][2] = qz[nt][3] = 0.f;
+          constexpr int TERMS = F32 ? 3 : 1;
+          const uint4* kc = reinterpret_cast<const uint4*>(unit) + lane;
+          const uint4* ksteps = reinterpret_cast<const uint4*>(unit + quant4_kstep_off(D) + c * KS * 4);
+          const uint4* kzeros = reinterpret_cast<const uint4*>(unit + quant4_kzero_off(D) + c * KS * 8);
 #pragma unroll
-            for (int k4 = 0; k4 < KS / 4; ++k4) {
-              const uint4 st4 = ksteps[k4], z4[2] = {kzeros[2 * k4], kzeros[2 * k4 + 1]};
+          for (int k4 = 0; k4 < KS / 4; ++k4) {
+            const uint4 st4 = ksteps[k4], z4[2] = {kzeros[2 * k4], kzeros[2 * k4 + 1]};
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int kk = 4 * k4 + y;
-                const uint4 v = kc[kk * 32];
-                const uint2 st = steps_f16(word_of(st4, y));
-                const uint32_t z0 = word_of(z4[y / 2], 2 * (y % 2)), z1 = word_of(z4[y / 2], 2 * (y % 2) + 1), za[4] = {z0, z0, z1, z1};
-                uint32_t qs[NT][TERMS][2];
+            for (int y = 0; y < 4; ++y) {
+              const int kk = 4 * k4 + y;
+              const uint4 v = kc[kk * 32];
+              const uint2 st = steps_f16(word_of(st4, y));
+              const uint32_t z0 = word_of(z4[y / 2], 2 * (y % 2)), z1 = word_of(z4[y / 2], 2 * (y % 2) + 1), za[4] = {z0, z0, z1, z1};
+              uint32_t qs[NT][TERMS][2];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = TERMS - 1; x >= 0; --x) {
+                  uint2 q;
+                  if constexpr (NT == 1 && !F32)
+                    q = make_uint2(qr[kk][0], qr[kk][1]);
+                  else
+                    q = reinterpret_cast<const uint2*>(q_s)[((nt * KS + kk) * TERMS + x) * 32 + lane];
+                  mma16816(qz[nt], za, q.x, q.y);
+                  qs[nt][x][0] = mul_f16x2(q.x, st.x);
+                  qs[nt][x][1] = mul_f16x2(q.y, st.y);
+                }
+#pragma unroll
+              for (int w = 0; w < SL; ++w) {
+                uint32_t a[4];
+                codes_f16(word_of(v, w), a);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                  for (int x = TERMS - 1; x >= 0; --x) {
-                    uint2 q;
-                    if constexpr (NT == 1 && !F32)
-                      q = make_uint2(qr[kk][0], qr[kk][1]);
-                    else
-                      q = reinterpret_cast<const uint2*>(q_s)[((nt * KS + kk) * TERMS + x) * 32 + lane];
-                    mma16816(qz[nt], za, q.x, q.y);
-                    qs[nt][x][0] = mul_f16x2(q.x, st.x);
-                    qs[nt][x][1] = mul_f16x2(q.y, st.y);
-                  }
-#pragma unroll
-                for (int w = 0; w < SL; ++w) {
-                  uint32_t a[4];
-                  codes_f16(word_of(v, w), a);
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int x = TERMS - 1; x >= 0; --x) mma16816(sc[nt][w], a, qs[nt][x][0], qs[nt][x][1]);
-                }
+                  for (int x = TERMS - 1; x >= 0; --x) mma16816(sc[nt][w], a, qs[nt][x][0], qs[nt][x][1]);
               }
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int w = 0; w < SL; ++w) codes_split(sc[nt][w]);
           }
-          // ---- softmax over the 16 SL tokens ----
-          // (Warp-wide branches around the masks or the rescaling, and packed pairs, were all
-          // slower: they keep the next products' loads from moving up. 256 units x 65536
-          // tokens, us: as it is 669, masks behind a branch 675, packed 723.)
-          float ev[SL][2];
 #pragma unroll
-          for (int w = 0; w < SL; ++w) {
-            ev[w][0] = es[16 * (s0 + w) + tok];
-            ev[w][1] = es[16 * (s0 + w) + tok + 2];
-          }
-          const int pos = j * kQB + 16 * s0 + tok;
-          float corr[NT][2], vsc[NT][2];
-          uint32_t pb[NT][SL][2], pl[F32 ? NT : 1][SL][2];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+            for (int w = 0; w < SL; ++w) codes_split(sc[nt][w]);
+        }
+        // ---- softmax over the 16 SL tokens ----
+        // (Warp-wide branches around the masks or the rescaling, and packed pairs, were all
+        // slower: they keep the next products' loads from moving up. 256 units x 65536
+        // tokens, us: as it is 669, masks behind a branch 675, packed 723.)
+        float ev[SL][2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float f = (NT == 1 ? fac[0][x] : rs_s[nt * 8 + 2 * c + x]) * ks * kQScale<D>;  // (the power of two first)
-              const int sees = NT == 1 ? vis[0][x] : vis_s[nt * 8 + 2 * c + x];
-              float mx = -INFINITY;
-              if constexpr (BITS == 8) {
+        for (int w = 0; w < SL; ++w) {
+          ev[w][0] = es[16 * (s0 + w) + tok];
+          ev[w][1] = es[16 * (s0 + w) + tok + 2];
+        }
+        const int pos = j * kQB + 16 * s0 + tok;
+        float corr[NT][2], vsc[NT][2];
+        uint32_t pb[NT][SL][2], pl[F32 ? NT : 1][SL][2];
 #pragma unroll
-                for (int w = 0; w < SL; ++w)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                  for (int y = 0; y < 2; ++y) {
-                    float& l = sc[nt][w][2 * y + x];
-                    l = l * f + ev[w][y];
-                    if (ev[w][y] == -INFINITY || (edge && pos + 16 * w + 2 * y >= sees)) l = -INFINITY;
-                    mx = max_nan(mx, l);
-                  }
-              } else {
-#pragma unroll
-                for (int w = 0; w < SL; ++w) {
-#pragma unroll
-                  for (int y = 0; y < 2; ++y) {
-                    float& l = sc[nt][w][2 * y + x];
-                    l = l * (f * (y ? 0x1p20f : 0x1p24f)) + (qz[nt][x] * f + ev[w][y]);
-                    if (EDGE && (ev[w][y] == -INFINITY || pos + 16 * w + 2 * y >= sees)) l = -INFINITY;
-                  }
-                  mx = max3_nan(mx, sc[nt][w][x], sc[nt][w][2 + x]);
-                }
-              }
-              mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float mn = max_nan(m_run[nt][x], mx), mu = finite_max(mn);
-              corr[nt][x] = exp_from(m_run[nt][x], mu);
-              vsc[nt][x] = mx == -INFINITY ? 0.f : vs;  // (nothing visible: whatever the scale)
-              m_run[nt][x] = mn;
-              float sum = 0.f;
+          for (int x = 0; x < 2; ++x) {
+            const float f = (NT == 1 ? fac[0][x] : rs_s[nt * 8 + 2 * c + x]) * ks * kQScale<D>;  // (the power of two first)
+            const int sees = NT == 1 ? vis[0][x] : vis_s[nt * 8 + 2 * c + x];
+            float mx = -INFINITY;
+            if constexpr (BITS == 8) {
 #pragma unroll
               for (int w = 0; w < SL; ++w)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   float& l = sc[nt][w][2 * y + x];
-                  // times 2^14: for bf16 in the exponent, which costs 2^-21.5 of a weight
-                  if constexpr (F32) {
-                    l = ex2((l - mu) * kQLog2e) * 16384.f;
-                  } else {
-                    l = ex2(fmaf(l - mu, kQLog2e, 14.f));
-                  }
-                  sum += l;
+                  l = l * f + ev[w][y];
+                  if (ev[w][y] == -INFINITY || (edge && pos + 16 * w + 2 * y >= sees)) l = -INFINITY;
+                  mx = max_nan(mx, l);
                 }
-              l_run[nt][x] = l_run[nt][x] * corr[nt][x] + sum;
-              blk_l[nt][x] = SL == 4 && BITS == 4 ? sum : blk_l[nt][x] * corr[nt][x] + sum;
+            } else {
+#pragma unroll
+              for (int w = 0; w < SL; ++w) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  float& l = sc[nt][w][2 * y + x];
+                  l = l * (f * (y ? 0x1p20f : 0x1p24f)) + (qz[nt][x] * f + ev[w][y]);
+                  if (ev[w][y] == -INFINITY || (edge && pos + 16 * w + 2 * y >= sees)) l = -INFINITY;
+                }
+                mx = max3_nan(mx, sc[nt][w][x], sc[nt][w][2 + x]);
+              }
             }
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = max_nan(m_run[nt][x], mx), mu = finite_max(mn);
+            corr[nt][x] = exp_from(m_run[nt][x], mu);
+            vsc[nt][x] = mx == -INFINITY ? 0.f : vs;  // (nothing visible: whatever the scale)
+            m_run[nt][x] = mn;
+            float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < SL; ++w)
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
-                const float x0 = sc[nt][w][2 * y], x1 = sc[nt][w][2 * y + 1];
-                const uint32_t hh = f16x2(x0, x1);
-                pb[nt][w][y] = transpose8x8(hh);
+                float& l = sc[nt][w][2 * y + x];
+                // times 2^14: for bf16 in the exponent, which costs 2^-21.5 of a weight
                 if constexpr (F32) {
-                  const float2 r = f32x2(hh);
-                  pl[nt][w][y] = transpose8x8(f16x2(x0 - r.x, x1 - r.y));
+                  l = ex2((l - mu) * kQLog2e) * 16384.f;
+                } else {
+                  l = ex2(fmaf(l - mu, kQLog2e, 14.f));
                 }
+                sum += l;
               }
+            l_run[nt][x] = l_run[nt][x] * corr[nt][x] + sum;
+            blk_l[nt][x] = SL == 4 && BITS == 4 ? sum : blk_l[nt][x] * corr[nt][x] + sum;
           }
-          // ---- o = o * corr + scale * (V^T P) ----
-          if constexpr (BITS == 8) {
-            const uint4* vw = kw + D;  // 16 D bytes on
 #pragma unroll
-            for (int jj = 0; jj < KS / 2; ++jj) {
-              uint4 v[SL];
+          for (int w = 0; w < SL; ++w)
 #pragma unroll
-              for (int w = 0; w < SL; ++w) v[w] = vw[w * 2 * D + jj * 32];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                float t[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
-#pragma unroll
-                for (int w = 0; w < SL; ++w) {
-                  const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
-                  const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (F32) mma16816(t[nt], a, pl[nt][w][0], pl[nt][w][1]);
-                    mma16816(t[nt], a, pb[nt][w][0], pb[nt][w][1]);
-                  }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    float& oo = o[nt][2 * jj + y][x];
-                    oo = oo * corr[nt][x & 1] + t[nt][x] * vsc[nt][x & 1];
-                  }
+            for (int y = 0; y < 2; ++y) {
+              const float x0 = sc[nt][w][2 * y], x1 = sc[nt][w][2 * y + 1];
+              const uint32_t hh = f16x2(x0, x1);
+              pb[nt][w][y] = transpose8x8(hh);
+              if constexpr (F32) {
+                const float2 r = f32x2(hh);
+                pl[nt][w][y] = transpose8x8(f16x2(x0 - r.x, x1 - r.y));
               }
             }
-          } else {
-            const uint4* vc = reinterpret_cast<const uint4*>(unit + 32 * D) + lane;
+        }
+        // ---- o = o * corr + scale * (V^T P) ----
+        if constexpr (BITS == 8) {
+          const uint4* vw = kw + D;  // 16 D bytes on
 #pragma unroll
-            for (int r = 0; r < D / 64; ++r) {  // runs of 64 dims
-              const uint4* vsteps = reinterpret_cast<const uint4*>(unit + quant4_vstep_off(D) + r * 128 + c * 32);
-              const uint4* vzeros = reinterpret_cast<const uint4*>(unit + quant4_vzero_off(D) + r * 128 + c * 32);
-              const uint4 s4[2] = {vsteps[0], vsteps[1]}, z4[2] = {vzeros[0], vzeros[1]};
-              uint32_t ps[NT][SL][2], pt[F32 ? NT : 1][SL][2];  // weights times steps
-              float base[NT][2];                                // ... with the zeros
+          for (int jj = 0; jj < KS / 2; ++jj) {
+            uint4 v[SL];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float tz[4] = {};
+            for (int w = 0; w < SL; ++w) v[w] = vw[w * 2 * D + jj * 32];
 #pragma unroll
-                for (int w = 0; w < SL; ++w) {
-                  const uint32_t z0 = word_of(z4[w / 2], 2 * (w % 2)), z1 = word_of(z4[w / 2], 2 * (w % 2) + 1), za[4] = {z0, z0, z1, z1};
-                  if constexpr (F32) mma16816(tz, za, pl[nt][w][0], pl[nt][w][1]);
-                  mma16816(tz, za, pb[nt][w][0], pb[nt][w][1]);
+            for (int y = 0; y < 2; ++y) {
+              float t[NT][4];
 #pragma unroll
-                  for (int y = 0; y < 2; ++y) {
-                    const uint32_t st = word_of(s4[w / 2], 2 * (w % 2) + y);
-                    if constexpr (F32) {
-                      const float2 hi = f32x2(pb[nt][w][y]), lo = f32x2(pl[nt][w][y]), t = f32x2(st);
-                      const float x0 = (hi.x + lo.x) * t.x, x1 = (hi.y + lo.y) * t.y;
-                      ps[nt][w][y] = f16x2(x0, x1);
-                      const float2 r2 = f32x2(ps[nt][w][y]);
-                      pt[nt][w][y] = f16x2(x0 - r2.x, x1 - r2.y);
-                    } else {
-                      ps[nt][w][y] = mul_f16x2(pb[nt][w][y], st);
-                    }
-                  }
+              for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
+#pragma unroll
+              for (int w = 0; w < SL; ++w) {
+                const uint32_t w0 = y ? v[w].z : v[w].x, w1 = y ? v[w].w : v[w].y;
+                const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2(w0 >> 16), e4m3x2_f16x2(w1 >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if constexpr (F32) mma16816(t[nt], a, pl[nt][w][0], pl[nt][w][1]);
+                  mma16816(t[nt], a, pb[nt][w][0], pb[nt][w][1]);
                 }
-                base[nt][0] = tz[0] * vsc[nt][0];
-                base[nt][1] = tz[1] * vsc[nt][1];
               }
 #pragma unroll
-              for (int m = 4 * r; m < 4 * r + 4; ++m) {
-                const uint4 v = vc[m * 32];
-                float t[NT][4];
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
+                for (int x = 0; x < 4; ++x) {
+                  float& oo = o[nt][2 * jj + y][x];
+                  oo = oo * corr[nt][x & 1] + t[nt][x] * vsc[nt][x & 1];
+                }
+            }
+          }
+        } else {
+          const uint4* vc = reinterpret_cast<const uint4*>(unit + 32 * D) + lane;
 #pragma unroll
-                for (int w = 0; w < SL; ++w) {
-                  uint32_t a[4];
-                  codes_f16(word_of(v, w), a);
+          for (int r = 0; r < D / 64; ++r) {  // runs of 64 dims
+            const uint4* vsteps = reinterpret_cast<const uint4*>(unit + quant4_vstep_off(D) + r * 128 + c * 32);
+            const uint4* vzeros = reinterpret_cast<const uint4*>(unit + quant4_vzero_off(D) + r * 128 + c * 32);
+            const uint4 s4[2] = {vsteps[0], vsteps[1]}, z4[2] = {vzeros[0], vzeros[1]};
+            uint32_t ps[NT][SL][2], pt[F32 ? NT : 1][SL][2];  // weights times steps
+            float base[NT][2];                                // ... with the zeros
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    if constexpr (F32) mma16816(t[nt], a, pt[nt][w][0], pt[nt][w][1]);
-                    mma16816(t[nt], a, ps[nt][w][0], ps[nt][w][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              float tz[4] = {};
+#pragma unroll
+              for (int w = 0; w < SL; ++w) {
+                const uint32_t z0 = word_of(z4[w / 2], 2 * (w % 2)), z1 = word_of(z4[w / 2], 2 * (w % 2) + 1), za[4] = {z0, z0, z1, z1};
+                if constexpr (F32) mma16816(tz, za, pl[nt][w][0], pl[nt][w][1]);
+                mma16816(tz, za, pb[nt][w][0], pb[nt][w][1]);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t st = word_of(s4[w / 2], 2 * (w % 2) + y);
+                  if constexpr (F32) {
+                    const float2 hi = f32x2(pb[nt][w][y]), lo = f32x2(pl[nt][w][y]), t = f32x2(st);
+                    const float x0 = (hi.x + lo.x) * t.x, x1 = (hi.y + lo.y) * t.y;
+                    ps[nt][w][y] = f16x2(x0, x1);
+                    const float2 r2 = f32x2(ps[nt][w][y]);
+                    pt[nt][w][y] = f16x2(x0 - r2.x, x1 - r2.y);
+                  } else {
+                    ps[nt][w][y] = mul_f16x2(pb[nt][w][y], st);
                   }
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) codes_split(t[nt]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    float& oo = o[nt][m][x];
-                    oo = oo * corr[nt][x & 1] + base[nt][x & 1] + t[nt][x] * (vsc[nt][x & 1] * (x < 2 ? 0x1p24f : 0x1p20f));
-                  }
               }
+              base[nt][0] = tz[0] * vsc[nt][0];
+              base[nt][1] = tz[1] * vsc[nt][1];
+            }
+#pragma unroll
+            for (int m = 4 * r; m < 4 * r + 4; ++m) {
+              const uint4 v = vc[m * 32];
+              float t[NT][4];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.f;
+#pragma unroll
+              for (int w = 0; w < SL; ++w) {
+                uint32_t a[4];
+                codes_f16(word_of(v, w), a);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if constexpr (F32) mma16816(t[nt], a, pt[nt][w][0], pt[nt][w][1]);
+                  mma16816(t[nt], a, ps[nt][w][0], ps[nt][w][1]);
+                }
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) codes_split(t[nt]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  float& oo = o[nt][m][x];
+                  oo = oo * corr[nt][x & 1] + base[nt][x & 1] + t[nt][x] * (vsc[nt][x & 1] * (x < 2 ? 0x1p24f : 0x1p20f));
+                }
             }
           }
         }
-      };
-      if constexpr (BITS == 8) {
-        block(std::true_type());
-      } else if (!null_unit) {
-        // A masked token's logit is -inf by the sum, whatever its key, unless the block's steps or zeros
-        // are no numbers: then its rows are NaN by any token that is not masked, and a block without
-        // one is passed over. Rows that do not see the whole block look at every token. (A check of every
-        // token in every block: 413 us at 256 units x 65536 tokens.)
-        const bool live = es[lane] != -INFINITY || es[lane + 32] != -INFINITY;
-        if (__any_sync(0xffffffffu, edge))
-          block(std::true_type());
-        else if (__any_sync(0xffffffffu, live))
-          block(std::false_type());
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
