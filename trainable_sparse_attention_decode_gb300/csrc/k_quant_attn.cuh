@@ -220,13 +220,18 @@ struct QGeom {
   // 4 slots and 8 stages 677, 3 and 9 671, 5 and 10 694, 3 and 6 721, 6 and 6 745, 2 and 8
   // 907 (two warps cannot keep up); the first leaves shared memory for the join's CTAs to
   // wait on the same SMs. d = 64 (64 units x 16384), 8 and 16 33.6, 4 and 16 33.9, 8 and 8 41.
-  static constexpr int IS = NT == 2 ? 6 / RG : RG > 1 ? 8 / RG : D == 128 && BITS == 8 ? 4 : 8;
+  // 4 bits are less to copy and hardly less to compute: with them as many warps as the registers
+  // allow for, 12 of 128 for more than 8 rows (d = 128, 32 rows over 32 units of 8200 tokens: 6 warps of
+  // two row groups of 16 46.9 us, 8 of four groups 44.9, 12 43.8), and a longer ring: us at 8 rows of
+  // d = 128, 256 units x 65536 tokens (d = 64, 256 units x 16384), 8 slots and 8 stages 576, 4 and 16 515,
+  // 9 and 18 461, 8 and 16 404 (82.6), 8 and 24 (74.8).
+  static constexpr int IS = BITS == 4 ? (RG > 1 ? 12 / RG : 8) : NT == 2 ? 6 / RG : RG > 1 ? 8 / RG : D == 128 ? 4 : 8;
   static constexpr int W = IS * RG;             // consumer warps; a producer and a helper come on top
   static constexpr int THREADS = 32 * (W + 2);
   // What the compiler is told of the threads: 480 hold it to 136 registers, so that the join fits
   // beside the stream (kQcPerSm). fp32 takes the 144 that it may.
   static constexpr int BOUND = D == 64 && ROWS == 8 && !F32 ? 480 : THREADS;
-  static constexpr int STAGES = BITS == 4 ? (NT * RG == 1 ? 16 : 12) : D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 8 : 9;
+  static constexpr int STAGES = BITS == 4 ? (RG > 1 ? 12 : D == 64 ? 24 : 16) : D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 8 : 9;
   static constexpr int SL = 4;                  // slices of a block that a warp takes at once
   static constexpr int NQ = 2, ND = NT * RG == 1 && !(BITS == 4 && D == 128) ? 2 : 1;  // buffers for queries and for the warps' parts
   static constexpr int RP = D + 4;              // padded row of a part
@@ -1451,7 +1456,7 @@ cudaError_t stream_launches(const Shape& s, const QPlan& pl, const QStreamParams
     e = stream_variant<D, 1, 1, F32, BITS>(pl, p, stream);
   else if (pl.rows == 16)
     e = stream_variant<D, 1, 2, F32, BITS>(pl, p, stream);
-  else if constexpr (F32)
+  else if constexpr (F32 || BITS == 4)
     e = stream_variant<D, 1, 4, F32, BITS>(pl, p, stream);
   else
     e = stream_variant<D, 2, 2, F32, BITS>(pl, p, stream);
