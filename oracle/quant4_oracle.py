@@ -104,7 +104,7 @@ def _group(y, drop):
     """Codes, step, zero of groups y [g][m] (masked elements NaN)."""
     some = ~np.isnan(y).all(1)
     yy = np.where(some[:, None], y, 0.0)
-    zero = down16(np.fmin.reduce(yy, 1))
+    zero = down16(np.fmin.reduce(yy, 1) + 0.0)
     room = (np.fmax.reduce(yy, 1) - zero.astype(np.float64)).astype(f32) * (f32(1) / f32(15))
     step = up16(room.astype(np.float64), drop)
     inv = np.divide(f32(1), step.astype(f32), out=np.zeros(len(y), f32), where=step > 0)

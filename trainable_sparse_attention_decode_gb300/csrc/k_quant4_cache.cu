@@ -7,16 +7,23 @@
 namespace nosa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // reading back
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 struct UnitAppend4 {
   int n0, add;
 };
 // What the call does to unit u: tokens before it, new ones (0 where the unit is left as it was).
+template <bool EARLY>
 __device__ __forceinline__ UnitAppend4 unit_append(const QAppendArgs& p, int Hkv, int u, bool flag) {
   UnitAppend4 r;
-  r.n0 = quant_len(p.lens, u, p.max_blocks, p.status, flag);
-  r.add = quant_count(p.n_new, u / Hkv, p.n, p.status, flag);
+  r.n0 = quant_len<EARLY>(p.lens, u, p.max_blocks, p.status, flag);
+  r.add = quant_count<EARLY>(p.n_new, u / Hkv, p.n, p.status, flag);
   if (r.n0 < 0) {
     r.n0 = r.add = 0;
   } else if (r.n0 > kQB * p.max_blocks - r.add) {
@@ -26,145 +33,379 @@ __device__ __forceinline__ UnitAppend4 unit_append(const QAppendArgs& p, int Hkv
   return r;
 }
 
-// Element x of new token `tok` of (request b, head h), as the cache takes it: keys turned
-// and rounded to their type.
+// Chunk i of new token `tok`'s key of (request b, head h), turned and rounded, as two vectors.
 template <typename T>
-__device__ __forceinline__ T new_element(const Q4AppendArgs& p, bool key, int b, int h, int tok, int x) {
-  const QStrides& st = key ? p.a.ks : p.a.vs;
-  const T* row = static_cast<const T*>(key ? p.a.k : p.a.v) + b * st.b + (long long)tok * st.t + h * st.h;
-  if (!key || x >= 2 * p.rope.pairs) return row[x];
-  const RopePlace w = rope_place(p.rope, x);
-  return from_f32<T>(rope_turn(to_f32(row[x]), to_f32(row[w.other]), w.first, rope_angle(p.rope, (long long)b * p.a.n + tok, w.pair)));
+__device__ __forceinline__ void new_key(const Q4AppendArgs& p, int b, int h, int tok, int i, const RopeChunk& ch, Vec8<T>* v) {
+  const T* row = static_cast<const T*>(p.a.k) + b * p.a.ks.b + (long long)tok * p.a.ks.t + h * p.a.ks.h;
+  v[0].load(row + ch.lo);
+  v[1].load(row + ch.hi);
+  if (!ch.turned) return;
+  float2 cs[8];
+  rope_angles<false>(p.rope, (long long)b * p.a.n + tok, i, cs);
+  float x[16];
+  v[0].get(x);
+  v[1].get(x + 8);
+  rope_turn_chunk(p.rope.interleaved, cs, x);
+  v[0].set(x);
+  v[1].set(x + 8);
 }
 
-// Element x of row t of a tail unit.
+// Row t, dims x .. x + 7 of a tail unit: keys in 16-byte chunks, values in rows.
 template <typename T, int D>
-__device__ __forceinline__ size_t tail_at(bool key, int t, int x) {
-  constexpr int CE = 16 / (int)sizeof(T);
-  return key ? ((size_t)(x / CE) * kQB + t) * CE + x % CE : (size_t)kQB * D + (size_t)t * D + x;
+__device__ __forceinline__ void tail_load(const T* tail, bool key, int t, int x, Vec8<T>& v) {
+  if (!key) {
+    v.load(tail + kQB * D + t * D + x);
+  } else if constexpr (sizeof(T) == 2) {
+    v.load(tail + (x / 8 * kQB + t) * 8);
+  } else {
+    v.a = *reinterpret_cast<const float4*>(tail + (x / 4 * kQB + t) * 4);
+    v.b = *reinterpret_cast<const float4*>(tail + ((x / 4 + 1) * kQB + t) * 4);
+  }
+}
+template <typename T, int D>
+__device__ __forceinline__ void tail_store(T* tail, bool key, int t, int x, const Vec8<T>& v) {
+  if (!key) {
+    v.store(tail + kQB * D + t * D + x);
+  } else if constexpr (sizeof(T) == 2) {
+    v.store(tail + (x / 8 * kQB + t) * 8);
+  } else {
+    *reinterpret_cast<float4*>(tail + (x / 4 * kQB + t) * 4) = v.a;
+    *reinterpret_cast<float4*>(tail + ((x / 4 + 1) * kQB + t) * 4) = v.b;
+  }
 }
 
-// Blocks that the call completes: grid (units, most blocks).
+// x as bits: the nearest integer n in 0 .. 15 to x plus kMagicBits (the sum's last place is 1, so
+// the addition rounds).
+constexpr uint32_t kMagicBits = 0x4B400000u;
+__device__ __forceinline__ uint32_t code_bits(float y, float r) { return __float_as_uint(fmaf(y, r, 12582912.f)); }
+
+// A block of a unit's tokens on its way into 4 bits. CTAs of 2 D threads: thread (i, tp) has
+// chunk i of D / 16 and a pair of tokens, of the keys the two of a word (4 (tp / 2) + tp % 2 and
+// the second after it), of the values two of the four of a word (2 tp and 2 tp + 1). The block
+// stays in registers, in the tokens' type, from its loads to its codes:
+//   channels' extremes: over the thread's tokens, over the warp's by shuffles that halve the
+//     values each lane has, over the warps through shared memory;
+//   tokens' extremes: over four lanes;
+//   codes: (x / scale - zero) / step + 1.5 2^23, whose last bits are the code; a word is the sum
+//     of its codes' bits, shifted, less what the exponents add up to.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) quant4_blocks_kernel(Q4AppendArgs p, int Hkv, long long payload) {
-  __shared__ T x_s[kQB][D];
-  __shared__ float e_s[kQB], zero_s[D > 128 ? D : 128], step_s[128];
-  __shared__ unsigned amax_s;
-  const int u = blockIdx.x, j = blockIdx.y, b = u / Hkv, h = u % Hkv, tid = threadIdx.x;
-  const UnitAppend4 ap = unit_append(p.a, Hkv, u, false);
-  const int old = ap.n0 % kQB;
-  if (j >= (old + ap.add) / kQB) return;
-  const int to = p.a.tab[(long long)u * p.a.max_blocks + ap.n0 / kQB + j];
-  if (to < 0 || (long long)to >= p.a.n_units) {
-    if (tid == 0) quant_flag(p.a.status, kQErrIndex);
-    return;
+struct Quant4Block {
+  static constexpr int NT = 2 * D, WARPS = NT / 32, CH = D / 16, PITCH = 528;  // (bytes of 512, padded against bank conflicts)
+  static constexpr int REST = quant4_unit_bytes(D) - 64 * D;
+  struct Shared {
+    __align__(16) uint8_t code[2 * CH * PITCH];
+    __align__(16) uint8_t rest[REST];  // steps, zeros, logits, scales: as in the unit from byte 64 D on
+    __align__(16) float part[WARPS][2 * D];  // channels: - least, largest
+    __align__(16) float2 zr[D];              // channels: zero, 1 / step
+    uint32_t top[2][WARPS];                  // largest magnitudes of keys and values
+  };
+  const Q4AppendArgs& p;
+  const T* tail;
+  int Hkv, u, b, h, n0, old, tid;
+
+  __device__ __forceinline__ Quant4Block(const Q4AppendArgs& p_, int Hkv_, int u_, int n0_, const T* tail_)
+      : p(p_), tail(tail_), Hkv(Hkv_), u(u_), b(u_ / Hkv_), h(u_ % Hkv_), n0(n0_), old(n0_ % kQB), tid(threadIdx.x) {}
+
+  __device__ __forceinline__ float logit(int first, int t) const {
+    if (first + t < 0) return reinterpret_cast<const float*>(tail + 2 * kQB * D)[t];
+    return p.a.e != nullptr ? p.a.e[((long long)b * p.a.n + first + t) * Hkv + h] : 0.f;
   }
-  uint8_t* unit = p.a.units + (long long)to * quant4_unit_bytes(D);
-  const T* tail = reinterpret_cast<const T*>(p.a.tail + u * payload);
-  const int first = j * kQB - old;  // the block's first token among the new ones, or before them
-  if (tid < kQB) {
-    float e = 0.f;
-    if (first + tid < 0)
-      e = reinterpret_cast<const float*>(tail + 2 * kQB * D)[tid];
-    else if (p.a.e != nullptr)
-      e = p.a.e[((long long)b * p.a.n + first + tid) * Hkv + h];
-    e_s[tid] = e;
-    reinterpret_cast<float*>(unit + quant4_e_off(D))[tid] = e;
-  }
-  for (int part = 0; part < 2; ++part) {
-    const bool key = part == 0;
-    const int groups = key ? D : kQB * D / 64;  // channels, or runs of 64 dims of a token
-    if (tid == 0) amax_s = 0;
-    __syncthreads();
-    unsigned mx = 0;
-    for (int i = tid; i < kQB * D; i += kThreads) {
-      const int t = i / D, x = i % D;
-      const T y = first + t < 0 ? tail[tail_at<T, D>(key, t, x)] : new_element<T>(p, key, b, h, first + t, x);
-      x_s[t][x] = y;
-      if (e_s[t] != -INFINITY) mx = max(mx, __float_as_uint(to_f32(y)) & 0x7FFFFFFFu);
+
+  // Block j of the new blocks (0: the one that the tail began) into its unit (whole CTA).
+  __device__ __forceinline__ void run(int j, Shared& sh) const {
+    const int to = p.a.tab[(long long)u * p.a.max_blocks + n0 / kQB + j];
+    const int first = j * kQB - old;  // the block's first token among the new ones, or before them
+    const int i = tid % CH, tp = tid / CH, lane = tid & 31, warp = tid >> 5;
+    const RopeChunk ch = rope_chunk(p.rope, i);
+    const int kt = 4 * (tp / 2) + tp % 2, vt = 2 * tp;
+    Vec8<T> k[2][2], v[2][2];
+    bool klive[2], vlive[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int t = vt + r;
+      if (first + t >= 0) {
+        const T* row = static_cast<const T*>(p.a.v) + b * p.a.vs.b + (long long)(first + t) * p.a.vs.t + h * p.a.vs.h + 16 * i;
+        v[r][0].load(row);
+        v[r][1].load(row + 8);
+      } else {
+        tail_load<T, D>(tail, false, t, 16 * i, v[r][0]);
+        tail_load<T, D>(tail, false, t, 16 * i + 8, v[r][1]);
+      }
+      vlive[r] = logit(first, t) != -INFINITY;
+      klive[r] = logit(first, kt + 2 * r) != -INFINITY;
     }
-    atomicMax(&amax_s, mx);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int t = kt + 2 * r;
+      if (first + t >= 0) {
+        new_key<T>(p, b, h, first + t, i, ch, k[r]);
+      } else {
+        tail_load<T, D>(tail, true, t, ch.lo, k[r][0]);
+        tail_load<T, D>(tail, true, t, ch.hi, k[r][1]);
+      }
+    }
+    if (tid < kQB) reinterpret_cast<float*>(sh.rest + 7 * D)[tid] = logit(first, tid);
+    if (tid < 6) reinterpret_cast<uint32_t*>(sh.rest + 7 * D)[kQB + 2 + tid] = 0;
+    // A masked token counts as its neighbour, or not at all.
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float zero[8] = {};
+      if (!klive[r]) {
+        k[r][0] = k[1 - r][0];
+        k[r][1] = k[1 - r][1];
+      }
+      if (!vlive[r]) {
+        v[r][0].set(zero);
+        v[r][1].set(zero);
+      }
+    }
+    // ---- extremes ----
+    uint32_t topk = 0, topv = 0;
+    {
+      float red[32];  // - least and largest of the chunk's dims
+      {
+        float x[16], y[16];
+        k[0][0].get(x); k[0][1].get(x + 8);
+        k[1][0].get(y); k[1][1].get(y + 8);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          red[c] = max_nan(-x[c], -y[c]);
+          red[16 + c] = max_nan(x[c], y[c]);
+        }
+        if (!klive[0] && !klive[1]) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) red[c] = -INFINITY;
+        }
+      }
+      constexpr int STEPS = CH == 8 ? 2 : 3, LEFT = 32 >> STEPS;
+      int at = 0;  // of the 32 values
+#pragma unroll
+      for (int step = 0; step < STEPS; ++step) {  // lanes of the same chunk: each keeps half of the values
+        const int n = 16 >> step;                 // ... and the lane that has the other half is n away
+        const bool up = (lane & n) != 0;
+        at += up ? n : 0;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          if (c >= n) continue;
+          const float send = up ? red[c] : red[c + n], keep = up ? red[c + n] : red[c];
+          red[c] = max_nan(keep, __shfl_xor_sync(0xffffffffu, send, n));
+        }
+      }
+      const int c0 = at % 16, dim = c0 < 8 ? ch.lo + c0 : ch.hi + c0 - 8;
+      float4* to4 = reinterpret_cast<float4*>(sh.part[warp] + at / 16 * D + dim);
+#pragma unroll
+      for (int c = 0; c < LEFT; c += 4) to4[c / 4] = make_float4(red[c], red[c + 1], red[c + 2], red[c + 3]);
+#pragma unroll
+      for (int c = 0; c < LEFT; ++c) topk = max(topk, red[c] == -INFINITY ? 0u : __float_as_uint(red[c]) & 0x7FFFFFFFu);
+    }
+    float vlo[2], vhi[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float x[16];
+      v[r][0].get(x);
+      v[r][1].get(x + 8);
+      float lo = -x[0], hi = x[0];
+#pragma unroll
+      for (int c = 1; c < 16; ++c) {
+        lo = max_nan(lo, -x[c]);
+        hi = max_nan(hi, x[c]);
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o *= 2) {
+        lo = max_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      vlo[r] = -lo;
+      vhi[r] = hi;
+      topv = max(topv, max(__float_as_uint(lo) & 0x7FFFFFFFu, __float_as_uint(hi) & 0x7FFFFFFFu));
+    }
+    topk = __reduce_max_sync(0xffffffffu, topk);
+    topv = __reduce_max_sync(0xffffffffu, topv);
+    if (lane == 0) {
+      sh.top[0][warp] = topk;
+      sh.top[1][warp] = topv;
+    }
     __syncthreads();
-    const unsigned top = amax_s;
-    const bool bad = top >= 0x7F800000u, none = top < 0x0D800000u;  // not finite; below 2^-100
-    const float inv = none || bad ? 0.f : __uint_as_float((256u - (top >> 23)) << 23);
-    if (tid == 0)
-      reinterpret_cast<float*>(unit + quant4_e_off(D))[kQB + part] =
-          bad ? __uint_as_float(0x7FC00000u) : none ? 0.f : __uint_as_float(((top >> 23) - 2) << 23);
-    if (tid < groups) {
-      float lo = INFINITY, hi = -INFINITY;
-      for (int i = 0; i < 64; ++i) {
-        const int t = key ? i : tid % kQB, x = key ? tid : tid / kQB * 64 + i;
-        if (e_s[t] == -INFINITY) continue;
-        const float y = to_f32(x_s[t][x]) * inv;
-        lo = fminf(lo, y);
-        hi = fmaxf(hi, y);
+    // ---- scales, steps, zeros ----
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      topk = max(topk, sh.top[0][w]);
+      topv = max(topv, sh.top[1][w]);
+    }
+    const bool ok[2] = {topk >= 0x0D800000u && topk < 0x7F800000u, topv >= 0x0D800000u && topv < 0x7F800000u};  // finite, not below 2^-100
+    const float kinv = ok[0] ? __uint_as_float((256u - (topk >> 23)) << 23) : 0.f;
+    const float vinv = ok[1] ? __uint_as_float((256u - (topv >> 23)) << 23) : 0.f;
+    if (tid < 2) {
+      const uint32_t top = tid ? topv : topk;
+      reinterpret_cast<uint32_t*>(sh.rest + 7 * D)[kQB + tid] = top >= 0x7F800000u ? 0x7FC00000u : top >= 0x0D800000u ? ((top >> 23) - 2) << 23 : 0u;
+    }
+    if (tid < D) {
+      float lo = -INFINITY, hi = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        lo = max_nan(lo, sh.part[w][tid]);
+        hi = max_nan(hi, sh.part[w][D + tid]);
       }
       unsigned short z = 0, s = 0;
-      if (!bad && !none && lo <= hi) {
-        z = __half_as_ushort(__float2half_rd(lo));
-        s = __half_as_ushort(__float2half_ru(__fmul_rn(__fsub_rn(hi, half_bits(z)), 1.f / 15.f)));
-        if (key) s = (s + 0xFF) & 0xFF00;
+      if (ok[0]) {
+        z = __half_as_ushort(__float2half_rd(-lo * kinv + 0.f));  // (no -0)
+        s = __half_as_ushort(__float2half_ru(__fmul_rn(__fsub_rn(hi * kinv, half_bits(z)), 1.f / 15.f)));
+        s = (s + 0xFF) & 0xFF00;
       }
-      zero_s[tid] = half_bits(z);
-      step_s[tid] = half_bits(s);
-      if (key) {
-        unit[quant4_kstep_off(D) + quant4_order(tid, D)] = s >> 8;
-        reinterpret_cast<unsigned short*>(unit + quant4_kzero_off(D))[quant4_order(tid, D)] = z;
-      } else {
-        const int at = tid / kQB * kQB + quant4_order(tid % kQB, kQB);
-        reinterpret_cast<unsigned short*>(unit + quant4_vstep_off(D))[at] = s;
-        reinterpret_cast<unsigned short*>(unit + quant4_vzero_off(D))[at] = z;
+      const float st = half_bits(s);
+      sh.zr[tid] = make_float2(half_bits(z), st > 0.f ? __frcp_rn(st) : 0.f);
+      sh.rest[quant4_order(tid, D)] = s >> 8;
+      reinterpret_cast<unsigned short*>(sh.rest + D)[quant4_order(tid, D)] = z;
+    }
+    float vz[2], vr[2];
+    {
+      uint32_t zz = 0, ss = 0;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        unsigned short z = 0, s = 0;
+        if (ok[1] && vlive[r]) {
+          z = __half_as_ushort(__float2half_rd(vlo[r] * vinv + 0.f));
+          s = __half_as_ushort(__float2half_ru(__fmul_rn(__fsub_rn(vhi[r] * vinv, half_bits(z)), 1.f / 15.f)));
+        }
+        const float st = half_bits(s);
+        vz[r] = half_bits(z);
+        vr[r] = st > 0.f ? __frcp_rn(st) : 0.f;
+        zz |= (uint32_t)z << (16 * r);
+        ss |= (uint32_t)s << (16 * r);
+      }
+      if (i % 4 == 0) {
+        const int at = i / 4 * kQB + quant4_order(vt, kQB);  // (even: the two tokens are next to each other)
+        *reinterpret_cast<uint32_t*>(sh.rest + 3 * D + 2 * at) = ss;
+        *reinterpret_cast<uint32_t*>(sh.rest + 5 * D + 2 * at) = zz;
+      }
+    }
+    // ---- codes of the values ----
+    {
+      float x[2][16];
+      v[0][0].get(x[0]); v[0][1].get(x[0] + 8);
+      v[1][0].get(x[1]); v[1][1].get(x[1] + 8);
+      const int hh = tp & 1, c = tp / 2 % 4, w = tp / 8;
+      uint32_t word[8];
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {  // dims d and d + 8 of the two tokens
+        uint32_t n[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) n[r][e] = code_bits(fmaf(x[r][d + 8 * e], vinv, -vz[r]), vr[r]);
+        const uint32_t sum = (((n[1][1] << 4) + n[1][0]) << 16) + (n[0][1] << 4) + n[0][0] - kMagicBits * 0x00110011u;
+        word[d] = (ok[1] ? sum : 0u) << (8 * hh);
+      }
+      uint8_t* row = sh.code + (CH + i) * PITCH + 16 * c + 4 * w;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {  // the other two tokens of the words are CH lanes away; each thread puts four words down
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, hh ? word[d] : word[d + 4], CH);
+        *reinterpret_cast<uint32_t*>(row + 64 * (d + 4 * hh)) = (hh ? word[d + 4] : word[d]) | other;
       }
     }
     __syncthreads();
-    // a thread has words of eight codes: it looks for the codes that belong there
-    for (int i = tid; i < 8 * D; i += kThreads) {
-      const int m = i / 128, lane = i / 4 % 32, w = i % 4, g = lane / 4, c = lane % 4;
-      uint32_t word = 0;
-      for (int k = 0; k < 8; ++k) {
-        const int half = k % 2, i4 = k / 4 + k / 2 % 2 * 2;
-        const int t = 16 * w + (key ? 4 * (g / 2) + g % 2 + 2 * half : 4 * c + i4);
-        const int x = 16 * m + (key ? 4 * c + i4 : g + 8 * half);
-        const int grp = key ? x : x / 64 * kQB + t;
-        const float s = step_s[grp];
-        if (e_s[t] == -INFINITY || !(s > 0.f)) continue;
-        const float y = __fsub_rn(to_f32(x_s[t][x]) * inv, zero_s[grp]);
-        word |= (uint32_t)(int)(fmaf(y, __frcp_rn(s), 12582912.f) - 12582912.f) << (4 * k);
+    // ---- codes of the keys ----
+    {
+      const uint32_t mask = ok[0] ? (klive[0] ? 0x0F0F0F0Fu : 0u) | (klive[1] ? 0xF0F0F0F0u : 0u) : 0u;
+      const int g = tp % 8, w = tp / 8;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {  // the chunk's two vectors
+        const int dim = half ? ch.hi : ch.lo;
+        float x[2][8];
+        k[0][half].get(x[0]);
+        k[1][half].get(x[1]);
+        uint8_t* row = sh.code + dim / 16 * PITCH + 16 * (4 * g + dim % 16 / 4) + 4 * w;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t word = 0;
+          float2 zr[4];
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const float4 y = *reinterpret_cast<const float4*>(&sh.zr[dim + 4 * c + e]);
+            zr[e] = make_float2(y.x, y.y);
+            zr[e + 1] = make_float2(y.z, y.w);
+          }
+#pragma unroll
+          for (int n = 7; n >= 0; --n) {  // nibble n: token n % 2, dim 2 (n / 2 % 2) + n / 4
+            const int e = n / 2 % 2 * 2 + n / 4;
+            word = (word << 4) + code_bits(fmaf(x[n % 2][4 * c + e], kinv, -zr[e].x), zr[e].y);
+          }
+          *reinterpret_cast<uint32_t*>(row + 16 * c) = (word - kMagicBits * 0x11111111u) & mask;
+        }
       }
-      reinterpret_cast<uint32_t*>(unit + part * 32 * D)[i] = word;
     }
     __syncthreads();
+    if (to < 0 || (long long)to >= p.a.n_units) {
+      if (tid == 0) quant_flag(p.a.status, kQErrIndex);
+      return;
+    }
+    uint8_t* unit = p.a.units + (long long)to * quant4_unit_bytes(D);
+    for (int o = tid; o < 4 * D; o += NT)
+      reinterpret_cast<uint4*>(unit)[o] = *reinterpret_cast<const uint4*>(sh.code + o / 32 * PITCH + o % 32 * 16);
+    for (int o = tid; o < REST / 16; o += NT) reinterpret_cast<uint4*>(unit + 64 * D)[o] = reinterpret_cast<const uint4*>(sh.rest)[o];
   }
-  if (tid < 6) reinterpret_cast<uint32_t*>(unit + quant4_e_off(D))[kQB + 2 + tid] = 0;
+};
+
+// Blocks that the call completes: grid (units, most blocks), so that neighbouring CTAs read the
+// heads of the same tokens.
+template <typename T, int D>
+__global__ void __launch_bounds__(2 * D, (sizeof(T) == 2 ? 3 : 2) * 128 / D) quant4_blocks_kernel(Q4AppendArgs p, int Hkv, long long payload) {
+  __shared__ typename Quant4Block<T, D>::Shared sh;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int u = blockIdx.x, j = blockIdx.y;
+  const UnitAppend4 ap = unit_append<false>(p.a, Hkv, u, false);
+  if (j >= (ap.n0 % kQB + ap.add) / kQB) return;
+  Quant4Block<T, D>(p, Hkv, u, ap.n0, reinterpret_cast<const T*>(p.a.tail + u * payload)).run(j, sh);
 }
 
-// The units' tails and lengths.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) quant4_tail_kernel(Q4AppendArgs p, int Hkv, long long payload) {
+// The unit's tail and length; with BLOCK also the one block that at most 64 new tokens can
+// complete (single tokens: one launch).
+template <typename T, int D, bool BLOCK>
+__global__ void __launch_bounds__(2 * D) quant4_tail_kernel(Q4AppendArgs p, int Hkv, long long payload) {
   const int u = blockIdx.x, b = u / Hkv, h = u % Hkv, tid = threadIdx.x;
-  const UnitAppend4 ap = unit_append(p.a, Hkv, u, tid == 0);
-  __syncthreads();  // every thread has the length
-  const int old = ap.n0 % kQB, done = (old + ap.add) / kQB;
-  const int first = done > 0 ? 0 : old, left = old + ap.add - done * kQB;
+  if (BLOCK) griddep_wait();  // (the call's first launch)
+  griddep_launch_dependents();
+  const UnitAppend4 ap = unit_append<!BLOCK>(p.a, Hkv, u, tid == 0);
   T* tail = reinterpret_cast<T*>(p.a.tail + u * payload);
-  for (int i = tid; i < (left - first) * D; i += kThreads) {
-    const int r = first + i / D, x = i % D, tok = done * kQB + r - old;
-    tail[tail_at<T, D>(true, r, x)] = new_element<T>(p, true, b, h, tok, x);
-    tail[tail_at<T, D>(false, r, x)] = new_element<T>(p, false, b, h, tok, x);
+  const int old = ap.n0 % kQB, done = (old + ap.add) / kQB;
+  if constexpr (BLOCK) {
+    __shared__ typename Quant4Block<T, D>::Shared sh;
+    if (done > 0) Quant4Block<T, D>(p, Hkv, u, ap.n0, tail).run(0, sh);
+  }
+  if (!BLOCK) griddep_wait();  // the blocks' launch has read the old tail
+  __syncthreads();             // ... and so has this one, and the length
+  const int first = done > 0 ? 0 : old, left = old + ap.add - done * kQB;
+  constexpr int CH = D / 16;
+  for (int id = tid; id < (left - first) * CH * 2; id += 2 * D) {
+    const int i = id % CH, r = first + id / (2 * CH), tok = done * kQB + r - old;
+    Vec8<T> x[2];
+    if (id / CH % 2 == 0) {
+      const RopeChunk ch = rope_chunk(p.rope, i);
+      new_key<T>(p, b, h, tok, i, ch, x);
+      tail_store<T, D>(tail, true, r, ch.lo, x[0]);
+      tail_store<T, D>(tail, true, r, ch.hi, x[1]);
+    } else {
+      const T* row = static_cast<const T*>(p.a.v) + b * p.a.vs.b + (long long)tok * p.a.vs.t + h * p.a.vs.h + 16 * i;
+      x[0].load(row);
+      x[1].load(row + 8);
+      tail_store<T, D>(tail, false, r, 16 * i, x[0]);
+      tail_store<T, D>(tail, false, r, 16 * i + 8, x[1]);
+    }
   }
   float* te = reinterpret_cast<float*>(tail + 2 * kQB * D);
-  for (int r = first + tid; r < left; r += kThreads)
+  for (int r = first + tid; r < left; r += 2 * D)
     te[r] = p.a.e != nullptr ? p.a.e[((long long)b * p.a.n + (long long)done * kQB + r - old) * Hkv + h] : 0.f;
   if (tid == 0) p.a.lens_out[u] = p.a.lens[u] + ap.add;
 }
 
 template <typename T, int D>
 cudaError_t append_variant(const Shape& s, const Q4AppendArgs& a, cudaStream_t stream) {
+  if (a.a.n <= kQB) return launch_dependent(quant4_tail_kernel<T, D, true>, dim3(s.U), 2 * D, 0, stream, a, s.Hkv, s.payload);
   const int most = (int)std::min<long long>((a.a.n + kQB - 1LL) / kQB, a.a.max_blocks);
-  if (most > 0) quant4_blocks_kernel<T, D><<<dim3(s.U, most), kThreads, 0, stream>>>(a, s.Hkv, s.payload);
-  quant4_tail_kernel<T, D><<<s.U, kThreads, 0, stream>>>(a, s.Hkv, s.payload);
-  return cudaGetLastError();
+  const cudaError_t e = launch_dependent(quant4_blocks_kernel<T, D>, dim3(s.U, most), 2 * D, 0, stream, a, s.Hkv, s.payload);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(quant4_tail_kernel<T, D, false>, dim3(s.U), 2 * D, 0, stream, a, s.Hkv, s.payload);
 }
 
 // Blocks read back: a CTA per block. Masked tokens are zeros.
