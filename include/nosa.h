@@ -687,7 +687,7 @@ nosa_status nosa_quant4_append(const nosa_config* cfg, int32_t max_blocks, int32
  * each element (step * n + zero) * scale rounded to cfg's dtype, masked tokens zeros. Async.
  *   ids   : device int32 [n] or NULL (then n <= n_units); an id out of range is flagged and
  *           its block of the outputs left as it was. The same id may come more than once.
- *   k_out, v_out : device [n][64][head_dim] of cfg dtype, each may be NULL
+ *   k_out, v_out : device [n][64][head_dim] of cfg dtype, 32-byte aligned, each may be NULL
  *   e_out : device fp32 [n][64], the tokens' logits, or NULL
  */
 nosa_status nosa_quant4_read(const nosa_config* cfg, const void* units, int64_t n_units,

@@ -753,8 +753,8 @@ def nosa_quant4_read(cfg: NosaConfig, units, k_out=None, v_out=None, e_out=None,
         st = lib.nosa_quant4_read(
             C.byref(cfg), _buffer(units, dev, torch.uint8, "units", 16), count // size,
             None if ids is None else _arg(ids, dev, (n,), torch.int32, "ids"), n,
-            None if k_out is None else _arg(k_out, dev, (n, 64, d), dt, "k_out", 16),
-            None if v_out is None else _arg(v_out, dev, (n, 64, d), dt, "v_out", 16),
+            None if k_out is None else _arg(k_out, dev, (n, 64, d), dt, "k_out", 32),
+            None if v_out is None else _arg(v_out, dev, (n, 64, d), dt, "v_out", 32),
             None if e_out is None else _arg(e_out, dev, (n, 64), torch.float32, "e_out"),
             None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
             torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))

@@ -7,8 +7,6 @@
 namespace nosa {
 namespace {
 
-constexpr int kThreads = 256;  // reading back
-
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -408,36 +406,117 @@ cudaError_t append_variant(const Shape& s, const Q4AppendArgs& a, cudaStream_t s
   return launch_dependent(quant4_tail_kernel<T, D, false>, dim3(s.U), 2 * D, 0, stream, a, s.Hkv, s.payload);
 }
 
-// Blocks read back: a CTA per block. Masked tokens are zeros.
+// Code (bits `at` to `at` + 3 of a word) as fp32.
+__device__ __forceinline__ float code_f32(uint32_t word, int at) {
+  return __uint_as_float((word >> at & 15u) | 0x4B000000u) - 8388608.f;
+}
+// 32 bytes, a whole sector, at once.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Blocks read back: a CTA of D threads per block. A thread takes two of the keys' 16-byte
+// loads, 8 tokens of four dims, and of the values the words of four tokens and sixteen dims; lanes
+// are ordered so that a warp's stores are whole rows. Masked tokens are zeros.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) quant4_read_kernel(Q4ReadArgs p) {
+__global__ void __launch_bounds__(D) quant4_read_kernel(Q4ReadArgs p) {
+  constexpr int CH = D / 16;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31;
   for (long long n = blockIdx.x; n < p.n; n += gridDim.x) {
     const long long at = p.ids != nullptr ? p.ids[n] : n;
     if (at < 0 || at >= p.n_units) {
-      if (threadIdx.x == 0) quant_flag(p.status, kQErrIndex);
+      if (tid == 0) quant_flag(p.status, kQErrIndex);
       continue;
     }
     const uint8_t* unit = p.units + at * quant4_unit_bytes(D);
     const float* e = reinterpret_cast<const float*>(unit + quant4_e_off(D));
-    for (int i = threadIdx.x; i < kQB * D; i += kThreads) {
-      const int t = i / D, x = i % D, kb = quant4_k_bit(t, x), vb = quant4_v_bit(t, x);
-      const int ko = quant4_order(x, D), vo = x / 64 * kQB + quant4_order(t, kQB);
-      const int kc = unit[kb / 8] >> (kb % 8) & 15, vc = unit[32 * D + vb / 8] >> (vb % 8) & 15;
-      const float ks = half_bits(unit[quant4_kstep_off(D) + ko] << 8), kz = half_bits(reinterpret_cast<const unsigned short*>(unit + quant4_kzero_off(D))[ko]);
-      const float vs = half_bits(reinterpret_cast<const unsigned short*>(unit + quant4_vstep_off(D))[vo]);
-      const float vz = half_bits(reinterpret_cast<const unsigned short*>(unit + quant4_vzero_off(D))[vo]);
-      const bool live = e[t] != -INFINITY;
-      if (p.k != nullptr) static_cast<T*>(p.k)[n * kQB * D + i] = from_f32<T>(live ? fmaf(ks, (float)kc, kz) * e[kQB] : 0.f);
-      if (p.v != nullptr) static_cast<T*>(p.v)[n * kQB * D + i] = from_f32<T>(live ? fmaf(vs, (float)vc, vz) * e[kQB + 1] : 0.f);
+    const int vm = tid % CH, vc = tid / CH % 4, vw = tid / CH / 4;
+    uint4 kq[2];
+    uint32_t ksteps = 0, vq[8];
+    uint2 kzeros = make_uint2(0, 0), vsteps = kzeros, vzeros = kzeros;
+    const int km = tid % (D / 4) / 4, kc = tid % 4, kg = tid / (D / 4);
+    if (p.k != nullptr) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) kq[r] = reinterpret_cast<const uint4*>(unit)[km * 32 + 4 * (kg + 4 * r) + kc];
+      const int o = 4 * (kc * CH + km);
+      ksteps = *reinterpret_cast<const uint32_t*>(unit + quant4_kstep_off(D) + o);
+      kzeros = *reinterpret_cast<const uint2*>(unit + quant4_kzero_off(D) + 2 * o);
     }
-    if (p.e != nullptr && threadIdx.x < kQB) p.e[n * kQB + threadIdx.x] = e[threadIdx.x];
+    if (p.v != nullptr) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) vq[x] = reinterpret_cast<const uint32_t*>(unit + 32 * D)[4 * (vm * 32 + 4 * x + vc) + vw];
+      const int o = vm / 4 * kQB + 4 * (4 * vc + vw);
+      vsteps = *reinterpret_cast<const uint2*>(unit + quant4_vstep_off(D) + 2 * o);
+      vzeros = *reinterpret_cast<const uint2*>(unit + quant4_vzero_off(D) + 2 * o);
+    }
+    const float e0 = e[lane], e1 = e[lane + 32], ks = e[kQB], vs = e[kQB + 1];
+    const uint32_t live[2] = {__ballot_sync(0xffffffffu, e0 != -INFINITY), __ballot_sync(0xffffffffu, e1 != -INFINITY)};
+    auto is_live = [&](int t) { return (live[t / 32] >> (t % 32) & 1u) != 0; };
+    if (p.e != nullptr && tid < kQB) p.e[n * kQB + tid] = tid < 32 ? e0 : e1;
+    if (p.k != nullptr) {
+      float st[4], z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        st[i] = half_bits(ksteps >> (8 * i) << 8 & 0xFF00u);
+        z[i] = half_bits((i < 2 ? kzeros.x : kzeros.y) >> (16 * (i % 2)) & 0xFFFFu);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int g = kg + 4 * r;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t word = w == 0 ? kq[r].x : w == 1 ? kq[r].y : w == 2 ? kq[r].z : kq[r].w;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int t = 16 * w + 4 * (g / 2) + g % 2 + 2 * half;
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = is_live(t) ? fmaf(st[i], code_f32(word, 4 * (half + 2 * (i / 2) + 4 * (i % 2))), z[i]) * ks : 0.f;
+            T* to = static_cast<T*>(p.k) + (n * kQB + t) * D + 16 * km + 4 * kc;
+            if constexpr (sizeof(T) == 4)
+              *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+            else
+              *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]));
+          }
+        }
+      }
+    }
+    if (p.v != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * vw + 4 * vc + i;
+        const float st = half_bits((i < 2 ? vsteps.x : vsteps.y) >> (16 * (i % 2)) & 0xFFFFu);
+        const float z = half_bits((i < 2 ? vzeros.x : vzeros.y) >> (16 * (i % 2)) & 0xFFFFu);
+        float f[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) f[x] = is_live(t) ? fmaf(st, code_f32(vq[x % 8], 4 * (x / 8 + 2 * (i / 2) + 4 * (i % 2))), z) * vs : 0.f;
+        T* to = static_cast<T*>(p.v) + (n * kQB + t) * D + 16 * vm;
+        if constexpr (sizeof(T) == 4) {
+          store32(to, reinterpret_cast<const uint32_t*>(f));
+          store32(to + 8, reinterpret_cast<const uint32_t*>(f + 8));
+        } else {
+          uint32_t w[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[x] = bf16x2(f[2 * x], f[2 * x + 1]);
+          store32(to, w);
+        }
+      }
+    }
   }
 }
 
 template <typename T, int D>
 cudaError_t read_variant(const Q4ReadArgs& a, cudaStream_t stream) {
-  if (a.n > 0) quant4_read_kernel<T, D><<<(int)std::min<long long>(a.n, 1 << 20), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (a.n == 0) return cudaSuccess;
+  return launch_dependent(quant4_read_kernel<T, D>, dim3((unsigned)std::min<long long>(a.n, 1 << 20)), D, 0, stream, a);
 }
 
 }  // namespace

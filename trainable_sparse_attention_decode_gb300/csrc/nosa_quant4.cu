@@ -103,9 +103,9 @@ nosa_status nosa_quant4_read(const nosa_config* cfg, const void* units, int64_t 
   if (st != NOSA_OK) return st;
   if (n < 0 || n_units < 0 || (n_units > 0 && !units)) return invalid("NULL or negative argument");
   if (!ids && n > n_units) return invalid("n is more than the units");
-  if (!aligned_to(units, 16) || !aligned_to(k_out, 16) || !aligned_to(v_out, 16) || !aligned_to(ids, 4) || !aligned_to(e_out, 4) ||
+  if (!aligned_to(units, 16) || !aligned_to(k_out, 32) || !aligned_to(v_out, 32) || !aligned_to(ids, 4) || !aligned_to(e_out, 4) ||
       !aligned_to(status, 4))
-    return invalid("misaligned pointer (units, k_out, v_out 16 bytes)");
+    return invalid("misaligned pointer (units 16 bytes; k_out, v_out 32)");
   Q4ReadArgs a{};
   a.units = static_cast<const uint8_t*>(units);
   a.n_units = n_units;
