@@ -72,10 +72,45 @@ __device__ __forceinline__ void tail_store(T* tail, bool key, int t, int x, cons
   }
 }
 
-// x as bits: the nearest integer n in 0 .. 15 to x plus kMagicBits (the sum's last place is 1, so
-// the addition rounds).
+// Two numbers' nearest integers n in 0 .. 15 to (x - zero) * r, as kMagicBits + n: the last place
+// of 1.5 2^23 is 1, so adding it rounds.
 constexpr uint32_t kMagicBits = 0x4B400000u;
-__device__ __forceinline__ uint32_t code_bits(float y, float r) { return __float_as_uint(fmaf(y, r, 12582912.f)); }
+__device__ __forceinline__ uint2 code_bits(float2 x, float2 inv, float2 minus_zero, float2 r) {
+  const float2 t = __ffma2_rn(__ffma2_rn(x, inv, minus_zero), r, make_float2(12582912.f, 12582912.f));
+  return make_uint2(__float_as_uint(t.x), __float_as_uint(t.y));
+}
+
+// Extremes of a thread's elements, in a form that reductions by shuffles take: pairs of bf16
+// numbers, or single fp32 numbers. NaN stays NaN.
+template <typename T> struct Extreme;
+template <> struct Extreme<__nv_bfloat16> {
+  using V = uint32_t;
+  static constexpr int PER = 2;  // elements of a value
+  static __device__ __forceinline__ uint32_t none() { return 0xFF80FF80u; }
+  static __device__ __forceinline__ __nv_bfloat162 b(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
+  static __device__ __forceinline__ uint32_t u(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+  static __device__ __forceinline__ uint32_t most(uint32_t x, uint32_t y) { return u(__hmax2_nan(b(x), b(y))); }
+  static __device__ __forceinline__ uint32_t minus_least(uint32_t x, uint32_t y) { return u(__hmin2_nan(b(x), b(y))) ^ 0x80008000u; }
+  static __device__ __forceinline__ uint32_t minus(uint32_t x) { return x ^ 0x80008000u; }
+  static __device__ __forceinline__ void values(const Vec8<__nv_bfloat16>& v, uint32_t* x) { x[0] = v.r.x; x[1] = v.r.y; x[2] = v.r.z; x[3] = v.r.w; }
+  static __device__ __forceinline__ float whole(uint32_t x) { return max_nan(bf16_lo(x), bf16_hi(x)); }
+  // largest magnitude, as bits of an fp32 number; none() counts for nothing
+  static __device__ __forceinline__ uint32_t size(uint32_t x) {
+    const uint32_t lo = x << 16, hi = x & 0xFFFF0000u;
+    return max(lo == 0xFF800000u ? 0u : lo & 0x7FFFFFFFu, hi == 0xFF800000u ? 0u : hi & 0x7FFFFFFFu);
+  }
+};
+template <> struct Extreme<float> {
+  using V = float;
+  static constexpr int PER = 1;
+  static __device__ __forceinline__ float none() { return -INFINITY; }
+  static __device__ __forceinline__ float most(float x, float y) { return max_nan(x, y); }
+  static __device__ __forceinline__ float minus_least(float x, float y) { return max_nan(-x, -y); }
+  static __device__ __forceinline__ float minus(float x) { return -x; }
+  static __device__ __forceinline__ void values(const Vec8<float>& v, float* x) { v.get(x); }
+  static __device__ __forceinline__ float whole(float x) { return x; }
+  static __device__ __forceinline__ uint32_t size(float x) { return x == -INFINITY ? 0u : __float_as_uint(x) & 0x7FFFFFFFu; }
+};
 
 // A block of a unit's tokens on its way into 4 bits. CTAs of 2 D threads: thread (i, tp) has
 // chunk i of D / 16 and a pair of tokens, of the keys the two of a word (4 (tp / 2) + tp % 2 and
@@ -88,14 +123,15 @@ __device__ __forceinline__ uint32_t code_bits(float y, float r) { return __float
 //     of its codes' bits, shifted, less what the exponents add up to.
 template <typename T, int D>
 struct Quant4Block {
+  using X = Extreme<T>;
   static constexpr int NT = 2 * D, WARPS = NT / 32, CH = D / 16, PITCH = 528;  // (bytes of 512, padded against bank conflicts)
   static constexpr int REST = quant4_unit_bytes(D) - 64 * D;
   struct Shared {
     __align__(16) uint8_t code[2 * CH * PITCH];
     __align__(16) uint8_t rest[REST];  // steps, zeros, logits, scales: as in the unit from byte 64 D on
-    __align__(16) float part[WARPS][2 * D];  // channels: - least, largest
-    __align__(16) float2 zr[D];              // channels: zero, 1 / step
-    uint32_t top[2][WARPS];                  // largest magnitudes of keys and values
+    __align__(16) T part[WARPS][2 * D];                // channels: - least, largest
+    __align__(16) float minus_zero[D], inv_step[D];    // channels
+    uint32_t top[2][WARPS];                            // largest magnitudes of keys and values
   };
   const Q4AppendArgs& p;
   const T* tail;
@@ -108,6 +144,14 @@ struct Quant4Block {
     if (first + t < 0) return reinterpret_cast<const float*>(tail + 2 * kQB * D)[t];
     return p.a.e != nullptr ? p.a.e[((long long)b * p.a.n + first + t) * Hkv + h] : 0.f;
   }
+  // fp16 bits of a group's zero and step
+  template <bool KEY>
+  static __device__ __forceinline__ uint2 zero_step(float lo, float hi, float inv) {
+    const uint32_t z = __half_as_ushort(__float2half_rd(lo * inv + 0.f));  // (no -0)
+    const uint32_t s = __half_as_ushort(__float2half_ru(__fmul_rn(__fsub_rn(hi * inv, half_bits(z)), 1.f / 15.f)));
+    return make_uint2(z, KEY ? (s + 0xFFu) & 0xFF00u : s);
+  }
+  static __device__ __forceinline__ float inv_of(uint32_t step) { return step != 0 ? __frcp_rn(half_bits(step)) : 0.f; }
 
   // Block j of the new blocks (0: the one that the tail began) into its unit (whole CTA).
   __device__ __forceinline__ void run(int j, Shared& sh) const {
@@ -117,7 +161,6 @@ struct Quant4Block {
     const RopeChunk ch = rope_chunk(p.rope, i);
     const int kt = 4 * (tp / 2) + tp % 2, vt = 2 * tp;
     Vec8<T> k[2][2], v[2][2];
-    bool klive[2], vlive[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int t = vt + r;
@@ -129,9 +172,8 @@ struct Quant4Block {
         tail_load<T, D>(tail, false, t, 16 * i, v[r][0]);
         tail_load<T, D>(tail, false, t, 16 * i + 8, v[r][1]);
       }
-      vlive[r] = logit(first, t) != -INFINITY;
-      klive[r] = logit(first, kt + 2 * r) != -INFINITY;
     }
+    const float e0 = logit(first, lane), e1 = logit(first, lane + 32);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int t = kt + 2 * r;
@@ -142,12 +184,18 @@ struct Quant4Block {
         tail_load<T, D>(tail, true, t, ch.hi, k[r][1]);
       }
     }
-    if (tid < kQB) reinterpret_cast<float*>(sh.rest + 7 * D)[tid] = logit(first, tid);
-    if (tid < 6) reinterpret_cast<uint32_t*>(sh.rest + 7 * D)[kQB + 2 + tid] = 0;
+    if (warp == 0) {
+      reinterpret_cast<float*>(sh.rest + 7 * D)[lane] = e0;
+      reinterpret_cast<float*>(sh.rest + 7 * D)[lane + 32] = e1;
+      if (lane < 6) reinterpret_cast<uint32_t*>(sh.rest + 7 * D)[kQB + 2 + lane] = 0;
+    }
+    const uint32_t l0 = __ballot_sync(0xffffffffu, e0 != -INFINITY), l1 = __ballot_sync(0xffffffffu, e1 != -INFINITY);
+    const uint32_t kl = (kt < 32 ? l0 : l1) >> (kt % 32), vl = (vt < 32 ? l0 : l1) >> (vt % 32);
+    const bool klive[2] = {(kl & 1u) != 0, (kl & 4u) != 0}, vlive[2] = {(vl & 1u) != 0, (vl & 2u) != 0};
     // A masked token counts as its neighbour, or not at all.
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float zero[8] = {};
+      const float zero[8] = {};
       if (!klive[r]) {
         k[r][0] = k[1 - r][0];
         k[r][1] = k[1 - r][1];
@@ -160,62 +208,68 @@ struct Quant4Block {
     // ---- extremes ----
     uint32_t topk = 0, topv = 0;
     {
-      float red[32];  // - least and largest of the chunk's dims
-      {
-        float x[16], y[16];
-        k[0][0].get(x); k[0][1].get(x + 8);
-        k[1][0].get(y); k[1][1].get(y + 8);
+      constexpr int N = 32 / X::PER;  // values: of - least and of largest, one or two of the chunk's dims each
+      typename X::V red[N], x[N / 2], y[N / 2];
+      X::values(k[0][0], x); X::values(k[0][1], x + N / 4);
+      X::values(k[1][0], y); X::values(k[1][1], y + N / 4);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          red[c] = max_nan(-x[c], -y[c]);
-          red[16 + c] = max_nan(x[c], y[c]);
-        }
-        if (!klive[0] && !klive[1]) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) red[c] = -INFINITY;
-        }
+      for (int c = 0; c < N / 2; ++c) {
+        red[c] = X::minus_least(x[c], y[c]);
+        red[N / 2 + c] = X::most(x[c], y[c]);
       }
-      constexpr int STEPS = CH == 8 ? 2 : 3, LEFT = 32 >> STEPS;
-      int at = 0;  // of the 32 values
+      if (!klive[0] && !klive[1]) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) red[c] = X::none();
+      }
+      constexpr int STEPS = CH == 8 ? 2 : 3, LEFT = N >> STEPS;
+      int at = 0;  // of the values
 #pragma unroll
       for (int step = 0; step < STEPS; ++step) {  // lanes of the same chunk: each keeps half of the values
-        const int n = 16 >> step;                 // ... and the lane that has the other half is n away
-        const bool up = (lane & n) != 0;
+        const int n = N / 2 >> step, away = 16 >> step;
+        const bool up = (lane & away) != 0;
         at += up ? n : 0;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < N / 2; ++c) {
           if (c >= n) continue;
-          const float send = up ? red[c] : red[c + n], keep = up ? red[c + n] : red[c];
-          red[c] = max_nan(keep, __shfl_xor_sync(0xffffffffu, send, n));
+          const typename X::V send = up ? red[c] : red[c + n], keep = up ? red[c + n] : red[c];
+          red[c] = X::most(keep, __shfl_xor_sync(0xffffffffu, send, away));
         }
       }
-      const int c0 = at % 16, dim = c0 < 8 ? ch.lo + c0 : ch.hi + c0 - 8;
-      float4* to4 = reinterpret_cast<float4*>(sh.part[warp] + at / 16 * D + dim);
+      const int c0 = at % (N / 2) * X::PER, dim = c0 < 8 ? ch.lo + c0 : ch.hi + c0 - 8;
+      T* out = sh.part[warp] + at / (N / 2) * D + dim;
+      if constexpr (LEFT == 2) {
+        *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(red);
+      } else {
 #pragma unroll
-      for (int c = 0; c < LEFT; c += 4) to4[c / 4] = make_float4(red[c], red[c + 1], red[c + 2], red[c + 3]);
+        for (int c = 0; c < LEFT; c += 4) reinterpret_cast<uint4*>(out)[c / 4] = *reinterpret_cast<const uint4*>(red + c);
+      }
 #pragma unroll
-      for (int c = 0; c < LEFT; ++c) topk = max(topk, red[c] == -INFINITY ? 0u : __float_as_uint(red[c]) & 0x7FFFFFFFu);
+      for (int c = 0; c < LEFT; ++c) topk = max(topk, X::size(red[c]));
     }
-    float vlo[2], vhi[2];
+    float vlo = 0.f, vhi = 0.f;  // of the lane's one of the two tokens: even lanes the first, odd ones the second
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float x[16];
-      v[r][0].get(x);
-      v[r][1].get(x + 8);
-      float lo = -x[0], hi = x[0];
+      constexpr int N = 16 / X::PER;
+      typename X::V x[N];
+      X::values(v[r][0], x);
+      X::values(v[r][1], x + N / 2);
+      typename X::V lo = X::minus(x[0]), hi = x[0];
 #pragma unroll
-      for (int c = 1; c < 16; ++c) {
-        lo = max_nan(lo, -x[c]);
-        hi = max_nan(hi, x[c]);
+      for (int c = 1; c < N; ++c) {
+        lo = X::most(lo, X::minus(x[c]));
+        hi = X::most(hi, x[c]);
       }
 #pragma unroll
       for (int o = 1; o < 4; o *= 2) {
-        lo = max_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        lo = X::most(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = X::most(hi, __shfl_xor_sync(0xffffffffu, hi, o));
       }
-      vlo[r] = -lo;
-      vhi[r] = hi;
-      topv = max(topv, max(__float_as_uint(lo) & 0x7FFFFFFFu, __float_as_uint(hi) & 0x7FFFFFFFu));
+      const float l = X::whole(lo), g = X::whole(hi);
+      topv = max(topv, max(__float_as_uint(l) & 0x7FFFFFFFu, __float_as_uint(g) & 0x7FFFFFFFu));
+      if ((i & 1) == r) {
+        vlo = -l;
+        vhi = g;
+      }
     }
     topk = __reduce_max_sync(0xffffffffu, topk);
     topv = __reduce_max_sync(0xffffffffu, topv);
@@ -241,58 +295,42 @@ struct Quant4Block {
       float lo = -INFINITY, hi = -INFINITY;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
-        lo = max_nan(lo, sh.part[w][tid]);
-        hi = max_nan(hi, sh.part[w][D + tid]);
+        lo = fmaxf(lo, to_f32(sh.part[w][tid]));  // (where there is a NaN, ok is false)
+        hi = fmaxf(hi, to_f32(sh.part[w][D + tid]));
       }
-      unsigned short z = 0, s = 0;
-      if (ok[0]) {
-        z = __half_as_ushort(__float2half_rd(-lo * kinv + 0.f));  // (no -0)
-        s = __half_as_ushort(__float2half_ru(__fmul_rn(__fsub_rn(hi * kinv, half_bits(z)), 1.f / 15.f)));
-        s = (s + 0xFF) & 0xFF00;
-      }
-      const float st = half_bits(s);
-      sh.zr[tid] = make_float2(half_bits(z), st > 0.f ? __frcp_rn(st) : 0.f);
-      sh.rest[quant4_order(tid, D)] = s >> 8;
-      reinterpret_cast<unsigned short*>(sh.rest + D)[quant4_order(tid, D)] = z;
-    }
-    float vz[2], vr[2];
-    {
-      uint32_t zz = 0, ss = 0;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        unsigned short z = 0, s = 0;
-        if (ok[1] && vlive[r]) {
-          z = __half_as_ushort(__float2half_rd(vlo[r] * vinv + 0.f));
-          s = __half_as_ushort(__float2half_ru(__fmul_rn(__fsub_rn(vhi[r] * vinv, half_bits(z)), 1.f / 15.f)));
-        }
-        const float st = half_bits(s);
-        vz[r] = half_bits(z);
-        vr[r] = st > 0.f ? __frcp_rn(st) : 0.f;
-        zz |= (uint32_t)z << (16 * r);
-        ss |= (uint32_t)s << (16 * r);
-      }
-      if (i % 4 == 0) {
-        const int at = i / 4 * kQB + quant4_order(vt, kQB);  // (even: the two tokens are next to each other)
-        *reinterpret_cast<uint32_t*>(sh.rest + 3 * D + 2 * at) = ss;
-        *reinterpret_cast<uint32_t*>(sh.rest + 5 * D + 2 * at) = zz;
-      }
+      const uint2 zs = ok[0] ? zero_step<true>(-lo, hi, kinv) : make_uint2(0, 0);
+      sh.minus_zero[tid] = -half_bits(zs.x);
+      sh.inv_step[tid] = inv_of(zs.y);
+      sh.rest[quant4_order(tid, D)] = zs.y >> 8;
+      reinterpret_cast<unsigned short*>(sh.rest + D)[quant4_order(tid, D)] = zs.x;
     }
     // ---- codes of the values ----
     {
+      const uint2 zs = ok[1] && vlive[i & 1] ? zero_step<false>(vlo, vhi, vinv) : make_uint2(0, 0);
+      if (i % 4 < 2) {
+        const int at = i / 4 * kQB + quant4_order(vt, kQB) + i % 4;  // (vt is even: the second token is next to the first)
+        reinterpret_cast<unsigned short*>(sh.rest + 3 * D)[at] = zs.y;
+        reinterpret_cast<unsigned short*>(sh.rest + 5 * D)[at] = zs.x;
+      }
+      const float mz = -half_bits(zs.x), rs = inv_of(zs.y);
+      const float mz1 = __shfl_xor_sync(0xffffffffu, mz, 1), rs1 = __shfl_xor_sync(0xffffffffu, rs, 1);
+      const float z2[2] = {i & 1 ? mz1 : mz, i & 1 ? mz : mz1}, r2[2] = {i & 1 ? rs1 : rs, i & 1 ? rs : rs1};
       float x[2][16];
       v[0][0].get(x[0]); v[0][1].get(x[0] + 8);
       v[1][0].get(x[1]); v[1][1].get(x[1] + 8);
       const int hh = tp & 1, c = tp / 2 % 4, w = tp / 8;
+      const uint32_t mask = ok[1] ? 0xFFFFFFFFu : 0u;
       uint32_t word[8];
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {  // dims d and d + 8 of the two tokens
-        uint32_t n[2][2];
+      for (int d = 0; d < 8; d += 2) {  // dims d, d + 1 and the eighth ones after them, of the two tokens
+        uint2 n[2][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) n[r][e] = code_bits(fmaf(x[r][d + 8 * e], vinv, -vz[r]), vr[r]);
-        const uint32_t sum = (((n[1][1] << 4) + n[1][0]) << 16) + (n[0][1] << 4) + n[0][0] - kMagicBits * 0x00110011u;
-        word[d] = (ok[1] ? sum : 0u) << (8 * hh);
+          for (int e = 0; e < 2; ++e)
+            n[r][e] = code_bits(make_float2(x[r][d + 8 * e], x[r][d + 8 * e + 1]), make_float2(vinv, vinv), make_float2(z2[r], z2[r]), make_float2(r2[r], r2[r]));
+        word[d] = (((((n[1][1].x << 4) + n[1][0].x) << 16) + (n[0][1].x << 4) + n[0][0].x - kMagicBits * 0x00110011u) & mask) << (8 * hh);
+        word[d + 1] = (((((n[1][1].y << 4) + n[1][0].y) << 16) + (n[0][1].y << 4) + n[0][0].y - kMagicBits * 0x00110011u) & mask) << (8 * hh);
       }
       uint8_t* row = sh.code + (CH + i) * PITCH + 16 * c + 4 * w;
 #pragma unroll
@@ -306,6 +344,7 @@ struct Quant4Block {
     {
       const uint32_t mask = ok[0] ? (klive[0] ? 0x0F0F0F0Fu : 0u) | (klive[1] ? 0xF0F0F0F0u : 0u) : 0u;
       const int g = tp % 8, w = tp / 8;
+      const float2 inv = make_float2(kinv, kinv);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {  // the chunk's two vectors
         const int dim = half ? ch.hi : ch.lo;
@@ -314,21 +353,17 @@ struct Quant4Block {
         k[1][half].get(x[1]);
         uint8_t* row = sh.code + dim / 16 * PITCH + 16 * (4 * g + dim % 16 / 4) + 4 * w;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t word = 0;
-          float2 zr[4];
+        for (int c = 0; c < 8; c += 4) {
+          const float4 z = *reinterpret_cast<const float4*>(sh.minus_zero + dim + c), s = *reinterpret_cast<const float4*>(sh.inv_step + dim + c);
+          uint2 n[2][2];  // of token r, dims 2 y and 2 y + 1: nibbles r + 2 y and r + 2 y + 4
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float4 y = *reinterpret_cast<const float4*>(&sh.zr[dim + 4 * c + e]);
-            zr[e] = make_float2(y.x, y.y);
-            zr[e + 1] = make_float2(y.z, y.w);
+          for (int r = 0; r < 2; ++r) {
+            n[r][0] = code_bits(make_float2(x[r][c], x[r][c + 1]), inv, make_float2(z.x, z.y), make_float2(s.x, s.y));
+            n[r][1] = code_bits(make_float2(x[r][c + 2], x[r][c + 3]), inv, make_float2(z.z, z.w), make_float2(s.z, s.w));
           }
-#pragma unroll
-          for (int n = 7; n >= 0; --n) {  // nibble n: token n % 2, dim 2 (n / 2 % 2) + n / 4
-            const int e = n / 2 % 2 * 2 + n / 4;
-            word = (word << 4) + code_bits(fmaf(x[n % 2][4 * c + e], kinv, -zr[e].x), zr[e].y);
-          }
-          *reinterpret_cast<uint32_t*>(row + 16 * c) = (word - kMagicBits * 0x11111111u) & mask;
+          const uint32_t lo = (n[1][1].x << 12) + (n[0][1].x << 8) + (n[1][0].x << 4) + n[0][0].x;
+          const uint32_t hi = (n[1][1].y << 12) + (n[0][1].y << 8) + (n[1][0].y << 4) + n[0][0].y;
+          *reinterpret_cast<uint32_t*>(row + 4 * c) = ((hi << 16) + lo - kMagicBits * 0x11111111u) & mask;
         }
       }
     }
@@ -338,16 +373,18 @@ struct Quant4Block {
       return;
     }
     uint8_t* unit = p.a.units + (long long)to * quant4_unit_bytes(D);
+#pragma unroll
     for (int o = tid; o < 4 * D; o += NT)
       reinterpret_cast<uint4*>(unit)[o] = *reinterpret_cast<const uint4*>(sh.code + o / 32 * PITCH + o % 32 * 16);
-    for (int o = tid; o < REST / 16; o += NT) reinterpret_cast<uint4*>(unit + 64 * D)[o] = reinterpret_cast<const uint4*>(sh.rest)[o];
+    if (tid < REST / 16) reinterpret_cast<uint4*>(unit + 64 * D)[tid] = reinterpret_cast<const uint4*>(sh.rest)[tid];
+    static_assert(REST / 16 <= NT, "one store of a thread");
   }
 };
 
 // Blocks that the call completes: grid (units, most blocks), so that neighbouring CTAs read the
 // heads of the same tokens.
 template <typename T, int D>
-__global__ void __launch_bounds__(2 * D, (sizeof(T) == 2 ? 3 : 2) * 128 / D) quant4_blocks_kernel(Q4AppendArgs p, int Hkv, long long payload) {
+__global__ void __launch_bounds__(2 * D, (sizeof(T) == 2 ? 4 : 2) * 128 / D) quant4_blocks_kernel(Q4AppendArgs p, int Hkv, long long payload) {
   __shared__ typename Quant4Block<T, D>::Shared sh;
   griddep_wait();
   griddep_launch_dependents();
