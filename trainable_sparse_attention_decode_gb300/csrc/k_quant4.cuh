@@ -49,6 +49,7 @@ __host__ __device__ constexpr int quant4_order(int x, int n) { return 4 * (x % 1
 struct Q4AppendArgs {
   QAppendArgs a;
   RopeArgs rope;
+  int wide;  // v's rows start on 32-byte boundaries
 };
 struct Q4ReadArgs {
   const uint8_t* units;

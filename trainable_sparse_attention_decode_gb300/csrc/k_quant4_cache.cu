@@ -131,7 +131,7 @@ struct Quant4Block {
     __align__(16) uint8_t rest[REST];  // steps, zeros, logits, scales: as in the unit from byte 64 D on
     __align__(16) T part[WARPS][2 * D];                // channels: - least, largest
     __align__(16) float minus_zero[D], inv_step[D];    // channels
-    uint32_t top[2][WARPS];                            // largest magnitudes of keys and values
+    __align__(16) uint32_t top[2][WARPS];              // largest magnitudes of keys and values
   };
   const Q4AppendArgs& p;
   const T* tail;
@@ -166,8 +166,13 @@ struct Quant4Block {
       const int t = vt + r;
       if (first + t >= 0) {
         const T* row = static_cast<const T*>(p.a.v) + b * p.a.vs.b + (long long)(first + t) * p.a.vs.t + h * p.a.vs.h + 16 * i;
-        v[r][0].load(row);
-        v[r][1].load(row + 8);
+        if (p.wide) {  // sixteen elements in a row
+#pragma unroll
+          for (int y = 0; y < (int)sizeof(T) / 2; ++y) load32(row + y * 32 / sizeof(T), reinterpret_cast<uint32_t*>(v[r]) + 8 * y);
+        } else {
+          v[r][0].load(row);
+          v[r][1].load(row + 8);
+        }
       } else {
         tail_load<T, D>(tail, false, t, 16 * i, v[r][0]);
         tail_load<T, D>(tail, false, t, 16 * i + 8, v[r][1]);
@@ -280,9 +285,10 @@ struct Quant4Block {
     __syncthreads();
     // ---- scales, steps, zeros ----
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      topk = max(topk, sh.top[0][w]);
-      topv = max(topv, sh.top[1][w]);
+    for (int w = 0; w < WARPS; w += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(&sh.top[0][w]), y = *reinterpret_cast<const uint4*>(&sh.top[1][w]);
+      topk = max(max(topk, max(x.x, x.y)), max(x.z, x.w));
+      topv = max(max(topv, max(y.x, y.y)), max(y.z, y.w));
     }
     const bool ok[2] = {topk >= 0x0D800000u && topk < 0x7F800000u, topv >= 0x0D800000u && topv < 0x7F800000u};  // finite, not below 2^-100
     const float kinv = ok[0] ? __uint_as_float((256u - (topk >> 23)) << 23) : 0.f;

@@ -21,6 +21,7 @@ struct RopeArgs {
   long long axis_stride; // batch x n
   int len, pairs;        // positions of the table; pairs of a row (0: no rotation)
   int interleaved;       // pairs (2i, 2i + 1) instead of (i, i + pairs)
+  int wide;              // the table starts on a 32-byte boundary
   uint32_t axes[kRopeMaxAxes];  // axis of pair i: bits 2 (i % 16) of word i / 16
   int* status;
 };
@@ -81,6 +82,13 @@ __device__ __forceinline__ RopeChunk rope_chunk(const RopeArgs& p, int i) {
   return {split ? 8 * i : 16 * i, split ? p.pairs + 8 * i : 16 * i + 8, turned};
 }
 
+// 32 bytes, a whole sector, at once.
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+
 // Cosines and sines of pairs 8 i .. 8 i + 7 of token row `at`: four 16-byte loads where the
 // pairs have one axis.
 template <bool EARLY>
@@ -92,6 +100,11 @@ __device__ __forceinline__ void rope_angles(const RopeArgs& p, long long at, int
   w &= 0xFFFFu;
   if (w == (w & 3u) * 0x5555u) {
     const float4* src = reinterpret_cast<const float4*>(p.table + (long long)rope_position<EARLY>(p, at, 8 * i) * p.pairs + 8 * i);
+    if (p.wide && !EARLY) {  // half the passes through L1: a warp's lanes are 64 bytes apart
+#pragma unroll
+      for (int k = 0; k < 2; ++k) load32(src + 2 * k, reinterpret_cast<uint32_t*>(cs + 4 * k));
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float4 x = rope_load<EARLY>(src + k);

@@ -28,6 +28,7 @@ nosa_status take_rope(const nosa_config& cfg, const nosa_rope* rope, const int32
   out.axis_stride = (long long)cfg.batch * n;
   out.len = rope->table_len;
   out.interleaved = rope->interleaved != 0;
+  out.wide = aligned_to(rope->table, 32);
   out.status = status;
   return NOSA_OK;
 }
@@ -93,6 +94,8 @@ nosa_status nosa_quant4_append(const nosa_config* cfg, int32_t max_blocks, int32
                         lens_out, status, a.a)) != NOSA_OK)
     return st;
   if ((st = take_rope(*cfg, rope, positions, n_tokens, status, a.rope)) != NOSA_OK) return st;
+  const int sector = 32 / s.elt;
+  a.wide = aligned_to(v, 32) && a.a.vs.b % sector == 0 && a.a.vs.t % sector == 0 && a.a.vs.h % sector == 0;
   DeviceGuard guard(cfg->device);
   return launched(launch_quant4_append(s, a, static_cast<cudaStream_t>(stream)), "4-bit cache append");
 }
