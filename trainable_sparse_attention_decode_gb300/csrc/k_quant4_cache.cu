@@ -16,12 +16,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 struct UnitAppend4 {
   int n0, add;
 };
-// What the call does to unit u: tokens before it, new ones (0 where the unit is left as it was).
+// What the call does to unit u of request b: tokens before it, new ones (0 where the unit is left as it was).
 template <bool EARLY>
-__device__ __forceinline__ UnitAppend4 unit_append(const QAppendArgs& p, int Hkv, int u, bool flag) {
+__device__ __forceinline__ UnitAppend4 unit_append(const QAppendArgs& p, int b, int u, bool flag) {
   UnitAppend4 r;
   r.n0 = quant_len<EARLY>(p.lens, u, p.max_blocks, p.status, flag);
-  r.add = quant_count<EARLY>(p.n_new, u / Hkv, p.n, p.status, flag);
+  r.add = quant_count<EARLY>(p.n_new, b, p.n, p.status, flag);
   if (r.n0 < 0) {
     r.n0 = r.add = 0;
   } else if (r.n0 > kQB * p.max_blocks - r.add) {
@@ -31,19 +31,19 @@ __device__ __forceinline__ UnitAppend4 unit_append(const QAppendArgs& p, int Hkv
   return r;
 }
 
-// Chunk i of new token `tok`'s key of (request b, head h), turned and rounded, as two vectors.
+// Chunk i (axes w) of a new token's key, turned and rounded, as two vectors: the key's row and
+// where the token's positions are.
 template <typename T>
-__device__ __forceinline__ void new_key(const Q4AppendArgs& p, int b, int h, int tok, int i, const RopeChunk& ch, Vec8<T>* v) {
-  const T* row = static_cast<const T*>(p.a.k) + b * p.a.ks.b + (long long)tok * p.a.ks.t + h * p.a.ks.h;
+__device__ __forceinline__ void new_key(const RopeArgs& p, const T* row, const int32_t* pos, uint32_t w, int i, const RopeChunk& ch, Vec8<T>* v) {
   v[0].load(row + ch.lo);
   v[1].load(row + ch.hi);
   if (!ch.turned) return;
   float2 cs[8];
-  rope_angles<false>(p.rope, (long long)b * p.a.n + tok, i, cs);
+  rope_angles(p, w, pos, i, cs);
   float x[16];
   v[0].get(x);
   v[1].get(x + 8);
-  rope_turn_chunk(p.rope.interleaved, cs, x);
+  rope_turn_chunk(p.interleaved, cs, x);
   v[0].set(x);
   v[1].set(x + 8);
 }
@@ -99,6 +99,18 @@ template <> struct Extreme<__nv_bfloat16> {
     const uint32_t lo = x << 16, hi = x & 0xFFFF0000u;
     return max(lo == 0xFF800000u ? 0u : lo & 0x7FFFFFFFu, hi == 0xFF800000u ? 0u : hi & 0x7FFFFFFFu);
   }
+  template <int N> static __device__ __forceinline__ uint32_t sizes(const uint32_t* x) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int c = 0; c < N; ++c) m = __vmaxu2(m, x[c] & 0x7FFF7FFFu);
+    uint32_t top = max(m << 16, m & 0xFFFF0000u);
+    if (top >= 0x7F800000u) {  // (seldom: something that is not finite, or none())
+      top = 0;
+#pragma unroll
+      for (int c = 0; c < N; ++c) top = max(top, size(x[c]));
+    }
+    return top;
+  }
 };
 template <> struct Extreme<float> {
   using V = float;
@@ -109,13 +121,18 @@ template <> struct Extreme<float> {
   static __device__ __forceinline__ float minus(float x) { return -x; }
   static __device__ __forceinline__ void values(const Vec8<float>& v, float* x) { v.get(x); }
   static __device__ __forceinline__ float whole(float x) { return x; }
-  static __device__ __forceinline__ uint32_t size(float x) { return x == -INFINITY ? 0u : __float_as_uint(x) & 0x7FFFFFFFu; }
+  template <int N> static __device__ __forceinline__ uint32_t sizes(const float* x) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < N; ++c) top = max(top, x[c] == -INFINITY ? 0u : __float_as_uint(x[c]) & 0x7FFFFFFFu);
+    return top;
+  }
 };
 
-// A block of a unit's tokens on its way into 4 bits. CTAs of 2 D threads: thread (i, tp) has
-// chunk i of D / 16 and a pair of tokens, of the keys the two of a word (4 (tp / 2) + tp % 2 and
-// the second after it), of the values two of the four of a word (2 tp and 2 tp + 1). The block
-// stays in registers, in the tokens' type, from its loads to its codes:
+// A block of a unit's tokens on its way into 4 bits, its keys and its values apart. CTAs of 2 D
+// threads: thread (i, tp) has chunk i of D / 16 and a pair of tokens, of the keys the two of a word
+// (4 (tp / 2) + tp % 2 and the second after it), of the values two of the four of a word (2 tp and
+// 2 tp + 1). The block stays in registers, in the tokens' type, from its loads to its codes:
 //   channels' extremes: over the thread's tokens, over the warp's by shuffles that halve the
 //     values each lane has, over the warps through shared memory;
 //   tokens' extremes: over four lanes;
@@ -125,25 +142,43 @@ template <typename T, int D>
 struct Quant4Block {
   using X = Extreme<T>;
   static constexpr int NT = 2 * D, WARPS = NT / 32, CH = D / 16, PITCH = 528;  // (bytes of 512, padded against bank conflicts)
-  static constexpr int REST = quant4_unit_bytes(D) - 64 * D;
   struct Shared {
-    __align__(16) uint8_t code[2 * CH * PITCH];
-    __align__(16) uint8_t rest[REST];  // steps, zeros, logits, scales: as in the unit from byte 64 D on
-    __align__(16) T part[WARPS][2 * D];                // channels: - least, largest
-    __align__(16) float minus_zero[D], inv_step[D];    // channels
-    __align__(16) uint32_t top[2][WARPS];              // largest magnitudes of keys and values
+    __align__(16) uint8_t code[CH * PITCH];
+    __align__(16) uint8_t params[4 * D];             // steps and zeros as in the unit: 3 D bytes of the keys, 4 D of the values
+    __align__(16) T part[WARPS][2 * D];              // channels: - least, largest
+    __align__(16) float minus_zero[D], inv_step[D];  // channels
+    __align__(16) uint32_t top[WARPS];               // largest magnitudes
   };
   const Q4AppendArgs& p;
   const T* tail;
-  int Hkv, u, b, h, n0, old, tid;
+  int Hkv, u, b, h, n0, tid, lane, warp, i, tp, first;
+  uint32_t live0, live1;  // tokens that are not masked
+  float e0, e1;           // logits of tokens `lane` and lane + 32
 
-  __device__ __forceinline__ Quant4Block(const Q4AppendArgs& p_, int Hkv_, int u_, int n0_, const T* tail_)
-      : p(p_), tail(tail_), Hkv(Hkv_), u(u_), b(u_ / Hkv_), h(u_ % Hkv_), n0(n0_), old(n0_ % kQB), tid(threadIdx.x) {}
+  // Block j of the new blocks (0: the one that the tail began).
+  __device__ __forceinline__ Quant4Block(const Q4AppendArgs& p_, int Hkv_, int b_, int h_, int n0_, const T* tail_, int j)
+      : p(p_), tail(tail_), Hkv(Hkv_), u(b_ * Hkv_ + h_), b(b_), h(h_), n0(n0_), tid(threadIdx.x), lane(threadIdx.x & 31),
+        warp(threadIdx.x >> 5), i(threadIdx.x % CH), tp(threadIdx.x / CH), first(j * kQB - n0_ % kQB), e0(0.f), e1(0.f) {}
 
-  __device__ __forceinline__ float logit(int first, int t) const {
-    if (first + t < 0) return reinterpret_cast<const float*>(tail + 2 * kQB * D)[t];
-    return p.a.e != nullptr ? p.a.e[((long long)b * p.a.n + first + t) * Hkv + h] : 0.f;
+  // (first: the block's first token among the new ones, or before them)
+  __device__ __forceinline__ long long at0() const { return (long long)b * p.a.n + first; }
+  __device__ __forceinline__ void load_logits() {
+    const float* old_e = reinterpret_cast<const float*>(tail + 2 * kQB * D);
+    if (first + lane < 0)
+      e0 = old_e[lane];
+    else if (p.a.e != nullptr)
+      e0 = (p.a.e + at0() * Hkv + h)[lane * Hkv];
+    if (first + lane + 32 < 0)
+      e1 = old_e[lane + 32];
+    else if (p.a.e != nullptr)
+      e1 = (p.a.e + at0() * Hkv + h)[(lane + 32) * Hkv];
   }
+  __device__ __forceinline__ void find_live() {
+    live0 = __ballot_sync(0xffffffffu, e0 != -INFINITY);
+    live1 = __ballot_sync(0xffffffffu, e1 != -INFINITY);
+  }
+  __device__ __forceinline__ uint32_t live_from(int t) const { return (t < 32 ? live0 : live1) >> (t % 32); }
+
   // fp16 bits of a group's zero and step
   template <bool KEY>
   static __device__ __forceinline__ uint2 zero_step(float lo, float hi, float inv) {
@@ -153,65 +188,60 @@ struct Quant4Block {
   }
   static __device__ __forceinline__ float inv_of(uint32_t step) { return step != 0 ? __frcp_rn(half_bits(step)) : 0.f; }
 
-  // Block j of the new blocks (0: the one that the tail began) into its unit (whole CTA).
-  __device__ __forceinline__ void run(int j, Shared& sh) const {
-    const int to = p.a.tab[(long long)u * p.a.max_blocks + n0 / kQB + j];
-    const int first = j * kQB - old;  // the block's first token among the new ones, or before them
-    const int i = tid % CH, tp = tid / CH, lane = tid & 31, warp = tid >> 5;
-    const RopeChunk ch = rope_chunk(p.rope, i);
-    const int kt = 4 * (tp / 2) + tp % 2, vt = 2 * tp;
-    Vec8<T> k[2][2], v[2][2];
+  // The block's largest magnitude from the threads': whether it is finite and not below 2^-100
+  // (whole CTA).
+  __device__ __forceinline__ bool whole_top(Shared& sh, uint32_t& top) const {
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) sh.top[warp] = top;
+    __syncthreads();
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int t = vt + r;
-      if (first + t >= 0) {
-        const T* row = static_cast<const T*>(p.a.v) + b * p.a.vs.b + (long long)(first + t) * p.a.vs.t + h * p.a.vs.h + 16 * i;
-        if (p.wide) {  // sixteen elements in a row
-#pragma unroll
-          for (int y = 0; y < (int)sizeof(T) / 2; ++y) load32(row + y * 32 / sizeof(T), reinterpret_cast<uint32_t*>(v[r]) + 8 * y);
-        } else {
-          v[r][0].load(row);
-          v[r][1].load(row + 8);
-        }
-      } else {
-        tail_load<T, D>(tail, false, t, 16 * i, v[r][0]);
-        tail_load<T, D>(tail, false, t, 16 * i + 8, v[r][1]);
-      }
+    for (int w = 0; w < WARPS; w += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(&sh.top[w]);
+      top = max(max(top, max(x.x, x.y)), max(x.z, x.w));
     }
-    const float e0 = logit(first, lane), e1 = logit(first, lane + 32);
+    return top >= 0x0D800000u && top < 0x7F800000u;
+  }
+  static __device__ __forceinline__ float inv_scale(uint32_t top) { return __uint_as_float((256u - (top >> 23)) << 23); }
+  static __device__ __forceinline__ uint32_t scale_bits(uint32_t top) {
+    return top >= 0x7F800000u ? 0x7FC00000u : top >= 0x0D800000u ? ((top >> 23) - 2) << 23 : 0u;
+  }
+  // The unit that the table names; null and flagged where it names none.
+  __device__ __forceinline__ uint8_t* unit_of(int to) const {
+    if (to >= 0 && (long long)to < p.a.n_units) return p.a.units + (long long)to * quant4_unit_bytes(D);
+    if (tid == 0) quant_flag(p.a.status, kQErrIndex);
+    return nullptr;
+  }
+
+  __device__ __forceinline__ void keys(Shared& sh, int to) {
+    const RopeChunk ch = rope_chunk(p.rope, i);
+    const uint32_t axes = rope_axes(p.rope, i);
+    const int kt = 4 * (tp / 2) + tp % 2;
+    const T* k0 = static_cast<const T*>(p.a.k) + b * p.a.ks.b + h * p.a.ks.h + first * p.a.ks.t;
+    Vec8<T> k[2][2];
+    load_logits();
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int t = kt + 2 * r;
-      if (first + t >= 0) {
-        new_key<T>(p, b, h, first + t, i, ch, k[r]);
-      } else {
+      if (first + t < 0) {
         tail_load<T, D>(tail, true, t, ch.lo, k[r][0]);
         tail_load<T, D>(tail, true, t, ch.hi, k[r][1]);
+      } else {
+        new_key<T>(p.rope, k0 + t * p.a.ks.t, p.rope.pos + at0() + t, axes, i, ch, k[r]);
       }
     }
-    if (warp == 0) {
-      reinterpret_cast<float*>(sh.rest + 7 * D)[lane] = e0;
-      reinterpret_cast<float*>(sh.rest + 7 * D)[lane + 32] = e1;
-      if (lane < 6) reinterpret_cast<uint32_t*>(sh.rest + 7 * D)[kQB + 2 + lane] = 0;
-    }
-    const uint32_t l0 = __ballot_sync(0xffffffffu, e0 != -INFINITY), l1 = __ballot_sync(0xffffffffu, e1 != -INFINITY);
-    const uint32_t kl = (kt < 32 ? l0 : l1) >> (kt % 32), vl = (vt < 32 ? l0 : l1) >> (vt % 32);
-    const bool klive[2] = {(kl & 1u) != 0, (kl & 4u) != 0}, vlive[2] = {(vl & 1u) != 0, (vl & 2u) != 0};
-    // A masked token counts as its neighbour, or not at all.
+    find_live();
+    const uint32_t l = live_from(kt);
+    const bool live[2] = {(l & 1u) != 0, (l & 4u) != 0};
+    if (!(live[0] && live[1])) {  // a masked token counts as its neighbour
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float zero[8] = {};
-      if (!klive[r]) {
-        k[r][0] = k[1 - r][0];
-        k[r][1] = k[1 - r][1];
-      }
-      if (!vlive[r]) {
-        v[r][0].set(zero);
-        v[r][1].set(zero);
-      }
+      for (int r = 0; r < 2; ++r)
+        if (!live[r]) {
+          k[r][0] = k[1 - r][0];
+          k[r][1] = k[1 - r][1];
+        }
     }
     // ---- extremes ----
-    uint32_t topk = 0, topv = 0;
+    uint32_t top;
     {
       constexpr int N = 32 / X::PER;  // values: of - least and of largest, one or two of the chunk's dims each
       typename X::V red[N], x[N / 2], y[N / 2];
@@ -222,7 +252,7 @@ struct Quant4Block {
         red[c] = X::minus_least(x[c], y[c]);
         red[N / 2 + c] = X::most(x[c], y[c]);
       }
-      if (!klive[0] && !klive[1]) {
+      if (!live[0] && !live[1]) {
 #pragma unroll
         for (int c = 0; c < N; ++c) red[c] = X::none();
       }
@@ -248,10 +278,99 @@ struct Quant4Block {
 #pragma unroll
         for (int c = 0; c < LEFT; c += 4) reinterpret_cast<uint4*>(out)[c / 4] = *reinterpret_cast<const uint4*>(red + c);
       }
-#pragma unroll
-      for (int c = 0; c < LEFT; ++c) topk = max(topk, X::size(red[c]));
+      top = X::template sizes<LEFT>(red);
     }
-    float vlo = 0.f, vhi = 0.f;  // of the lane's one of the two tokens: even lanes the first, odd ones the second
+    const bool ok = whole_top(sh, top);
+    const float inv = ok ? inv_scale(top) : 0.f;
+    // ---- steps and zeros ----
+    if (tid < D) {
+      float lo = -INFINITY, hi = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        lo = fmaxf(lo, to_f32(sh.part[w][tid]));  // (where there is a NaN, ok is false)
+        hi = fmaxf(hi, to_f32(sh.part[w][D + tid]));
+      }
+      const uint2 zs = ok ? zero_step<true>(-lo, hi, inv) : make_uint2(0, 0);
+      sh.minus_zero[tid] = -half_bits(zs.x);
+      sh.inv_step[tid] = inv_of(zs.y);
+      sh.params[quant4_order(tid, D)] = zs.y >> 8;
+      reinterpret_cast<unsigned short*>(sh.params + D)[quant4_order(tid, D)] = zs.x;
+    }
+    __syncthreads();
+    // ---- codes ----
+    const uint32_t mask = ok ? (live[0] ? 0x0F0F0F0Fu : 0u) | (live[1] ? 0xF0F0F0F0u : 0u) : 0u;
+    const int g = tp % 8, w = tp / 8;
+    const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // the chunk's two vectors
+      const int dim = half ? ch.hi : ch.lo;
+      float x[2][8];
+      k[0][half].get(x[0]);
+      k[1][half].get(x[1]);
+      uint8_t* row = sh.code + dim / 16 * PITCH + 16 * (4 * g + dim % 16 / 4) + 4 * w;
+#pragma unroll
+      for (int c = 0; c < 8; c += 4) {
+        const float4 z = *reinterpret_cast<const float4*>(sh.minus_zero + dim + c), s = *reinterpret_cast<const float4*>(sh.inv_step + dim + c);
+        uint2 n[2][2];  // of token r, dims 2 y and 2 y + 1: nibbles r + 2 y and r + 2 y + 4
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          n[r][0] = code_bits(make_float2(x[r][c], x[r][c + 1]), inv2, make_float2(z.x, z.y), make_float2(s.x, s.y));
+          n[r][1] = code_bits(make_float2(x[r][c + 2], x[r][c + 3]), inv2, make_float2(z.z, z.w), make_float2(s.z, s.w));
+        }
+        const uint32_t lo = (n[1][1].x << 12) + (n[0][1].x << 8) + (n[1][0].x << 4) + n[0][0].x;
+        const uint32_t hi = (n[1][1].y << 12) + (n[0][1].y << 8) + (n[1][0].y << 4) + n[0][0].y;
+        *reinterpret_cast<uint32_t*>(row + 4 * c) = ((hi << 16) + lo - kMagicBits * 0x11111111u) & mask;
+      }
+    }
+    __syncthreads();
+    uint8_t* unit = unit_of(to);
+    if (unit == nullptr) return;
+    reinterpret_cast<uint4*>(unit)[tid] = *reinterpret_cast<const uint4*>(sh.code + tid / 32 * PITCH + tid % 32 * 16);
+    if (tid < 3 * D / 16) reinterpret_cast<uint4*>(unit + 64 * D)[tid] = reinterpret_cast<const uint4*>(sh.params)[tid];
+    if (warp == WARPS - 1) {
+      float* e = reinterpret_cast<float*>(unit + quant4_e_off(D));
+      e[lane] = e0;
+      e[lane + 32] = e1;
+      if (lane < 7) reinterpret_cast<uint32_t*>(e)[kQB + (lane == 0 ? 0 : lane + 1)] = lane == 0 ? scale_bits(top) : 0u;
+    }
+  }
+
+  __device__ __forceinline__ void values(Shared& sh, int to) {
+    const int vt = 2 * tp;
+    const T* v0 = static_cast<const T*>(p.a.v) + b * p.a.vs.b + h * p.a.vs.h + first * p.a.vs.t;
+    Vec8<T> v[2][2];
+    load_logits();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int t = vt + r;
+      if (first + t < 0) {
+        tail_load<T, D>(tail, false, t, 16 * i, v[r][0]);
+        tail_load<T, D>(tail, false, t, 16 * i + 8, v[r][1]);
+      } else {
+        const T* row = v0 + t * p.a.vs.t + 16 * i;
+        if (p.wide) {  // sixteen elements in a row
+#pragma unroll
+          for (int y = 0; y < (int)sizeof(T) / 2; ++y) load32(row + y * 32 / sizeof(T), reinterpret_cast<uint32_t*>(v[r]) + 8 * y);
+        } else {
+          v[r][0].load(row);
+          v[r][1].load(row + 8);
+        }
+      }
+    }
+    find_live();
+    const uint32_t l = live_from(vt);
+    const bool live[2] = {(l & 1u) != 0, (l & 2u) != 0};
+    if (!(live[0] && live[1])) {  // a masked token counts for nothing
+      const float zero[8] = {};
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        if (!live[r]) {
+          v[r][0].set(zero);
+          v[r][1].set(zero);
+        }
+    }
+    uint32_t top = 0;
+    float lo1 = 0.f, hi1 = 0.f;  // of the lane's one of the two tokens: even lanes the first, odd ones the second
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       constexpr int N = 16 / X::PER;
@@ -269,150 +388,93 @@ struct Quant4Block {
         lo = X::most(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = X::most(hi, __shfl_xor_sync(0xffffffffu, hi, o));
       }
-      const float l = X::whole(lo), g = X::whole(hi);
-      topv = max(topv, max(__float_as_uint(l) & 0x7FFFFFFFu, __float_as_uint(g) & 0x7FFFFFFFu));
+      const float a = X::whole(lo), g = X::whole(hi);
+      top = max(top, max(__float_as_uint(a) & 0x7FFFFFFFu, __float_as_uint(g) & 0x7FFFFFFFu));
       if ((i & 1) == r) {
-        vlo = -l;
-        vhi = g;
+        lo1 = -a;
+        hi1 = g;
       }
     }
-    topk = __reduce_max_sync(0xffffffffu, topk);
-    topv = __reduce_max_sync(0xffffffffu, topv);
-    if (lane == 0) {
-      sh.top[0][warp] = topk;
-      sh.top[1][warp] = topv;
+    const bool ok = whole_top(sh, top);
+    const float inv = ok ? inv_scale(top) : 0.f;
+    const uint2 zs = ok && live[i & 1] ? zero_step<false>(lo1, hi1, inv) : make_uint2(0, 0);
+    if (i % 4 < 2) {
+      const int at = i / 4 * kQB + quant4_order(vt, kQB) + i % 4;  // (vt is even: the second token is next to the first)
+      reinterpret_cast<unsigned short*>(sh.params)[at] = zs.y;
+      reinterpret_cast<unsigned short*>(sh.params + 2 * D)[at] = zs.x;
+    }
+    const float mz = -half_bits(zs.x), rs = inv_of(zs.y);
+    const float mz1 = __shfl_xor_sync(0xffffffffu, mz, 1), rs1 = __shfl_xor_sync(0xffffffffu, rs, 1);
+    const float z2[2] = {i & 1 ? mz1 : mz, i & 1 ? mz : mz1}, r2[2] = {i & 1 ? rs1 : rs, i & 1 ? rs : rs1};
+    float x[2][16];
+    v[0][0].get(x[0]); v[0][1].get(x[0] + 8);
+    v[1][0].get(x[1]); v[1][1].get(x[1] + 8);
+    const int hh = tp & 1, c = tp / 2 % 4, w = tp / 8;
+    const uint32_t mask = ok ? 0xFFFFFFFFu : 0u;
+    uint32_t word[8];
+#pragma unroll
+    for (int d = 0; d < 8; d += 2) {  // dims d, d + 1 and the eighth ones after them, of the two tokens
+      uint2 n[2][2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          n[r][e] = code_bits(make_float2(x[r][d + 8 * e], x[r][d + 8 * e + 1]), make_float2(inv, inv), make_float2(z2[r], z2[r]), make_float2(r2[r], r2[r]));
+      word[d] = (((((n[1][1].x << 4) + n[1][0].x) << 16) + (n[0][1].x << 4) + n[0][0].x - kMagicBits * 0x00110011u) & mask) << (8 * hh);
+      word[d + 1] = (((((n[1][1].y << 4) + n[1][0].y) << 16) + (n[0][1].y << 4) + n[0][0].y - kMagicBits * 0x00110011u) & mask) << (8 * hh);
+    }
+    uint8_t* row = sh.code + i * PITCH + 16 * c + 4 * w;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {  // the other two tokens of the words are CH lanes away; each thread puts four words down
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, hh ? word[d] : word[d + 4], CH);
+      *reinterpret_cast<uint32_t*>(row + 64 * (d + 4 * hh)) = (hh ? word[d + 4] : word[d]) | other;
     }
     __syncthreads();
-    // ---- scales, steps, zeros ----
-#pragma unroll
-    for (int w = 0; w < WARPS; w += 4) {
-      const uint4 x = *reinterpret_cast<const uint4*>(&sh.top[0][w]), y = *reinterpret_cast<const uint4*>(&sh.top[1][w]);
-      topk = max(max(topk, max(x.x, x.y)), max(x.z, x.w));
-      topv = max(max(topv, max(y.x, y.y)), max(y.z, y.w));
-    }
-    const bool ok[2] = {topk >= 0x0D800000u && topk < 0x7F800000u, topv >= 0x0D800000u && topv < 0x7F800000u};  // finite, not below 2^-100
-    const float kinv = ok[0] ? __uint_as_float((256u - (topk >> 23)) << 23) : 0.f;
-    const float vinv = ok[1] ? __uint_as_float((256u - (topv >> 23)) << 23) : 0.f;
-    if (tid < 2) {
-      const uint32_t top = tid ? topv : topk;
-      reinterpret_cast<uint32_t*>(sh.rest + 7 * D)[kQB + tid] = top >= 0x7F800000u ? 0x7FC00000u : top >= 0x0D800000u ? ((top >> 23) - 2) << 23 : 0u;
-    }
-    if (tid < D) {
-      float lo = -INFINITY, hi = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        lo = fmaxf(lo, to_f32(sh.part[w][tid]));  // (where there is a NaN, ok is false)
-        hi = fmaxf(hi, to_f32(sh.part[w][D + tid]));
-      }
-      const uint2 zs = ok[0] ? zero_step<true>(-lo, hi, kinv) : make_uint2(0, 0);
-      sh.minus_zero[tid] = -half_bits(zs.x);
-      sh.inv_step[tid] = inv_of(zs.y);
-      sh.rest[quant4_order(tid, D)] = zs.y >> 8;
-      reinterpret_cast<unsigned short*>(sh.rest + D)[quant4_order(tid, D)] = zs.x;
-    }
-    // ---- codes of the values ----
-    {
-      const uint2 zs = ok[1] && vlive[i & 1] ? zero_step<false>(vlo, vhi, vinv) : make_uint2(0, 0);
-      if (i % 4 < 2) {
-        const int at = i / 4 * kQB + quant4_order(vt, kQB) + i % 4;  // (vt is even: the second token is next to the first)
-        reinterpret_cast<unsigned short*>(sh.rest + 3 * D)[at] = zs.y;
-        reinterpret_cast<unsigned short*>(sh.rest + 5 * D)[at] = zs.x;
-      }
-      const float mz = -half_bits(zs.x), rs = inv_of(zs.y);
-      const float mz1 = __shfl_xor_sync(0xffffffffu, mz, 1), rs1 = __shfl_xor_sync(0xffffffffu, rs, 1);
-      const float z2[2] = {i & 1 ? mz1 : mz, i & 1 ? mz : mz1}, r2[2] = {i & 1 ? rs1 : rs, i & 1 ? rs : rs1};
-      float x[2][16];
-      v[0][0].get(x[0]); v[0][1].get(x[0] + 8);
-      v[1][0].get(x[1]); v[1][1].get(x[1] + 8);
-      const int hh = tp & 1, c = tp / 2 % 4, w = tp / 8;
-      const uint32_t mask = ok[1] ? 0xFFFFFFFFu : 0u;
-      uint32_t word[8];
-#pragma unroll
-      for (int d = 0; d < 8; d += 2) {  // dims d, d + 1 and the eighth ones after them, of the two tokens
-        uint2 n[2][2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            n[r][e] = code_bits(make_float2(x[r][d + 8 * e], x[r][d + 8 * e + 1]), make_float2(vinv, vinv), make_float2(z2[r], z2[r]), make_float2(r2[r], r2[r]));
-        word[d] = (((((n[1][1].x << 4) + n[1][0].x) << 16) + (n[0][1].x << 4) + n[0][0].x - kMagicBits * 0x00110011u) & mask) << (8 * hh);
-        word[d + 1] = (((((n[1][1].y << 4) + n[1][0].y) << 16) + (n[0][1].y << 4) + n[0][0].y - kMagicBits * 0x00110011u) & mask) << (8 * hh);
-      }
-      uint8_t* row = sh.code + (CH + i) * PITCH + 16 * c + 4 * w;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {  // the other two tokens of the words are CH lanes away; each thread puts four words down
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, hh ? word[d] : word[d + 4], CH);
-        *reinterpret_cast<uint32_t*>(row + 64 * (d + 4 * hh)) = (hh ? word[d + 4] : word[d]) | other;
-      }
-    }
-    __syncthreads();
-    // ---- codes of the keys ----
-    {
-      const uint32_t mask = ok[0] ? (klive[0] ? 0x0F0F0F0Fu : 0u) | (klive[1] ? 0xF0F0F0F0u : 0u) : 0u;
-      const int g = tp % 8, w = tp / 8;
-      const float2 inv = make_float2(kinv, kinv);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {  // the chunk's two vectors
-        const int dim = half ? ch.hi : ch.lo;
-        float x[2][8];
-        k[0][half].get(x[0]);
-        k[1][half].get(x[1]);
-        uint8_t* row = sh.code + dim / 16 * PITCH + 16 * (4 * g + dim % 16 / 4) + 4 * w;
-#pragma unroll
-        for (int c = 0; c < 8; c += 4) {
-          const float4 z = *reinterpret_cast<const float4*>(sh.minus_zero + dim + c), s = *reinterpret_cast<const float4*>(sh.inv_step + dim + c);
-          uint2 n[2][2];  // of token r, dims 2 y and 2 y + 1: nibbles r + 2 y and r + 2 y + 4
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            n[r][0] = code_bits(make_float2(x[r][c], x[r][c + 1]), inv, make_float2(z.x, z.y), make_float2(s.x, s.y));
-            n[r][1] = code_bits(make_float2(x[r][c + 2], x[r][c + 3]), inv, make_float2(z.z, z.w), make_float2(s.z, s.w));
-          }
-          const uint32_t lo = (n[1][1].x << 12) + (n[0][1].x << 8) + (n[1][0].x << 4) + n[0][0].x;
-          const uint32_t hi = (n[1][1].y << 12) + (n[0][1].y << 8) + (n[1][0].y << 4) + n[0][0].y;
-          *reinterpret_cast<uint32_t*>(row + 4 * c) = ((hi << 16) + lo - kMagicBits * 0x11111111u) & mask;
-        }
-      }
-    }
-    __syncthreads();
-    if (to < 0 || (long long)to >= p.a.n_units) {
-      if (tid == 0) quant_flag(p.a.status, kQErrIndex);
-      return;
-    }
-    uint8_t* unit = p.a.units + (long long)to * quant4_unit_bytes(D);
-#pragma unroll
-    for (int o = tid; o < 4 * D; o += NT)
-      reinterpret_cast<uint4*>(unit)[o] = *reinterpret_cast<const uint4*>(sh.code + o / 32 * PITCH + o % 32 * 16);
-    if (tid < REST / 16) reinterpret_cast<uint4*>(unit + 64 * D)[tid] = reinterpret_cast<const uint4*>(sh.rest)[tid];
-    static_assert(REST / 16 <= NT, "one store of a thread");
+    uint8_t* unit = unit_of(to);
+    if (unit == nullptr) return;
+    reinterpret_cast<uint4*>(unit + 32 * D)[tid] = *reinterpret_cast<const uint4*>(sh.code + tid / 32 * PITCH + tid % 32 * 16);
+    if (tid < 4 * D / 16) reinterpret_cast<uint4*>(unit + quant4_vstep_off(D))[tid] = reinterpret_cast<const uint4*>(sh.params)[tid];
+    if (tid == NT - 1) reinterpret_cast<uint32_t*>(unit + quant4_e_off(D))[kQB + 1] = scale_bits(top);
   }
 };
 
-// Blocks that the call completes: grid (units, most blocks), so that neighbouring CTAs read the
-// heads of the same tokens.
+// Blocks that the call completes: grid (KV heads x keys and values, most blocks, requests), so that
+// neighbouring CTAs read the heads of the same tokens.
 template <typename T, int D>
-__global__ void __launch_bounds__(2 * D, (sizeof(T) == 2 ? 4 : 2) * 128 / D) quant4_blocks_kernel(Q4AppendArgs p, int Hkv, long long payload) {
+__global__ void __launch_bounds__(2 * D, (sizeof(T) == 2 ? 5 : 3) * 128 / D) quant4_blocks_kernel(Q4AppendArgs p, long long payload) {
   __shared__ typename Quant4Block<T, D>::Shared sh;
   griddep_wait();
   griddep_launch_dependents();
-  const int u = blockIdx.x, j = blockIdx.y;
-  const UnitAppend4 ap = unit_append<false>(p.a, Hkv, u, false);
+  const int h = blockIdx.x / 2, Hkv = gridDim.x / 2, j = blockIdx.y, b = blockIdx.z, u = b * Hkv + h;
+  const UnitAppend4 ap = unit_append<false>(p.a, b, u, false);
   if (j >= (ap.n0 % kQB + ap.add) / kQB) return;
-  Quant4Block<T, D>(p, Hkv, u, ap.n0, reinterpret_cast<const T*>(p.a.tail + u * payload)).run(j, sh);
+  const int to = p.a.tab[(long long)u * p.a.max_blocks + ap.n0 / kQB + j];
+  Quant4Block<T, D> q(p, Hkv, b, h, ap.n0, reinterpret_cast<const T*>(p.a.tail + u * payload), j);
+  if (blockIdx.x % 2 == 0)
+    q.keys(sh, to);
+  else
+    q.values(sh, to);
 }
 
 // The unit's tail and length; with BLOCK also the one block that at most 64 new tokens can
 // complete (single tokens: one launch).
 template <typename T, int D, bool BLOCK>
-__global__ void __launch_bounds__(2 * D) quant4_tail_kernel(Q4AppendArgs p, int Hkv, long long payload) {
-  const int u = blockIdx.x, b = u / Hkv, h = u % Hkv, tid = threadIdx.x;
+__global__ void __launch_bounds__(2 * D) quant4_tail_kernel(Q4AppendArgs p, long long payload) {
+  const int h = blockIdx.x, Hkv = gridDim.x, b = blockIdx.z, u = b * Hkv + h, tid = threadIdx.x;
   if (BLOCK) griddep_wait();  // (the call's first launch)
   griddep_launch_dependents();
-  const UnitAppend4 ap = unit_append<!BLOCK>(p.a, Hkv, u, tid == 0);
+  const UnitAppend4 ap = unit_append<!BLOCK>(p.a, b, u, tid == 0);
   T* tail = reinterpret_cast<T*>(p.a.tail + u * payload);
   const int old = ap.n0 % kQB, done = (old + ap.add) / kQB;
   if constexpr (BLOCK) {
     __shared__ typename Quant4Block<T, D>::Shared sh;
-    if (done > 0) Quant4Block<T, D>(p, Hkv, u, ap.n0, tail).run(0, sh);
+    if (done > 0) {
+      const int to = p.a.tab[(long long)u * p.a.max_blocks + ap.n0 / kQB];
+      Quant4Block<T, D> q(p, Hkv, b, h, ap.n0, tail, 0);
+      q.keys(sh, to);
+      __syncthreads();
+      q.values(sh, to);
+    }
   }
   if (!BLOCK) griddep_wait();  // the blocks' launch has read the old tail
   __syncthreads();             // ... and so has this one, and the length
@@ -423,7 +485,8 @@ __global__ void __launch_bounds__(2 * D) quant4_tail_kernel(Q4AppendArgs p, int 
     Vec8<T> x[2];
     if (id / CH % 2 == 0) {
       const RopeChunk ch = rope_chunk(p.rope, i);
-      new_key<T>(p, b, h, tok, i, ch, x);
+      new_key<T>(p.rope, static_cast<const T*>(p.a.k) + b * p.a.ks.b + (long long)tok * p.a.ks.t + h * p.a.ks.h,
+                 p.rope.pos + (long long)b * p.a.n + tok, rope_axes(p.rope, i), i, ch, x);
       tail_store<T, D>(tail, true, r, ch.lo, x[0]);
       tail_store<T, D>(tail, true, r, ch.hi, x[1]);
     } else {
@@ -442,11 +505,11 @@ __global__ void __launch_bounds__(2 * D) quant4_tail_kernel(Q4AppendArgs p, int 
 
 template <typename T, int D>
 cudaError_t append_variant(const Shape& s, const Q4AppendArgs& a, cudaStream_t stream) {
-  if (a.a.n <= kQB) return launch_dependent(quant4_tail_kernel<T, D, true>, dim3(s.U), 2 * D, 0, stream, a, s.Hkv, s.payload);
+  if (a.a.n <= kQB) return launch_dependent(quant4_tail_kernel<T, D, true>, dim3(s.Hkv, 1, s.batch), 2 * D, 0, stream, a, s.payload);
   const int most = (int)std::min<long long>((a.a.n + kQB - 1LL) / kQB, a.a.max_blocks);
-  const cudaError_t e = launch_dependent(quant4_blocks_kernel<T, D>, dim3(s.U, most), 2 * D, 0, stream, a, s.Hkv, s.payload);
+  const cudaError_t e = launch_dependent(quant4_blocks_kernel<T, D>, dim3(2 * s.Hkv, most, s.batch), 2 * D, 0, stream, a, s.payload);
   if (e != cudaSuccess) return e;
-  return launch_dependent(quant4_tail_kernel<T, D, false>, dim3(s.U), 2 * D, 0, stream, a, s.Hkv, s.payload);
+  return launch_dependent(quant4_tail_kernel<T, D, false>, dim3(s.Hkv, 1, s.batch), 2 * D, 0, stream, a, s.payload);
 }
 
 // Code (bits `at` to `at` + 3 of a word) as fp32.

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(HPT == 1 ? kRotateFew : kRotateMany, HPT == 1 
     }
     float2 cs[8];
     if (ch.turned) {
-      rope_angles<false>(p.rope, at, i, cs);
+      rope_angles(p.rope, rope_axes(p.rope, i), p.rope.pos + at, i, cs);
       if (p.backward) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) cs[k].y = -cs[k].y;

@@ -28,43 +28,6 @@ struct RopeArgs {
 
 #ifdef __CUDACC__
 
-__device__ __forceinline__ uint32_t rope_axis(const RopeArgs& p, int i) {
-  uint32_t w = p.axes[0];
-#pragma unroll
-  for (int k = 1; k < kRopeMaxAxes; ++k)
-    if (i / 16 == k) w = p.axes[k];
-  return (w >> (2 * (i % 16))) & 3u;
-}
-
-// EARLY: past L1, for kernels that read before their own griddep_wait (see launch_dependent).
-template <bool EARLY, typename T> __device__ __forceinline__ T rope_load(const T* p) { return EARLY ? __ldcg(p) : *p; }
-
-// Position of token row `at` on the axis of pair i; one that the table does not have is
-// flagged and clamped.
-template <bool EARLY = false>
-__device__ __forceinline__ int rope_position(const RopeArgs& p, long long at, int i) {
-  const int x = rope_load<EARLY>(p.pos + (long long)rope_axis(p, i) * p.axis_stride + at);
-  if (x >= 0 && x < p.len) return x;
-  if (p.status != nullptr) atomicOr(p.status, 2);  // NOSA_QUANT_INDEX
-  return x < 0 ? 0 : p.len - 1;
-}
-
-// Cosine and sine of pair i of token row `at`.
-__device__ __forceinline__ float2 rope_angle(const RopeArgs& p, long long at, int i) {
-  return p.table[(long long)rope_position(p, at, i) * p.pairs + i];
-}
-
-// Element x (< 2 pairs) of a row: which pair it belongs to, whether it is the pair's
-// first, and where the other one is.
-struct RopePlace {
-  int pair, other;
-  bool first;
-};
-__device__ __forceinline__ RopePlace rope_place(const RopeArgs& p, int x) {
-  if (p.interleaved) return {x >> 1, x ^ 1, (x & 1) == 0};
-  const bool first = x < p.pairs;
-  return {first ? x : x - p.pairs, first ? x + p.pairs : x - p.pairs, first};
-}
 __device__ __forceinline__ float rope_turn(float x, float other, bool first, float2 cs) {
   const float a = __fmul_rn(x, cs.x), b = __fmul_rn(other, cs.y);
   return first ? __fsub_rn(a, b) : __fadd_rn(a, b);
@@ -89,31 +52,41 @@ __device__ __forceinline__ void load32(const void* p, uint32_t* w) {
                : "l"(p));
 }
 
-// Cosines and sines of pairs 8 i .. 8 i + 7 of token row `at`: four 16-byte loads where the
-// pairs have one axis.
-template <bool EARLY>
-__device__ __forceinline__ void rope_angles(const RopeArgs& p, long long at, int i, float2* cs) {
-  uint32_t w = p.axes[0] >> (16 * (i & 1));
+// The axes of a chunk's pairs, two bits each.
+__device__ __forceinline__ uint32_t rope_axes(const RopeArgs& p, int i) {
+  uint32_t w = p.axes[0];
 #pragma unroll
   for (int k = 1; k < kRopeMaxAxes; ++k)
-    if (i / 2 == k) w = p.axes[k] >> (16 * (i & 1));
-  w &= 0xFFFFu;
+    if (i / 2 == k) w = p.axes[k];
+  return w >> (16 * (i & 1)) & 0xFFFFu;
+}
+// The position that `at` points to; one that the table does not have is flagged and clamped.
+__device__ __forceinline__ int rope_position(const RopeArgs& p, const int32_t* at) {
+  const int x = *at;
+  if ((unsigned)x < (unsigned)p.len) return x;
+  if (p.status != nullptr) atomicOr(p.status, 2);  // NOSA_QUANT_INDEX
+  return x < 0 ? 0 : p.len - 1;
+}
+// Cosines and sines of pairs 8 i .. 8 i + 7 (axes w) of the token whose position on axis 0 is at
+// `at`: two 32-byte loads where the pairs have one axis.
+__device__ __forceinline__ void rope_angles(const RopeArgs& p, uint32_t w, const int32_t* at, int i, float2* cs) {
   if (w == (w & 3u) * 0x5555u) {
-    const float4* src = reinterpret_cast<const float4*>(p.table + (long long)rope_position<EARLY>(p, at, 8 * i) * p.pairs + 8 * i);
-    if (p.wide && !EARLY) {  // half the passes through L1: a warp's lanes are 64 bytes apart
+    const float4* src = reinterpret_cast<const float4*>(p.table + (long long)rope_position(p, at + (w & 3u) * p.axis_stride) * p.pairs + 8 * i);
+    if (p.wide) {  // half the passes through L1: a warp's lanes are 64 bytes apart
 #pragma unroll
       for (int k = 0; k < 2; ++k) load32(src + 2 * k, reinterpret_cast<uint32_t*>(cs + 4 * k));
       return;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 x = rope_load<EARLY>(src + k);
+      const float4 x = src[k];
       cs[2 * k] = make_float2(x.x, x.y);
       cs[2 * k + 1] = make_float2(x.z, x.w);
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) cs[k] = rope_load<EARLY>(p.table + (long long)rope_position<EARLY>(p, at, 8 * i + k) * p.pairs + 8 * i + k);
+    for (int k = 0; k < 8; ++k)
+      cs[k] = p.table[(long long)rope_position(p, at + (w >> (2 * k) & 3u) * p.axis_stride) * p.pairs + 8 * i + k];
   }
 }
 // The sixteen elements of a turned chunk, unrounded.
