@@ -698,10 +698,12 @@ nosa_status nosa_quant4_read(const nosa_config* cfg, const void* units, int64_t 
  * nosa_quant_attention over 4-bit units, with the queries rotated on the way (rope NULL: as
  * they are): a row's products take bit for bit what nosa_rotate makes of it. positions as
  * above, for n_queries tokens of each request; those past q_len are not read. Logits are
- * held as precisely as with nosa_quant_attention (the product of a bf16 query element and a
- * key's step is exact, that of an fp32 one keeps 22 bits); a weight times the step of a
- * value is rounded to 11 bits (bf16 calls) or 22 (fp32). Other arguments and rules as
- * nosa_quant_attention.
+ * held as precisely as with nosa_quant_attention (the product of a query element and a key's
+ * step is exact, for fp32 as three terms of 8 bits, but for at most 2^-39 of the largest
+ * element of the row); a weight times the step of a value is rounded to 11 bits (bf16 calls)
+ * or 22 (fp32). The largest element of a query times that of a block's keys has to be below
+ * 2^120, a value below 2^118. With rope the workspace also holds the rotated queries. Other
+ * arguments and rules as nosa_quant_attention.
  */
 size_t nosa_quant4_attention_workspace_bytes(const nosa_config* cfg, int32_t max_blocks,
                                              int32_t n_queries, int32_t with_mass);

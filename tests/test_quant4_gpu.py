@@ -855,6 +855,167 @@ print("ok")
     assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
 
 
+@pytest.mark.parametrize("turned", [False, True])
+@pytest.mark.parametrize("dtype,batch,hq,hkv,d,T,n,cap", [
+    ("bf16", 2, 8, 2, 128, 1, 700, 11), ("bf16", 2, 8, 2, 64, 1, 700, 600), ("f32", 3, 4, 1, 64, 1, 400, 7), ("f32", 1, 4, 2, 128, 3, 999, 16),
+    ("bf16", 2, 8, 2, 128, 12, 900, 15), ("f32", 2, 8, 2, 64, 8, 300, 5), ("bf16", 300, 4, 4, 64, 1, 130, 3), ("bf16", 2, 8, 2, 128, 3, 200, 4)])
+def test_attention_wait_that_gives_up(dtype, batch, hq, hkv, d, T, n, cap, turned, monkeypatch):
+    """Waits that give up at once (set on the host): the status says so, the rows that exist are
+    NaN (every unit has blocks), the accumulated weights stay, the kernels end, and the next call is right."""
+    rng = np.random.default_rng(61)
+    c = Cache(rng, dtype, batch, hq, hkv, d, [n - h for _ in range(batch) for h in range(hkv)], cap=cap).upload()
+    q = query(rng, batch, T, hq, d, dtype)
+    turn = Turn(d, 1000)
+    pos = turn.positions(rng, batch, T)
+    kw = dict(rope=turn.rope, positions=dev(pos)) if turned else {}
+    q_len = [T] * (batch - 1) + [max(1, T - 1)]
+    m0 = rng.random(size=c.tab.shape).astype(np.float32)
+    mass = dev(m0)
+    c.run(q, q_len=q_len, mass=dev(m0), **kw)
+    ws = c.workspace
+    monkeypatch.setenv("NOSA_INJECT_FAIL", "wait")
+    for _ in range(3):
+        out, lse, status = c.run(q, q_len=q_len, mass=mass, decay=0.5, workspace=ws, **kw)
+        assert status == nosa.NOSA_QUANT_WAIT
+        for b in range(batch):
+            assert torch.isnan(out[b, :q_len[b]]).all() and torch.isnan(lse[b, :q_len[b]]).all()
+            assert (out[b, q_len[b]:] == 7).all() and (lse[b, q_len[b]:] == 7).all()
+        assert np.array_equal(mass.cpu().numpy(), m0)
+    monkeypatch.delenv("NOSA_INJECT_FAIL")
+    out, lse, status = c.run(q, q_len=q_len, mass=mass, decay=0.5, workspace=ws, **kw)
+    assert status == 0
+    c.check(turn.oracle(f64(q), pos, dtype) if turned else q, out, lse, q_len=q_len, mass0=m0, mass=f64(mass), decay=0.5)
+
+
+@pytest.mark.parametrize("dtype,batch,hq,hkv,d,cap", [("bf16", 64, 16, 8, 64, 4), ("f32", 40, 8, 8, 128, 4), ("bf16", 160, 24, 8, 128, 200),
+                                                      ("f32", 300, 4, 4, 64, 140)])
+def test_calls_behind_each_other_read_what_the_last_one_wrote(dtype, batch, hq, hkv, d, cap):
+    """Steps of append, attention, reading back, rotation and eviction over many units, whose lengths share
+    cache lines, queries and keys turned by positions that change in place: queued without a pause and
+    with the GPU waited for after every call, the bits are the same. A masked token's step is no number, so
+    that its part is gone through again."""
+    rng = np.random.default_rng(71)
+    U = batch * hkv
+    cfg = config(batch, hq, hkv, d, dtype)
+    turn = Turn(d, 999)
+    steps = 16
+    ins = [(query(rng, batch, 1, hkv, d, dtype, 1.0), query(rng, batch, 1, hkv, d, dtype, 1.0), query(rng, batch, 1, hq, d, dtype),
+            dev(turn.positions(rng, batch, 1))) for _ in range(steps)]
+    prompt = query(rng, batch, 3 * B, hkv, d, dtype, 1.0)
+    e = rng.normal(size=(batch, 3 * B, hkv)).astype(np.float32)
+    e[:, 7] = -np.inf
+    e, p_pos = dev(e), dev(turn.positions(rng, batch, 3 * B))
+    n_new = dev(rng.integers(1, 3 * B - 1, size=batch).astype(np.int32))
+    at = torch.as_tensor(Q.places(d)[2][7], device="cuda")
+
+    def loop(pause):
+        done = torch.cuda.synchronize if pause else lambda: None
+        units = torch.zeros(U * 4, Q.unit_bytes(d), dtype=torch.uint8, device="cuda")
+        tab = torch.zeros(U, cap, dtype=torch.int32, device="cuda")
+        tab[:, :4] = torch.arange(U * 4, dtype=torch.int32, device="cuda").view(U, 4)
+        tail = torch.zeros(U * nosa.nosa_payload_bytes(cfg), dtype=torch.uint8, device="cuda")
+        lens, mass = torch.zeros(U, dtype=torch.int32, device="cuda"), torch.zeros(U, cap, device="cuda")
+        ws = torch.zeros(nosa.nosa_quant4_attention_workspace_bytes(cfg, cap, 1, True), dtype=torch.uint8, device="cuda")
+        outs = [(torch.empty_like(ins[0][2]), torch.empty(batch, 1, hq, device="cuda"), torch.empty_like(ins[0][2]),
+                 torch.empty(U * 4, B, d, dtype=DT[dtype], device="cuda")) for _ in range(steps)]
+        pos = torch.zeros_like(ins[0][3])
+        torch.cuda.synchronize()
+        nosa.nosa_quant4_append(cfg, prompt, prompt, e, units, tab, tail, lens, n_new=n_new, rope=turn.rope, positions=p_pos)
+        done()
+        units.view(U, 4, -1)[:, 0, at + 1] |= 0x7E  # the masked token of the first block, if it is full: no number
+        done()
+        for (k, v, q, p), (out, lse, turned, back) in zip(ins, outs):
+            pos.copy_(p)
+            done()
+            nosa.nosa_quant4_append(cfg, k, v, None, units, tab, tail, lens, rope=turn.rope, positions=pos)
+            done()
+            nosa.nosa_quant4_attention(cfg, units, tab, tail, lens, q, out, lse=lse, mass=mass, decay=0.9, rope=turn.rope, positions=pos,
+                                       workspace=ws)
+            done()
+            nosa.nosa_rotate(cfg, turn.rope, pos, out, q_out=turned)
+            done()
+            nosa.nosa_quant4_read(cfg, units, back)
+            done()
+            nosa.nosa_quant_evict(cfg, 2, 1, tab, mass, lens)
+            done()
+        torch.cuda.synchronize()
+        return [x for four in outs for x in four] + [mass, lens, tail, units]
+
+    want = loop(True)
+    assert not torch.isnan(want[0]).any()
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(want, loop(False)))
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d,T,n", [("bf16", 8, 8, 64, 1, 70), ("bf16", 16, 4, 128, 1, 900), ("f32", 8, 2, 64, 4, 300), ("f32", 8, 4, 128, 1, 64)])
+def test_attention_queries_written_by_the_call_before(dtype, hq, hkv, d, T, n):
+    """Each call's queries are the outputs of the call before it, in two buffers that are written again
+    and again, turned on the way: queued without a pause and with one, the bits are the same."""
+    rng = np.random.default_rng(73)
+    c = Cache(rng, dtype, 20, hq, hkv, d, [n] * (20 * hkv)).upload()
+    first = query(rng, 20, T, hq, d, dtype)
+    ws = torch.empty(nosa.nosa_quant4_attention_workspace_bytes(c.cfg, c.cap, T), dtype=torch.uint8, device="cuda")
+    turn = Turn(d, 60)
+    pos = dev(turn.positions(rng, 20, T))
+
+    def chain(pause):
+        a, b, seen = first.clone(), torch.empty_like(first), []
+        for i in range(40):
+            nosa.nosa_quant4_attention(c.cfg, c.units, c.t_tab, c.tail, c.t_lens, a, b, rope=turn.rope, positions=pos, workspace=ws)
+            if pause:
+                torch.cuda.synchronize()
+            a, b = b, a
+            if i % 8 == 7:
+                seen.append(a.clone())
+        torch.cuda.synchronize()
+        return seen
+
+    want = chain(True)
+    for _ in range(5):
+        assert all(torch.equal(x, y) for x, y in zip(want, chain(False)))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 128)])
+def test_attention_the_longest_table(dtype, d):
+    """16384 table entries of a few units named again and again, all rows of a request."""
+    rng = np.random.default_rng(81)
+    c = Cache(rng, dtype, 1, 4, 1, d, [64 * 40 + 7])
+    c.cap = 16384
+    c.lens = np.array([64 * 16383 + 50], np.int32)
+    c.tab = rng.integers(0, len(c.images), size=(1, c.cap)).astype(np.int32)
+    c.upload()
+    q = query(rng, 1, 2, 4, d, dtype)
+    m0 = np.zeros(c.tab.shape, np.float32)
+    mass = dev(m0)
+    out, lse, status = c.run(q, mass=mass)
+    assert status == 0
+    c.check(q, out, lse, mass0=m0, mass=f64(mass))
+
+
+def test_rotate_in_a_graph_on_a_stream_of_its_own():
+    """A captured rotation, forth and back, replayed while the inputs change in place."""
+    rng = np.random.default_rng(83)
+    turn = Turn(128, 500, some_axes("sections", 64))
+    cfg = config(2, 8, 2, 128, "bf16")
+    q, k = query(rng, 2, 40, 8, 128, "bf16"), query(rng, 2, 40, 2, 128, "bf16")
+    pos = dev(turn.positions(rng, 2, 40))
+    qo, ko, back = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q)
+    g, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=stream):
+        nosa.nosa_rotate(cfg, turn.rope, pos, q, k, q_out=qo, k_out=ko)
+        nosa.nosa_rotate(cfg, turn.rope, pos, qo, q_out=back, backward=True)
+    for _ in range(3):
+        q.copy_(query(rng, 2, 40, 8, 128, "bf16"))
+        p = turn.positions(rng, 2, 40)
+        pos.copy_(dev(p))
+        g.replay()
+        torch.cuda.synchronize()
+        want = turn.oracle(f64(q), p, "bf16")
+        assert np.array_equal(f64(qo), want) and np.array_equal(f64(ko), turn.oracle(f64(k), p, "bf16"))
+        assert np.array_equal(f64(back), turn.oracle(want, p, "bf16", True))
+
+
 # ---------------------------------------------------------------------------
 # all of them, as a generation uses them
 # ---------------------------------------------------------------------------

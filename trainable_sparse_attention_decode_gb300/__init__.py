@@ -651,14 +651,15 @@ def _turn(rope, positions, device, batch, n, torch):
         if positions is not None:
             raise ValueError("positions without a rope")
         return None, None
-    if not isinstance(rope, NosaRope):
+    if type(rope) is not NosaRope:
         raise ValueError("rope must be made by nosa_rope")
     if rope.device != device:
         raise ValueError(f"the rope's table is on cuda:{rope.device}, the configuration's device is cuda:{device}")
     if positions is None:
         raise ValueError("positions is required")
-    shape = (batch, n) if rope.n_axes == 1 and positions.ndim == 2 else (rope.n_axes, batch, n)
-    return rope.ref, _arg(positions, device, shape, torch.int32, "positions")
+    axes = rope.n_axes
+    return rope.ref, _arg(positions, device, (batch, n) if axes == 1 and positions.ndim == 2 else (axes, batch, n),
+                          torch.int32, "positions")
 
 
 def nosa_rotate(cfg: NosaConfig, rope: NosaRope, positions, q, k=None, q_out=None, k_out=None, backward=False,
@@ -670,25 +671,27 @@ def nosa_rotate(cfg: NosaConfig, rope: NosaRope, positions, q, k=None, q_out=Non
     try:
         dev, batch, d = cfg.device, cfg.batch, cfg.head_dim
         dt = torch.float32 if cfg.dtype == NOSA_F32 else torch.bfloat16
-        if q is None and k is None:
-            raise ValueError("q or k is required")
-        if rope is None:
-            raise ValueError("rope is required")
-        if (q is None and q_out is not None) or (k is None and k_out is not None):
-            raise ValueError("an output without its input")
+        if rope is None or (q is None and k is None):
+            raise ValueError("rope and one of q and k are required")
         n = (k if q is None else q).shape[1]
         ref, pos = _turn(rope, positions, dev, batch, n, torch)
-        args = []
-        for x, y, heads, what in ((q, q_out, cfg.n_q_heads, "q"), (k, k_out, cfg.n_kv_heads, "k")):
-            if x is None:
-                args += (None, None, None, None)
-                continue
-            shp = (batch, n, heads, d)
-            xp = _rows(x, dev, shp, dt, what)
-            args += xp
-            args += xp if y is None or y is x else _rows(y, dev, shp, dt, what + "_out")
+        qp = qs = qop = qos = kp = ks = kop = kos = None
+        if q is not None:
+            shp = (batch, n, cfg.n_q_heads, d)
+            qop, qos = qp, qs = _rows(q, dev, shp, dt, "q")
+            if q_out is not None:
+                qop, qos = _rows(q_out, dev, shp, dt, "q_out")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if k is not None:
+            shp = (batch, n, cfg.n_kv_heads, d)
+            kop, kos = kp, ks = _rows(k, dev, shp, dt, "k")
+            if k_out is not None:
+                kop, kos = _rows(k_out, dev, shp, dt, "k_out")
+        elif k_out is not None:
+            raise ValueError("k_out without k")
         st = lib.nosa_rotate(
-            C.byref(cfg), ref, pos, n, *args, 1 if backward else 0,
+            C.byref(cfg), ref, pos, n, qp, qs, qop, qos, kp, ks, kop, kos, 1 if backward else 0,
             None if status is None else _arg(status, dev, (1,), torch.int32, "status"),
             torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
         if st:

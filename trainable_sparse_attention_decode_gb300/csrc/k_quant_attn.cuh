@@ -375,6 +375,7 @@ template <int D, int WR, int RP, int IS, bool F32, int BITS>
 __device__ __noinline__ void qa_part_again(const QStreamParams& p, int u, int j0, int j1, int first, float* red, const float2* ml) {
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   constexpr int DL = D / 32;  // dims of a lane
+  if (BITS == 4) griddep_wait();  // (who calls this may not have waited, and these are ordinary loads)
   const int b = u / p.Hkv, h = u % p.Hkv, lane = threadIdx.x & 31;
   const int n = max(0, quant_len(p.lens, u, p.max_blocks, nullptr, false)), qn = quant_count(p.q_len, b, p.T, nullptr, false);
   auto block = [&](int j) -> const uint8_t* {  // null: the table names no unit
