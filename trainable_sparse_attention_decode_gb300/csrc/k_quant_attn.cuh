@@ -1,4 +1,4 @@
-// Attention over the 8-bit block cache.
+// Attention over the block caches of 8 and of 4 bits.
 //
 // Row (t, g) of unit u sees tokens [0, len - T_b + t]: its logits are
 //     l_j = q . k_j / sqrt(d) + e_j   (e_j = -inf masks token j),
@@ -49,6 +49,32 @@
 // 4 heads, 32 units of 8200 tokens: 41 us; 128 rows over 16 units of 16384 tokens: 98 us)
 // the products' instructions bound it: about 1300 of a warp and block at 1.7 a cycle, six
 // consumer warps being all that the outputs' registers leave room for.
+//
+// The 4-bit cache takes the same launches with other products (BITS = 4):
+//     q . k_j   = scale (sum_x (q_x step_x) n_jx + sum_x q_x zero_x)
+//     sum_j p_j v_jx = scale (sum_j (p_j step_j) n_jx + sum_j p_j zero_j)   for the run of dims of x.
+// The codes n are operands as they lie in the unit, under a mask, as subnormal fp16 numbers
+// (codes_f16). The queries times the steps are made once a block: a step has three bits, so the
+// product of a bf16 element (or of an 8-bit term of an fp32 one: there are three) is exact and
+// the logits are as good as fp32 sums of exact products. The weights, rounded to fp16, times the
+// values' steps are rounded once more. The sums with the zeros are a product more whose rows are
+// all alike. Queries are turned by their positions in a launch before the stream, beside which the
+// stream starts: only its helper waits for them.
+// Measured on GB300:
+//   256 units x 65536 tokens, d = 128, 4 rows             2.45 GB   408 us   88 %
+//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.33 GB    73 us   66 %
+//   8 units x 131071 tokens, 4 rows                       0.15 GB    41 us   55 %
+//   64 units x 16384 tokens, d = 64, 2 rows               0.08 GB    28 us   42 %
+//   1 unit x 2031 tokens, d = 64, fp32                    0.2 MB    9.2 us
+// With half the bytes the consumers bound the stream: a block takes a warp about 940
+// instructions (256 of them unpack codes), eight warps issue 1.9 a cycle, and the same call with
+// all units in L2 takes 395 us. What was tried against it for 256 units x 65536 tokens: twelve
+// consumer warps that take registers from the producer's warpgroup, with the parts in the ring
+// 385 us, but 89 (73) for the ragged units, whose ends the longer joins held up; logits without
+// masks where every row sees the block 410 (404); the zeros' product as the codes' first summand 415
+// (407); fp16 codes with two masks and a shift more 407 (399). A join that fits beside the stream (its
+// registers or its threads cut) took 2 to 4 us longer than one that starts after it. 128 rows over 16
+// units of 16384 tokens take 101 us, 32 over 32 of 8200 38.6.
 #pragma once
 
 #include "k_quant4.cuh"
@@ -149,6 +175,18 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t* a) {
   a[1] = w & 0x00FF00FFu;
   a[3] = __byte_perm(w, 0, 0x4341);
   a[2] = a[3] & 0x000F000Fu;
+}
+// The same with 2 n - 15 for every code n: sums of weights times them stay near zero.
+__device__ __forceinline__ void codes_signed(uint32_t w, uint32_t* a) {
+  codes_f16(w, a);
+  const __half2 two = __float2half2_rn(2.f);
+  const __half2 off = __halves2half2(__ushort_as_half(0x800F), __ushort_as_half(0x800F));   // -2^-24 15
+  const __half2 both = __halves2half2(__ushort_as_half(0x80FF), __ushort_as_half(0x80FF));  // -2^-24 (15 + 16 15)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&a[i]), two, i % 2 ? both : off);
+    a[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 // A product of such a tile: rows 0..7 as 2^-24 of what the codes stand for, 8..15 as 2^-20.
 __device__ __forceinline__ void codes_split(float* d) {
@@ -865,6 +903,11 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
         const int pos = j * kQB + 16 * s0 + tok;
         float corr[NT][2], vsc[NT][2];
         uint32_t pb[NT][SL][2], pl[F32 ? NT : 1][SL][2];
+        // fp32: the weights' sums with zero + 7.5 step of each run of dims, the middle of the codes, which
+        // enter their product as 2 n - 15. Codes from 0 to 15 and the zeros would make two sums of one sign
+        // each that nearly cancel, while what the tensor cores cut off in them does not: 5e-5 of the output
+        // at 2031 tokens; with n - 8, 1e-5, and 7e-5 at 131071.
+        float mid[F32 && BITS == 4 ? D / 64 : 1][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -917,6 +960,31 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
               }
             l_run[nt][x] = l_run[nt][x] * corr[nt][x] + sum;
             blk_l[nt][x] = SL == 4 && BITS == 4 ? sum : blk_l[nt][x] * corr[nt][x] + sum;
+          }
+          if constexpr (F32 && BITS == 4) {
+            static_assert(NT == 1, "one row group of 8");
+#pragma unroll
+            for (int r = 0; r < D / 64; ++r) {
+              const uint4* steps = reinterpret_cast<const uint4*>(unit + quant4_vstep_off(D) + r * 128 + (g >> 1) * 32);
+              const uint4* zeros = reinterpret_cast<const uint4*>(unit + quant4_vzero_off(D) + r * 128 + (g >> 1) * 32);
+              const uint4 s4[2] = {steps[0], steps[1]}, z4[2] = {zeros[0], zeros[1]};
+              mid[r][0] = mid[r][1] = 0.f;
+#pragma unroll
+              for (int w = 0; w < SL; ++w)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const float2 st = f32x2(word_of(s4[w / 2], 2 * (w % 2) + y)), z = f32x2(word_of(z4[w / 2], 2 * (w % 2) + y));
+                  const float at = g & 1 ? fmaf(7.5f, st.y, z.y) : fmaf(7.5f, st.x, z.x);
+                  mid[r][0] += sc[nt][w][2 * y] * at;
+                  mid[r][1] += sc[nt][w][2 * y + 1] * at;
+                }
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                mid[r][x] += __shfl_xor_sync(0xffffffffu, mid[r][x], 4);
+                mid[r][x] += __shfl_xor_sync(0xffffffffu, mid[r][x], 8);
+                mid[r][x] += __shfl_xor_sync(0xffffffffu, mid[r][x], 16);
+              }
+            }
           }
 #pragma unroll
           for (int w = 0; w < SL; ++w)
@@ -978,8 +1046,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 #pragma unroll
               for (int w = 0; w < SL; ++w) {
                 const uint32_t z0 = word_of(z4[w / 2], 2 * (w % 2)), z1 = word_of(z4[w / 2], 2 * (w % 2) + 1), za[4] = {z0, z0, z1, z1};
-                if constexpr (F32) mma16816(tz, za, pl[nt][w][0], pl[nt][w][1]);
-                mma16816(tz, za, pb[nt][w][0], pb[nt][w][1]);
+                if constexpr (!F32) mma16816(tz, za, pb[nt][w][0], pb[nt][w][1]);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   const uint32_t st = word_of(s4[w / 2], 2 * (w % 2) + y);
@@ -994,8 +1061,8 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
                   }
                 }
               }
-              base[nt][0] = tz[0] * vsc[nt][0];
-              base[nt][1] = tz[1] * vsc[nt][1];
+              base[nt][0] = (F32 ? mid[F32 ? r : 0][0] : tz[0]) * vsc[nt][0];
+              base[nt][1] = (F32 ? mid[F32 ? r : 0][1] : tz[1]) * vsc[nt][1];
             }
 #pragma unroll
             for (int m = 4 * r; m < 4 * r + 4; ++m) {
@@ -1006,7 +1073,10 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 #pragma unroll
               for (int w = 0; w < SL; ++w) {
                 uint32_t a[4];
-                codes_f16(word_of(v, w), a);
+                if constexpr (F32)
+                  codes_signed(word_of(v, w), a);
+                else
+                  codes_f16(word_of(v, w), a);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                   if constexpr (F32) mma16816(t[nt], a, pt[nt][w][0], pt[nt][w][1]);
@@ -1020,7 +1090,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                   float& oo = o[nt][m][x];
-                  oo = oo * corr[nt][x & 1] + base[nt][x & 1] + t[nt][x] * (vsc[nt][x & 1] * (x < 2 ? 0x1p24f : 0x1p20f));
+                  oo = oo * corr[nt][x & 1] + base[nt][x & 1] + t[nt][x] * (vsc[nt][x & 1] * (x < 2 ? 0x1p24f : 0x1p20f) * (F32 ? 0.5f : 1.f));
                 }
             }
           }
