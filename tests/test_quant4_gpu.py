@@ -721,6 +721,49 @@ def test_attention_large_and_small_queries():
     c.check(q, out, lse)
 
 
+@pytest.mark.parametrize("d,n", [(64, 704), (128, 704), (64, 16384), (128, 16384)])
+def test_attention_fp32_outputs_in_the_norm(d, n):
+    """fp32 outputs keep fp32's bits in the norm too, where values of both signs nearly cancel.
+
+    Each weight is off by a few independent roundings (its two 11-bit terms and their products with a step,
+    2^-22 each; the exponential, 2^-22; its logit, some 2^-22), so sum w_j v_j of independent v_j is off by 2^-21
+    of its norm or so, and with the sums' own additions by 2^-19 at most. Sums that cut off at the size of
+    sum w_j |v_j| would show: that is sqrt(n) times the output here."""
+    rng = np.random.default_rng(d + n)
+    c = Cache(rng, "f32", 2, 4, 1, d, [n] * 2, cap=n // B + 1, masked=0.0).upload()
+    q = query(rng, 2, 1, 4, d, "f32")
+    out, lse, status = c.run(q)
+    assert status == 0
+    for u in range(2):
+        K, V, e, Ks, Vs = c.tokens(u)
+        want, wl = Q.attend(f64(q)[u, 0], K, V, e, np.full(4, n), Ks, Vs)[:2]
+        got = f64(out)[u, 0]
+        assert np.linalg.norm(got - want) <= 2.0 ** -19 * np.linalg.norm(want), u
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_logits_of_queries_with_large_elements(dtype, d):
+    """An element in 16 of a query is 512 times the others, the keys are not zero there: the lesser products
+    are not cut off at the size of the larger operands.
+
+    The codes are fp16 operands whose exponents are at most 2^6 too large for a code of 15; a sum of 16 products
+    is cut off 2^-24 below its largest exponent, so 2^-18 q step for each of the 15 lesser ones, and those are
+    independent: 2^-17 q step for d / 16 sums of 16, of which S is at least 7 d / 16 q step (step n + |zero| of
+    a normal sample's 16 levels): 2^-19.8 S / sqrt(d / 16), at most 2^-20 S for what the lse of a few large logits shows."""
+    rng = np.random.default_rng(d)
+    c = Cache(rng, dtype, 4, 8, 1, d, [704] * 4, masked=0.0).upload()
+    q = query(rng, 4, 1, 8, d, dtype)
+    q[..., 3::16] *= 512
+    out, lse, status = c.run(q)
+    assert status == 0
+    for u in range(4):
+        K, V, e, Ks, Vs = c.tokens(u)
+        want, wl, w, A, S = Q.attend(f64(q)[u, 0], K, V, e, np.full(8, 704), Ks, Vs)
+        assert np.all(np.abs(f64(lse)[u, 0] - wl) <= 2.0 ** -20 * S + 2.0 ** -23 * np.abs(wl)), u
+    c.check(q, out, lse)
+
+
 @pytest.mark.parametrize("dtype,d,T", [("bf16", 64, 1), ("bf16", 128, 1), ("f32", 64, 1), ("f32", 128, 1), ("bf16", 128, 8), ("f32", 128, 4)])
 def test_attention_queries_with_an_outlier(dtype, d, T):
     """One element of 30 000 in a query meets keys of zero: the logits keep the others' bits."""

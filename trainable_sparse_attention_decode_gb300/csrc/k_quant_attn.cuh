@@ -54,27 +54,28 @@
 //     q . k_j   = scale (sum_x (q_x step_x) n_jx + sum_x q_x zero_x)
 //     sum_j p_j v_jx = scale (sum_j (p_j step_j) n_jx + sum_j p_j zero_j)   for the run of dims of x.
 // The codes n are operands as they lie in the unit, under a mask, as subnormal fp16 numbers
-// (codes_f16). The queries times the steps are made once a block: a step has three bits, so the
+// (codes_f16; some of them raised, codes_of). The queries times the steps are made once a block: a step has three bits, so the
 // product of a bf16 element (or of an 8-bit term of an fp32 one: there are three) is exact and
 // the logits are as good as fp32 sums of exact products. The weights, rounded to fp16, times the
 // values' steps are rounded once more. The sums with the zeros are a product more whose rows are
 // all alike. Queries are turned by their positions in a launch before the stream, beside which the
 // stream starts: only its helper waits for them.
 // Measured on GB300:
-//   256 units x 65536 tokens, d = 128, 4 rows             2.45 GB   408 us   88 %
-//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.33 GB    73 us   66 %
+//   256 units x 65536 tokens, d = 128, 4 rows             2.45 GB   411 us   88 %
+//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.33 GB    74 us   65 %
 //   8 units x 131071 tokens, 4 rows                       0.15 GB    41 us   55 %
 //   64 units x 16384 tokens, d = 64, 2 rows               0.08 GB    28 us   42 %
 //   1 unit x 2031 tokens, d = 64, fp32                    0.2 MB    9.2 us
-// With half the bytes the consumers bound the stream: a block takes a warp about 940
-// instructions (256 of them unpack codes), eight warps issue 1.9 a cycle, and the same call with
-// all units in L2 takes 395 us. What was tried against it for 256 units x 65536 tokens: twelve
+// With half the bytes the consumers bound the stream: a block takes a warp about 1000
+// instructions (320 of them make operands of codes), eight warps issue 1.9 a cycle, and with
+// all units in L2 the call takes 3 % less. What was tried against it for 256 units x 65536 tokens
+// (before the keys' codes were raised, which costs 5 us): twelve
 // consumer warps that take registers from the producer's warpgroup, with the parts in the ring
 // 385 us, but 89 (73) for the ragged units, whose ends the longer joins held up; logits without
 // masks where every row sees the block 410 (404); the zeros' product as the codes' first summand 415
 // (407); fp16 codes with two masks and a shift more 407 (399). A join that fits beside the stream (its
 // registers or its threads cut) took 2 to 4 us longer than one that starts after it. 128 rows over 16
-// units of 16384 tokens take 101 us, 32 over 32 of 8200 38.6.
+// units of 16384 tokens take 101 us, 32 over 32 of 8200 39.6, in fp32 64.
 #pragma once
 
 #include "k_quant4.cuh"
@@ -176,22 +177,37 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t* a) {
   a[3] = __byte_perm(w, 0, 0x4341);
   a[2] = a[3] & 0x000F000Fu;
 }
-// The same with 2 n - 15 for every code n: sums of weights times them stay near zero.
-__device__ __forceinline__ void codes_signed(uint32_t w, uint32_t* a) {
+// What a product's sum cuts off goes by the exponents of the operands as they are written, and a subnormal's
+// is that of the least normal number: 2^6 above 15 units of it. So sums that have to keep fp32's bits take the
+// codes with a multiplication more. KeysBf16: rows 0..7 times 2^4, as 8..15 have it (logits of queries with
+// elements 512 times the others' are off by 2^-22 of the sum of their magnitudes, without it 2^-18; 406 -> 413
+// us for 256 units x 65536 tokens, with all four registers 422). KeysF32: all times 2^15, normal numbers.
+// ValuesF32: so too, less 7.5 of each code. ValuesBf16: as they lie, for the weights are rounded to 2^-11.
+enum class Codes { KeysBf16, KeysF32, ValuesBf16, ValuesF32 };
+template <Codes kind>
+__device__ __forceinline__ void codes_of(uint32_t w, uint32_t* a) {
   codes_f16(w, a);
-  const __half2 two = __float2half2_rn(2.f);
-  const __half2 off = __halves2half2(__ushort_as_half(0x800F), __ushort_as_half(0x800F));   // -2^-24 15
-  const __half2 both = __halves2half2(__ushort_as_half(0x80FF), __ushort_as_half(0x80FF));  // -2^-24 (15 + 16 15)
+  if (kind == Codes::ValuesBf16) return;
+  const __half2 up = __float2half2_rn(kind == Codes::KeysBf16 ? 16.f : 32768.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&a[i]), two, i % 2 ? both : off);
+    if (kind == Codes::KeysBf16 && i % 2) continue;
+    const __half2 x = *reinterpret_cast<const __half2*>(&a[i]);
+    const __half2 h = kind == Codes::ValuesF32 ? __hfma2(x, up, __float2half2_rn(i % 2 ? -7.5f * 17.f / 512.f : -7.5f / 512.f)) : __hmul2(x, up);
     a[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
 }
-// A product of such a tile: rows 0..7 as 2^-24 of what the codes stand for, 8..15 as 2^-20.
+// What one stands for in such a tile's product, rows 0..7 (low) and 8..15, after codes_split.
+template <Codes kind>
+__device__ __forceinline__ constexpr float codes_unit(bool low) {
+  return kind == Codes::KeysBf16 ? 0x1p20f : kind == Codes::ValuesBf16 ? (low ? 0x1p24f : 0x1p20f) : (low ? 0x1p9f : 0x1p5f);
+}
+// Takes the codes of rows 0..7 off rows 8..15.
+template <Codes kind>
 __device__ __forceinline__ void codes_split(float* d) {
-  d[2] -= d[0];
-  d[3] -= d[1];
+  constexpr float f = kind == Codes::KeysBf16 ? 0x1p-4f : 1.f;
+  d[2] -= d[0] * f;
+  d[3] -= d[1] * f;
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
@@ -746,6 +762,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
   }
 
   // ---- consumers ----
+  constexpr Codes kKeys = F32 ? Codes::KeysF32 : Codes::KeysBf16, kValues = F32 ? Codes::ValuesF32 : Codes::ValuesBf16;
   const int g = lane >> 2, c = lane & 3;
   const int tok = 4 * (g >> 1) + (g & 1);  // this lane's tokens of a slice: tok and tok + 2
   const int is = warp % IS, rg = warp / IS;
@@ -877,7 +894,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 #pragma unroll
               for (int w = 0; w < SL; ++w) {
                 uint32_t a[4];
-                codes_f16(word_of(v, w), a);
+                codes_of<kKeys>(word_of(v, w), a);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -888,7 +905,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int w = 0; w < SL; ++w) codes_split(sc[nt][w]);
+            for (int w = 0; w < SL; ++w) codes_split<kKeys>(sc[nt][w]);
         }
         // ---- softmax over the 16 SL tokens ----
         // (Warp-wide branches around the masks or the rescaling, and packed pairs, were all
@@ -904,9 +921,9 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
         float corr[NT][2], vsc[NT][2];
         uint32_t pb[NT][SL][2], pl[F32 ? NT : 1][SL][2];
         // fp32: the weights' sums with zero + 7.5 step of each run of dims, the middle of the codes, which
-        // enter their product as 2 n - 15. Codes from 0 to 15 and the zeros would make two sums of one sign
-        // each that nearly cancel, while what the tensor cores cut off in them does not: 5e-5 of the output
-        // at 2031 tokens; with n - 8, 1e-5, and 7e-5 at 131071.
+        // enter their product as n - 7.5. Codes from 0 to 15 and the zeros would make two sums of one sign
+        // each that nearly cancel, while what the tensor cores cut off in them does not. (The output is 4e-7
+        // off in the norm at 2031 tokens and 9e-7 at 131071, as that of fp32 sums is.)
         float mid[F32 && BITS == 4 ? D / 64 : 1][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -931,7 +948,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   float& l = sc[nt][w][2 * y + x];
-                  l = l * (f * (y ? 0x1p20f : 0x1p24f)) + (qz[nt][x] * f + ev[w][y]);
+                  l = l * (f * codes_unit<kKeys>(y == 0)) + (qz[nt][x] * f + ev[w][y]);
                   if (ev[w][y] == -INFINITY || (edge && pos + 16 * w + 2 * y >= sees)) l = -INFINITY;
                 }
                 mx = max3_nan(mx, sc[nt][w][x], sc[nt][w][2 + x]);
@@ -1073,10 +1090,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 #pragma unroll
               for (int w = 0; w < SL; ++w) {
                 uint32_t a[4];
-                if constexpr (F32)
-                  codes_signed(word_of(v, w), a);
-                else
-                  codes_f16(word_of(v, w), a);
+                codes_of<kValues>(word_of(v, w), a);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                   if constexpr (F32) mma16816(t[nt], a, pt[nt][w][0], pt[nt][w][1]);
@@ -1084,13 +1098,13 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
                 }
               }
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) codes_split(t[nt]);
+              for (int nt = 0; nt < NT; ++nt) codes_split<kValues>(t[nt]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                   float& oo = o[nt][m][x];
-                  oo = oo * corr[nt][x & 1] + base[nt][x & 1] + t[nt][x] * (vsc[nt][x & 1] * (x < 2 ? 0x1p24f : 0x1p20f) * (F32 ? 0.5f : 1.f));
+                  oo = oo * corr[nt][x & 1] + base[nt][x & 1] + t[nt][x] * (vsc[nt][x & 1] * codes_unit<kValues>(x < 2));
                 }
             }
           }
