@@ -180,7 +180,7 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t* a) {
 // What a product's sum cuts off goes by the exponents of the operands as they are written, and a subnormal's
 // is that of the least normal number: 2^6 above 15 units of it. So sums that have to keep fp32's bits take the
 // codes with a multiplication more. KeysBf16: rows 0..7 times 2^4, as 8..15 have it (logits of queries with
-// elements 512 times the others' are off by 2^-22 of the sum of their magnitudes, without it 2^-18; 406 -> 413
+// elements 512 times the others' are off by 2^-22 of the sum of their magnitudes, without it 2^-18; 406 -> 411
 // us for 256 units x 65536 tokens, with all four registers 422). KeysF32: all times 2^15, normal numbers.
 // ValuesF32: so too, less 7.5 of each code. ValuesBf16: as they lie, for the weights are rounded to 2^-11.
 enum class Codes { KeysBf16, KeysF32, ValuesBf16, ValuesF32 };
