@@ -653,7 +653,8 @@ nosa_status nosa_rotate(const nosa_config* cfg, const nosa_rope* rope, const int
  *   bytes [69 d, +2 d) : zeros of the values, fp16, in the same order
  *   bytes [71 d, +256) : fp32 eviction logits of the 64 tokens
  *   then fp32 key scale, fp32 value scale, zeros to a multiple of 32 bytes.
- * Steps are not negative. (What a masked token's steps, zeros and codes hold does not
+ * Steps are not negative and, as the append makes them, below 2: larger ones overflow the
+ * attention's operands. (What a masked token's steps, zeros and codes hold does not
  * count, but costs the attention time where a value's step or zero is no number.)
  */
 size_t nosa_quant4_unit_bytes(const nosa_config* cfg);
@@ -698,9 +699,9 @@ nosa_status nosa_quant4_read(const nosa_config* cfg, const void* units, int64_t 
  * nosa_quant_attention over 4-bit units, with the queries rotated on the way (rope NULL: as
  * they are): a row's products take bit for bit what nosa_rotate makes of it. positions as
  * above, for n_queries tokens of each request; those past q_len are not read. Logits are
- * held as precisely as with nosa_quant_attention (the product of a query element and a key's
- * step is exact, for fp32 as three terms of 8 bits, but for at most 2^-39 of the largest
- * element of the row); a weight times the step of a value is rounded to 11 bits (bf16 calls)
+ * fp32 sums, off by at most 2^-20 of the sum over dims of |q| (step n + |zero|) (the product of a
+ * query element and a key's step is exact, for fp32 as three terms of 8 bits, but for at most 2^-39
+ * of the largest element of the row); a weight times the step of a value is rounded to 11 bits (bf16 calls)
  * or 22 (fp32). The largest element of a query times that of a block's keys has to be below
  * 2^120, a value below 2^118. With rope the workspace also holds the rotated queries. Other
  * arguments and rules as nosa_quant_attention.

@@ -75,7 +75,7 @@
 // masks where every row sees the block 410 (404); the zeros' product as the codes' first summand 415
 // (407); fp16 codes with two masks and a shift more 407 (399). A join that fits beside the stream (its
 // registers or its threads cut) took 2 to 4 us longer than one that starts after it. 128 rows over 16
-// units of 16384 tokens take 101 us, 32 over 32 of 8200 39.6, in fp32 64.
+// units of 16384 tokens take 104 us, 32 over 32 of 8200 39.6, in fp32 64.
 #pragma once
 
 #include "k_quant4.cuh"
