@@ -663,15 +663,14 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 
   if (warp == W) {
     // ---- producer: lane s owns stage s and brings it items s, s + STAGES, ... ----
-    int it = lane, u = s_unit, tile = 0, j = 0, nb = 0, idx = -1;
+    int it = lane, u = s_unit, tile = 0, j = 0, nb = -1, idx = -1;
     long long pos = g0 - s_before + it;  // from the start of unit u
     auto seek = [&]() {                  // (u, tile, j) of the item, and its table entry
       if (it >= items) return;
-      for (;;) {
+      while (pos >= (long long)nb * p.tiles) {  // (the length is read where a unit begins)
+        pos -= (long long)max(0, nb) * p.tiles;
+        u += nb >= 0;
         nb = max(0, quant_len<kEarly>(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
-        if (pos < (long long)nb * p.tiles) break;
-        pos -= (long long)nb * p.tiles;
-        ++u;
       }
       tile = (int)pos / nb;
       j = (int)pos - tile * nb;
