@@ -37,7 +37,7 @@
 //
 // Measured on GB300 (bytes that the call cannot do without / time, of the measured copy
 // rate of 6793 GB/s):
-//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   668 us   96 %
+//   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   657 us   98 %
 //   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB   100 us   85 %
 //   8 units x 131071 tokens, 4 rows                       0.27 GB    50 us   81 %
 //   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    30 us   69 %
@@ -61,15 +61,16 @@
 // all alike. Queries are turned by their positions in a launch before the stream, beside which the
 // stream starts: only its helper waits for them.
 // Measured on GB300:
-//   256 units x 65536 tokens, d = 128, 4 rows             2.45 GB   411 us   88 %
-//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.33 GB    74 us   65 %
+//   256 units x 65536 tokens, d = 128, 4 rows             2.45 GB   395 us   92 %
+//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.33 GB    73 us   66 %
 //   8 units x 131071 tokens, 4 rows                       0.15 GB    41 us   55 %
 //   64 units x 16384 tokens, d = 64, 2 rows               0.08 GB    28 us   42 %
 //   1 unit x 2031 tokens, d = 64, fp32                    0.2 MB    9.2 us
 // With half the bytes the consumers bound the stream: a block takes a warp about 1000
 // instructions (320 of them make operands of codes), eight warps issue 1.9 a cycle, and with
 // all units in L2 the call takes 3 % less. What was tried against it for 256 units x 65536 tokens
-// (before the keys' codes were raised, which costs 5 us): twelve
+// (before the keys' codes were raised, which costs 5 us, and the producer read its table ahead,
+// which gives 16): twelve
 // consumer warps that take registers from the producer's warpgroup, with the parts in the ring
 // 385 us, but 89 (73) for the ragged units, whose ends the longer joins held up; logits without
 // masks where every row sees the block 410 (404); the zeros' product as the codes' first summand 415
@@ -663,26 +664,38 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 
   if (warp == W) {
     // ---- producer: lane s owns stage s and brings it items s, s + STAGES, ... ----
-    int it = lane, u = s_unit, tile = 0, j = 0, nb = -1, idx = -1;
-    long long pos = g0 - s_before + it;  // from the start of unit u
-    auto seek = [&]() {                  // (u, tile, j) of the item, and its table entry
-      if (it >= items) return;
-      while (pos >= (long long)nb * p.tiles) {  // (the length is read where a unit begins)
-        pos -= (long long)max(0, nb) * p.tiles;
-        u += nb >= 0;
-        nb = max(0, quant_len<kEarly>(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
+    // The table's entries come 32 items at a time and 32 to 64 ahead of the first item that has no stage yet
+    // (which holds a fast warp back 64 items after the slowest): with an entry read by its stage's lane every turn
+    // of the loop waited for the last turn's reads (256 units x 65536 tokens 400 us, now 395; 8 bits 666, 657).
+    int next = lane, u = s_unit, nb = -1;
+    long long pos = g0 - s_before + lane;  // of item `next`, from the start of unit u
+    auto entry = [&]() {                   // the table's entry of item `next`; then the one 32 on
+      int idx = -1;
+      if (next < items) {
+        while (pos >= (long long)nb * p.tiles) {  // (the length is read where a unit begins)
+          pos -= (long long)max(0, nb) * p.tiles;
+          u += nb >= 0;
+          nb = max(0, quant_len<kEarly>(p.lens, u, p.max_blocks, nullptr, false)) / kQB;
+        }
+        const int j = (int)pos % nb;
+        idx = kEarly ? __ldcg(p.tab + (long long)u * p.max_blocks + j) : p.tab[(long long)u * p.max_blocks + j];
       }
-      tile = (int)pos / nb;
-      j = (int)pos - tile * nb;
-      idx = kEarly ? __ldcg(p.tab + (long long)u * p.max_blocks + j) : p.tab[(long long)u * p.max_blocks + j];
+      next += 32;
+      pos += 32;
+      return idx;
     };
-    if (lane >= STAGES) it = items;
-    seek();
-    int fills = 0;
+    int cur = -1, ahead = entry(), base = -32;  // entries of items base + lane and base + 32 + lane
+    int it = lane < STAGES ? lane : items, fills = 0;
     uint64_t since = global_ns();
     for (int spin = 0; __any_sync(0xffffffffu, it < items); ++spin) {
       bool moved = false;
-      if (it < items && (fills == 0 || mbar_test(&empty[lane], (uint32_t)((fills - 1) & 1)))) {
+      const bool now = it < items && it < base + 64 && (fills == 0 || mbar_test(&empty[lane], (uint32_t)((fills - 1) & 1)));
+      int idx = __shfl_sync(0xffffffffu, cur, it - base);
+      if (__any_sync(0xffffffffu, now && it >= base + 32)) {
+        const int y = __shfl_sync(0xffffffffu, ahead, it - base);
+        if (it >= base + 32) idx = y;
+      }
+      if (now) {
         const bool bad = idx < 0 || (long long)idx >= p.n_units;
         null_s[lane] = bad;
         if (bad) {
@@ -694,9 +707,12 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
         }
         ++fills;
         it += STAGES;
-        pos += STAGES;
-        seek();
         moved = true;
+      }
+      if (__all_sync(0xffffffffu, it >= min(items, base + 32))) {
+        cur = ahead;
+        ahead = entry();
+        base += 32;
       }
       if (!__any_sync(0xffffffffu, moved)) __nanosleep(40);  // (leaves the issue slots to the others)
       if (__any_sync(0xffffffffu, moved)) {
