@@ -57,19 +57,19 @@
 // (codes_f16; some of them raised, codes_of). The queries times the steps are made once a block: a step has three bits, so the
 // product of a bf16 element (or of an 8-bit term of an fp32 one: there are three) is exact and
 // the logits are as good as fp32 sums of exact products. The weights, rounded to fp16, times the
-// values' steps are rounded once more. The sums with the zeros are a product more whose rows are
-// all alike. Queries are turned by their positions in a launch before the stream, beside which the
+// values' steps are rounded once more. The sums with the zeros are a product more: for keys its rows
+// are all alike, for values they are the two runs' (d = 128). Queries are turned by their positions in a launch before the stream, beside which the
 // stream starts: only its helper waits for them.
 // Measured on GB300:
-//   256 units x 65536 tokens, d = 128, 4 rows             2.45 GB   395 us   92 %
-//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.33 GB    73 us   66 %
-//   8 units x 131071 tokens, 4 rows                       0.15 GB    41 us   55 %
-//   64 units x 16384 tokens, d = 64, 2 rows               0.08 GB    28 us   42 %
+//   256 units x 65536 tokens, d = 128, 4 rows             2.45 GB   398 us   91 %
+//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.33 GB    74 us   65 %
+//   8 units x 131071 tokens, 4 rows                       0.15 GB    42 us   54 %
+//   64 units x 16384 tokens, d = 64, 2 rows               0.08 GB    29 us   40 %
 //   1 unit x 2031 tokens, d = 64, fp32                    0.2 MB    9.2 us
 // With half the bytes the consumers bound the stream: a block takes a warp about 1000
-// instructions (320 of them make operands of codes), eight warps issue 1.9 a cycle, and with
+// instructions (384 of them make operands of codes), eight warps issue 1.9 a cycle, and with
 // all units in L2 the call takes 3 % less. What was tried against it for 256 units x 65536 tokens
-// (before the keys' codes were raised, which costs 5 us, and the producer read its table ahead,
+// (before the codes were raised, which costs 5 us for the keys' and 3 for the values', and the producer read its table ahead,
 // which gives 16): twelve
 // consumer warps that take registers from the producer's warpgroup, with the parts in the ring
 // 385 us, but 89 (73) for the ragged units, whose ends the longer joins held up; logits without
@@ -178,21 +178,24 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t* a) {
   a[3] = __byte_perm(w, 0, 0x4341);
   a[2] = a[3] & 0x000F000Fu;
 }
-// What a product's sum cuts off goes by the exponents of the operands as they are written, and a subnormal's
-// is that of the least normal number: 2^6 above 15 units of it. So sums that have to keep fp32's bits take the
-// codes with a multiplication more. KeysBf16: rows 0..7 times 2^4, as 8..15 have it (logits of queries with
-// elements 512 times the others' are off by 2^-22 of the sum of their magnitudes, without it 2^-18; 406 -> 411
-// us for 256 units x 65536 tokens, with all four registers 422). KeysF32: all times 2^15, normal numbers.
-// ValuesF32: so too, less 7.5 of each code. ValuesBf16: as they lie, for the weights are rounded to 2^-11.
-enum class Codes { KeysBf16, KeysF32, ValuesBf16, ValuesF32 };
+// What a product's sum cuts off, always towards zero, goes by the exponents of the operands as they are written,
+// and a subnormal's is that of the least normal number: 2^10 times a code of 1 as it lies. So the codes take a
+// multiplication more. Bf16: rows 0..7 times 2^4, as 8..15 have it. Keys: logits of queries with elements 512
+// times the others' are off by 2^-22 of the sum of their magnitudes, without it 2^-18; 406 -> 411 us for 256
+// units x 65536 tokens, with all four registers 422. Values: codes are not negative, so what their sums lose is of
+// one sign and does not average out over the tokens as the output does. bf16 outputs over 131071 tokens of independent
+// values are off by 2.7e-4 of their norm beside their own rounding of 1.6e-3 (as at 4096: the weights' roundings) and
+// by less than 1e-4 to one side, without it by 5.5e-4 and 3.7e-4; 395 -> 407 us, of which the zeros' packed product
+// takes 8 back. (About the middle of the codes, as F32 takes them, which halves the weights' roundings too: 423.)
+// KeysF32: all times 2^15, normal numbers. ValuesF32: so too, less 7.5 of each code.
+enum class Codes { Bf16, KeysF32, ValuesF32 };
 template <Codes kind>
 __device__ __forceinline__ void codes_of(uint32_t w, uint32_t* a) {
   codes_f16(w, a);
-  if (kind == Codes::ValuesBf16) return;
-  const __half2 up = __float2half2_rn(kind == Codes::KeysBf16 ? 16.f : 32768.f);
+  const __half2 up = __float2half2_rn(kind == Codes::Bf16 ? 16.f : 32768.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (kind == Codes::KeysBf16 && i % 2) continue;
+    if (kind == Codes::Bf16 && i % 2) continue;
     const __half2 x = *reinterpret_cast<const __half2*>(&a[i]);
     const __half2 h = kind == Codes::ValuesF32 ? __hfma2(x, up, __float2half2_rn(i % 2 ? -7.5f * 17.f / 512.f : -7.5f / 512.f)) : __hmul2(x, up);
     a[i] = *reinterpret_cast<const uint32_t*>(&h);
@@ -201,12 +204,12 @@ __device__ __forceinline__ void codes_of(uint32_t w, uint32_t* a) {
 // What one stands for in such a tile's product, rows 0..7 (low) and 8..15, after codes_split.
 template <Codes kind>
 __device__ __forceinline__ constexpr float codes_unit(bool low) {
-  return kind == Codes::KeysBf16 ? 0x1p20f : kind == Codes::ValuesBf16 ? (low ? 0x1p24f : 0x1p20f) : (low ? 0x1p9f : 0x1p5f);
+  return kind == Codes::Bf16 ? 0x1p20f : low ? 0x1p9f : 0x1p5f;
 }
 // Takes the codes of rows 0..7 off rows 8..15.
 template <Codes kind>
 __device__ __forceinline__ void codes_split(float* d) {
-  constexpr float f = kind == Codes::KeysBf16 ? 0x1p-4f : 1.f;
+  constexpr float f = kind == Codes::Bf16 ? 0x1p-4f : 1.f;
   d[2] -= d[0] * f;
   d[3] -= d[1] * f;
 }
@@ -777,7 +780,7 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
   }
 
   // ---- consumers ----
-  constexpr Codes kKeys = F32 ? Codes::KeysF32 : Codes::KeysBf16, kValues = F32 ? Codes::ValuesF32 : Codes::ValuesBf16;
+  constexpr Codes kKeys = F32 ? Codes::KeysF32 : Codes::Bf16, kValues = F32 ? Codes::ValuesF32 : Codes::Bf16;
   const int g = lane >> 2, c = lane & 3;
   const int tok = 4 * (g >> 1) + (g & 1);  // this lane's tokens of a slice: tok and tok + 2
   const int is = warp % IS, rg = warp / IS;
@@ -1065,20 +1068,33 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
           }
         } else {
           const uint4* vc = reinterpret_cast<const uint4*>(unit + 32 * D) + lane;
+          // the weights with the zeros: rows 0..7 of the tile are the first run of 64 dims, 8..15 the last
+          float tz[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) tz[nt][0] = tz[nt][1] = tz[nt][2] = tz[nt][3] = 0.f;
+          if constexpr (!F32) {
+#pragma unroll
+            for (int w2 = 0; w2 < SL / 2; ++w2) {
+              const uint4* vzeros = reinterpret_cast<const uint4*>(unit + quant4_vzero_off(D) + c * 32) + w2;
+              const uint4 z4[2] = {vzeros[0], vzeros[(D - 64) / 8]};
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t za[4] = {word_of(z4[0], 2 * y), word_of(z4[1], 2 * y), word_of(z4[0], 2 * y + 1), word_of(z4[1], 2 * y + 1)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16816(tz[nt], za, pb[nt][2 * w2 + y][0], pb[nt][2 * w2 + y][1]);
+              }
+            }
+          }
 #pragma unroll
           for (int r = 0; r < D / 64; ++r) {  // runs of 64 dims
             const uint4* vsteps = reinterpret_cast<const uint4*>(unit + quant4_vstep_off(D) + r * 128 + c * 32);
-            const uint4* vzeros = reinterpret_cast<const uint4*>(unit + quant4_vzero_off(D) + r * 128 + c * 32);
-            const uint4 s4[2] = {vsteps[0], vsteps[1]}, z4[2] = {vzeros[0], vzeros[1]};
+            const uint4 s4[2] = {vsteps[0], vsteps[1]};
             uint32_t ps[NT][SL][2], pt[F32 ? NT : 1][SL][2];  // weights times steps
-            float base[NT][2];                                // ... with the zeros
+            float base[NT][2];                                // ... with the zeros (fp32: the middles)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float tz[4] = {};
 #pragma unroll
               for (int w = 0; w < SL; ++w) {
-                const uint32_t z0 = word_of(z4[w / 2], 2 * (w % 2)), z1 = word_of(z4[w / 2], 2 * (w % 2) + 1), za[4] = {z0, z0, z1, z1};
-                if constexpr (!F32) mma16816(tz, za, pb[nt][w][0], pb[nt][w][1]);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   const uint32_t st = word_of(s4[w / 2], 2 * (w % 2) + y);
@@ -1093,8 +1109,8 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
                   }
                 }
               }
-              base[nt][0] = (F32 ? mid[F32 ? r : 0][0] : tz[0]) * vsc[nt][0];
-              base[nt][1] = (F32 ? mid[F32 ? r : 0][1] : tz[1]) * vsc[nt][1];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) base[nt][x] = (F32 ? mid[F32 ? r : 0][x] : tz[nt][2 * r + x]) * vsc[nt][x];
             }
 #pragma unroll
             for (int m = 4 * r; m < 4 * r + 4; ++m) {
