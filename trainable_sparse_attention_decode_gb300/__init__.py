@@ -641,7 +641,8 @@ class NosaRope:
 
 def nosa_rope(table, axes=None, interleaved=False) -> NosaRope:
     """A rotation from table [positions][rot_dim / 2][2] fp32 (cosine and sine of each pair), the
-    axis of each pair (None: one axis), and the pairing: halves, or neighbours if interleaved."""
+    axis of each pair (None: axis 0), and the pairing: halves, or neighbours if interleaved. Positions
+    have the axes that the pairs use or more, up to 4."""
     return NosaRope(table, axes, interleaved)
 
 
@@ -657,7 +658,9 @@ def _turn(rope, positions, device, batch, n, torch):
         raise ValueError(f"the rope's table is on cuda:{rope.device}, the configuration's device is cuda:{device}")
     if positions is None:
         raise ValueError("positions is required")
-    axes = rope.n_axes
+    axes = rope.n_axes  # that the pairs use; positions may have more
+    if positions.ndim == 3 and axes < positions.shape[0] <= 4:
+        axes = positions.shape[0]
     return rope.ref, _arg(positions, device, (batch, n) if axes == 1 and positions.ndim == 2 else (axes, batch, n),
                           torch.int32, "positions")
 
