@@ -88,15 +88,23 @@ cudaError_t rotate_variant(const Shape& s, const RotateArgs& a, int full, cudaSt
 cudaError_t launch_rotate(const Shape& s, const RotateArgs& a, cudaStream_t stream) {
   const int heads = a.heads[0] + a.heads[1];
   if (a.rows * heads == 0) return cudaSuccess;
-  // Few rows: a thread for each head (500 tokens of 40 heads: 5.0 us, several heads a thread 3.5; 32
-  // tokens 2.3 and 2.9). Five heads a thread where they divide, else four (40 heads: five 110 us, four
-  // 139; 32 heads: five 101, four 95).
+  // Few chunks: a thread for each head. Chunks, us by threads for each head (several heads a thread), 40 heads
+  // of 128: 10 000 2.0 (2.8), 50 000 2.5 (2.8), 77 000 3.0 (2.9), 100 000 3.2 (3.2), 150 000 4.7 (4.2), 400 000 8.8
+  // (6.2); 8 heads of 128 and 24 of 64 cross there too.
   const long long work = a.rows * heads * (s.d / 16);
   const bool few = work <= 152 * 512;
   const int full = few ? 256 : work <= 4 << 20 ? kRotateMany : kRotateMany / 2;
   if (s.dtype == 0) return few ? rotate_variant<float, 1>(s, a, full, stream) : rotate_variant<float, 2>(s, a, full, stream);
   if (few) return rotate_variant<__nv_bfloat16, 1>(s, a, full, stream);
-  return heads % 5 == 0 ? rotate_variant<__nv_bfloat16, 5>(s, a, full, stream) : rotate_variant<__nv_bfloat16, 4>(s, a, full, stream);
+  // Four heads a thread, or five where that saves the warps a round: one of 32 threads takes 32 / per tokens, or a
+  // token in several rounds. us (four heads, five) for 270 MB, of d = 128 5 heads 55 46, 8 47 48, 9 60 48, 16 47 47, 20
+  // 62 45, 24 55 57, 25 50 59, 32 46 47, 36 63 44, 40 58 44, 48 51 55, 64 44 48 and, against the rule, 60 46 49; of d = 64
+  // 9 52 48, 32 46 51, 36 67 47, 40 61 44, 64 45 51 and, against it, 24 54 48, 25 53 47.
+  const auto rounds = [&](int heads_each) {  // of 32 tokens
+    const int per = (heads + heads_each - 1) / heads_each * (s.d / 16);
+    return per <= 32 ? 32 / (32 / per) : (per + 31) / 32 * 32;
+  };
+  return rounds(5) < rounds(4) ? rotate_variant<__nv_bfloat16, 5>(s, a, full, stream) : rotate_variant<__nv_bfloat16, 4>(s, a, full, stream);
 }
 
 }  // namespace nosa
