@@ -1233,13 +1233,14 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
   __shared__ float m_s[kQcRows], l_s[kQcRows], tw_s[kQcRows];
   __shared__ float2 st_s[kQcRows];
   __shared__ int2 scan_s[kQcThreads / 32];
-  // The values of a short tail by way of shared memory, so that a warp has a row, token by token,
-  // instead of a thread a column of all rows, reduced by shuffles. Measured, us (by columns): 32 rows over
-  // 32 units of 8200 tokens, 8 in the tail, 38.6 (43.4); 4 rows over 8 units of 131071, 63 in the tail,
-  // 41.7 (41.0).
+  // The values of the tail by way of shared memory, so that a warp has a row, token by token, instead of
+  // a thread a column of all rows, reduced by shuffles: the one grows with the tokens, the other with the
+  // rows, and they meet at about 16 + 11 rows tokens. us by rows (by columns) over 32 units of 8192 tokens and a tail
+  // of 8, 24, 40 and 63, d = 128: 1 row 19.1 (19.2) 19.4 (19.3) 20.1 (19.8) 21.3 (20.2); 2 rows 40 20.8 (20.8), 63
+  // 22.1 (21.4); 3 rows 40 21.2 (21.5), 63 22.7 (22.1); 4 rows 19.7 (21.9) 20.3 (22.1) 21.4 (22.5) 22.9 (23.0); 8 rows
+  // 40 23.8 (26.1), 63 25.9 (26.6); 32 rows 39.5 (44.3) 40.6 (44.3) 41.9 (44.6) 44.0 (45.1); d = 64 alike.
   constexpr bool kByRow = BITS == 4 && ELT == 2;
-  constexpr int kByRowMost = 24;
-  __shared__ __align__(16) T v_s[kByRow ? kByRowMost * D : 1];
+  __shared__ __align__(16) T v_s[kByRow ? kQB * D : 1];
   griddep_launch_dependents();
   const int vu = blockIdx.x, u = vu / p.tiles, tile = vu % p.tiles, b = u / p.Hkv, h = u % p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1318,7 +1319,7 @@ __global__ void __launch_bounds__(kQcThreads, kQcPerSm<T, D>) quant_combine_kern
     }
     __syncthreads();
     if (kLate) load_values();
-    const bool by_row = kByRow && nt <= kByRowMost;
+    const bool by_row = kByRow && nt <= 16 + 11 * live;
     if (by_row) {
 #pragma unroll
       for (int i = 0; i < TPT; ++i)
