@@ -699,11 +699,13 @@ nosa_status nosa_quant4_read(const nosa_config* cfg, const void* units, int64_t 
  * nosa_quant_attention over 4-bit units, with the queries rotated on the way (rope NULL: as
  * they are): a row's products take bit for bit what nosa_rotate makes of it. positions as
  * above, for n_queries tokens of each request; those past q_len are not read. Logits are
- * fp32 sums, off by at most 2^-20 of the sum over dims of |q| (step n + |zero|) (the product of a
- * query element and a key's step is exact, for fp32 as three terms of 8 bits, but for at most 2^-39
- * of the largest element of the row); a weight times the step of a value is rounded to 11 bits (bf16 calls)
- * or 22 (fp32). The largest element of a query times that of a block's keys has to be below
- * 2^120, a value below 2^118. With rope the workspace also holds the rotated queries. Other
+ * fp32 sums of products of which one of a query element and a key's step is exact (for fp32 as three
+ * terms of 8 bits), but for at most 2^-39 of the largest element of the row. They are off by at most
+ * 2^-18 of the sum over dims of |q| (15 step + |zero|) with the steps and zeros of the token's block: sixteen
+ * products are cut off at the size of the largest, so a token whose own terms are far smaller than those of
+ * its block has fewer bits. A weight, and its product with the step of a value, is rounded to 11 bits (bf16
+ * calls) or 22 (fp32). The largest element of a query times that of a block's keys has to be below 2^120, a value
+ * below 2^118. With rope the workspace also holds the rotated queries. Other
  * arguments and rules as nosa_quant_attention.
  */
 size_t nosa_quant4_attention_workspace_bytes(const nosa_config* cfg, int32_t max_blocks,

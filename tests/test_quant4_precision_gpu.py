@@ -1,11 +1,12 @@
-"""What the 4-bit block cache's attention keeps of the bits of its outputs over long caches."""
+"""What the 4-bit block cache's attention keeps of the bits of its logits and outputs: long caches, lopsided
+queries, large values."""
 import numpy as np
 import pytest
 import torch
 
 from oracle import quant4_oracle as Q
 from test_quant4_gpu import Cache
-from test_quant_gpu import DT, f64, query
+from test_quant_gpu import B, DT, f64, query
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +65,62 @@ def test_bf16_outputs_are_not_off_to_one_side(d):
         dims = np.arange(d) % 16 // 8 == half
         noise = 4 * np.sqrt((own[:, dims] ** 2).mean() / own[:, dims].size)
         assert abs(err[:, dims].mean()) <= lost + noise, half
+
+
+def one_block(d, codes, steps, zeros, token):
+    """The image of a block of keys `codes` [64][d] with these steps and zeros [d], values 0, in which one token counts."""
+    img = np.zeros((1, Q.unit_bytes(d)), np.uint8)
+    (kb, ks), _ = Q.code_places(d)
+    for half in (0, 4):
+        own = ks == half
+        img[0, kb[own]] |= (codes[own] << half).astype(np.uint8)
+    p = Q.places(d)
+    img[0, p[0]] = steps.astype(np.float16).view(np.uint16) >> 8
+    bits = zeros.astype(np.float16).view(np.uint16)
+    img[0, p[1]], img[0, p[1] + 1] = bits & 255, bits >> 8
+    e = np.full(B, -np.inf, np.float32)
+    e[token] = 0
+    img[0, 71 * d:71 * d + 4 * B + 8] = np.concatenate([e, np.ones(2, np.float32)]).view(np.uint8)
+    return img
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", ["one channel", "one channel, mostly zeros", "every 16th channel", "zeros of all sizes"])
+def test_single_logits_of_lopsided_queries(dtype, d, kind):
+    """A logit is off by at most 2^-18 of the sum over dims of |q| (15 step + |zero|), also of a token whose own sum is far
+    smaller: channels whose query element is up to 2^24 times the others', and whose codes and zeros may be 0.
+
+    A product of sixteen is cut off 2^-25 below the largest, whose operand's exponent is written as 2^6 for a code
+    at most: with M the largest |q| step of the sixteen dims, 17 terms of 2^-19 M, and a seventeenth of that for the
+    neighbour's code, for d / 16 sums: 2^-14.8 of the sum of the M, of which the bound's sum is at least 15 times: 2^-18.7.
+    The zeros' products add 17 * 2^-25, in fp32 the partial sums of three terms 3 d / 16 * 2^-24 (and the codes, as
+    normal numbers, less), and the logit its last three roundings."""
+    U = 64
+    for boost in range(0, 25, 3):
+        rng = np.random.default_rng(boost)
+        codes = np.where(rng.random((B, d)) < 0.5, 15, rng.integers(0, 16, size=(B, d)))
+        steps, zeros = np.full(d, 0.5), np.zeros(d)
+        big = np.arange(d) == 3
+        if kind == "one channel":
+            codes[:, 3] = np.where(np.arange(B) == 0, 15, rng.integers(1, 16, size=B))
+        elif kind == "one channel, mostly zeros":
+            codes[:, 3] = np.where(np.arange(B) == 0, 15, rng.integers(0, 2, size=B) * (np.arange(B) % 2))
+        elif kind == "every 16th channel":
+            codes[0::3], codes[1::3] = 15, 0
+            big = np.arange(d) % 16 == 0
+        else:
+            zeros = f64(torch.as_tensor(rng.normal(size=d)).half())
+        c = Cache(rng, dtype, U, 8, 1, d, [B] * U, masked=0.0)
+        c.images = np.concatenate([one_block(d, codes, steps, zeros, t) for t in range(U)])
+        c.tab = np.arange(U, dtype=np.int32)[:, None].copy()
+        c.upload()
+        q = np.abs(rng.normal(size=(1, 1, 8, d))) + 0.3
+        q[..., 4:] *= np.where(rng.random(d - 4) < 0.2, -1, 1)
+        q = torch.as_tensor(np.repeat(np.where(big, q * 2.0 ** boost, q), U, 0)).to(DT[dtype]).cuda()
+        out, lse, status = c.run(q)
+        assert status == 0
+        rows = f64(q)[0, 0]
+        want = rows @ (codes * steps + zeros).T / np.sqrt(d)
+        most = np.abs(rows) @ (15 * steps + np.abs(zeros)) / np.sqrt(d)
+        assert np.all(np.abs(f64(lse)[:, 0].T - want) <= 2.0 ** -18 * most[:, None] + 2.0 ** -22 * np.abs(want)), boost
