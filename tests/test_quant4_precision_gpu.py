@@ -124,3 +124,20 @@ def test_single_logits_of_lopsided_queries(dtype, d, kind):
         want = rows @ (codes * steps + zeros).T / np.sqrt(d)
         most = np.abs(rows) @ (15 * steps + np.abs(zeros)) / np.sqrt(d)
         assert np.all(np.abs(f64(lse)[:, 0].T - want) <= 2.0 ** -18 * most[:, None] + 2.0 ** -22 * np.abs(want)), boost
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64), ("f32", 128), ("bf16", 64)])
+def test_values_as_large_as_the_tokens_allow(dtype, d):
+    """Values whose number times their size stays below 2^126 do not leave fp32's range in the sums, and neither in the tail."""
+    rng = np.random.default_rng(1)
+    n = 4096 - 10
+    c = Cache(rng, dtype, 1, 4, 1, d, [n], masked=0.0)
+    v = 2.0 ** 113 * rng.uniform(1.0, 1.98, size=(len(c.images), B, d))
+    c.images = Q.encode(rng.normal(size=v.shape), v, np.zeros((len(v), B)))
+    c.tv = f64(torch.as_tensor(2.0 ** 113 * rng.uniform(1.0, 1.98, size=c.tv.shape)).to(DT[dtype]))
+    c.te[:] = 0
+    c.upload()
+    q = torch.zeros(1, 1, 4, d, dtype=DT[dtype], device="cuda")
+    out, lse, status = c.run(q)
+    assert status == 0
+    c.check(q, out, lse)
