@@ -3,9 +3,9 @@
 //
 // Both read and write everything once. Reading back is bound by HBM (GB300: 4096 blocks of
 // d = 128 in bf16, 174 MB, 28.7 us = 89 % of the measured copy rate; fp32, 307 MB, 46.7 us = 97 %).
-// Appending is bound by its instructions: the same blocks, 174 MB, 59 us = 43 % (without a
-// rotation 56; fp32 86 us = 53 %), about 1100 of a thread and block at 2.4 a cycle; of the 59 us
-// the loads by themselves take 38 (rotation: 7), the extremes 5, the codes and their way out 17. Tried: keys and
+// Appending is bound by its loads' latency and by its instructions together: the same blocks, 174 MB, 59 us
+// = 43 % (without a rotation 56; fp32 86 us = 53 %). The loads by themselves take 38 (rotation: 7), the extremes
+// 5, the codes and their way out 17; a block takes 16 warps 700 instructions each, at 2.5 a cycle. Tried: keys and
 // values by one CTA 58 us (fp32 90), CTAs that stay and load the next block while they work on one
 // 69 to 80, 4 or 6 CTAs an SM for 5 64 and 66. A token of 32 requests of 8 heads, every fourth of
 // which completes a block: 6.0 us, latency.

@@ -17,7 +17,7 @@
 //             leave their parts to a helper warp, which joins them and has the next
 //             unit's queries ready, and go on.
 //   combine : a CTA per unit and 8 rows attends to the tail in fp32 while the stream
-//             still runs, then joins the unit's parts.
+//             still runs, where it fits beside it (see kQcPerSm), then joins the unit's parts.
 //   weights : with accumulated weights, what the stream noted for each block is added
 //             up relative to the rows' final sums: by the join where one CTA has all
 //             rows of a unit (up to 8) and the table is short, else by a launch of its own.
@@ -38,15 +38,15 @@
 // Measured on GB300 (bytes that the call cannot do without / time, of the measured copy
 // rate of 6793 GB/s):
 //   256 units x 65536 tokens, d = 128, 4 rows, weights   4.37 GB   657 us   98 %
-//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB   100 us   85 %
-//   8 units x 131071 tokens, 4 rows                       0.27 GB    50 us   81 %
+//   128 units x 1 .. 32768 tokens, 3 rows, weights        0.58 GB   100 us   86 %
+//   8 units x 131071 tokens, 4 rows                       0.27 GB    49 us   82 %
 //   64 units x 16384 tokens, d = 64, 2 rows               0.14 GB    30 us   69 %
 //   1 unit x 2031 tokens, d = 64, fp32                    0.3 MB    8.1 us
 // The stream itself runs at the copy rate; what is left is fixed: 3.75 us until the
 // first unit has landed (lengths, table, unit: three dependent reads), about 4 us between
 // the first and the last CTA to end, 1.5 us for the last join inside a CTA, 3 us for the
 // join launch after it and 2.5 us for the weights'. With 32 rows (8 drafted tokens of
-// 4 heads, 32 units of 8200 tokens: 41 us; 128 rows over 16 units of 16384 tokens: 98 us)
+// 4 heads, 32 units of 8200 tokens: 41 us; 128 rows over 16 units of 16384 tokens: 97 us)
 // the products' instructions bound it: about 1300 of a warp and block at 1.7 a cycle, six
 // consumer warps being all that the outputs' registers leave room for.
 //
@@ -66,7 +66,7 @@
 //   8 units x 131071 tokens, 4 rows                       0.15 GB    42 us   54 %
 //   64 units x 16384 tokens, d = 64, 2 rows               0.08 GB    29 us   40 %
 //   1 unit x 2031 tokens, d = 64, fp32                    0.2 MB    9.2 us
-// With half the bytes the consumers bound the stream: a block takes a warp about 1000
+// With half the bytes the consumers bound the stream: a block takes a warp about 1050
 // instructions (384 of them make operands of codes), eight warps issue 1.9 a cycle, and with
 // all units in L2 the call takes 3 % less. What was tried against it for 256 units x 65536 tokens
 // (before the codes were raised, which costs 5 us for the keys' and 3 for the values', and the producer read its table ahead,
@@ -76,7 +76,7 @@
 // masks where every row sees the block 410 (404); the zeros' product as the codes' first summand 415
 // (407); fp16 codes with two masks and a shift more 407 (399). A join that fits beside the stream (its
 // registers or its threads cut) took 2 to 4 us longer than one that starts after it. 128 rows over 16
-// units of 16384 tokens take 104 us, 32 over 32 of 8200 39.6, in fp32 64.
+// units of 16384 tokens take 105 us, 32 over 32 of 8200 39.6, in fp32 65.
 #pragma once
 
 #include "k_quant4.cuh"
@@ -1209,8 +1209,8 @@ __global__ void __launch_bounds__(QGeom<D, NT, RG, F32, BITS>::BOUND, 1) quant_s
 
 // ---------------------------------------------------------------------------
 // Tail attention and the join. Grid (units x tiles, row groups of 8, z): a CTA writes
-// d / z dims of 8 rows. Before the stream has finished: the tail in fp32, its keys and
-// values in registers. After: every thread merges its share
+// d / z dims of 8 rows. Before the stream has finished, where the CTA fits beside it: the tail in
+// fp32, its keys and values in registers. After: every thread merges its share
 // of the unit's parts for four dims of a row, the shares join in shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kQcRows = 8;
@@ -1220,7 +1220,8 @@ constexpr int kQcRows = 8;
 // fp32): the values are then loaded after the keys are done with. Measured on GB300, us
 // (64 registers): 32 units x 1000 tokens 10.0 (14.3), 128 x 3000 17.3 (21.8), fp32 8 x 3000
 // 9.2 (15.0). (At 40 registers 20 bytes spill, outside the loops.) At d = 128 there is room for
-// 80 beside a bf16 stream, and the values come along with the keys.
+// 80 beside an 8-bit bf16 stream, and the values come along with the keys. Beside a 4-bit stream of d = 128,
+// ten warps of 168 registers, beside one of more than 8 rows and beside an fp32 one of d = 128 it does not fit.
 template <typename T, int D> constexpr int kQcPerSm = D == 64 ? (sizeof(T) == 4 ? 6 : 5) : 3;
 
 template <typename T, int D, int BITS>
