@@ -706,7 +706,7 @@ nosa_status nosa_quant4_read(const nosa_config* cfg, const void* units, int64_t 
  * its block has fewer bits. A weight, and its product with the step of a value, is rounded to 11 bits (bf16
  * calls) or 22 (fp32). The largest element of a query times that of a block's keys has to be below 2^120. Values
  * are summed with the row's largest weight as 1 before the sum is divided: a value times the number of tokens
- * that the row sees has to be below 2^126. With rope the workspace also holds the rotated queries. Other
+ * of its unit has to be below 2^126. With rope the workspace also holds the rotated queries. Other
  * arguments and rules as nosa_quant_attention.
  */
 size_t nosa_quant4_attention_workspace_bytes(const nosa_config* cfg, int32_t max_blocks,

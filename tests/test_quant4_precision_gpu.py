@@ -127,17 +127,19 @@ def test_single_logits_of_lopsided_queries(dtype, d, kind):
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64), ("f32", 128), ("bf16", 64)])
-def test_values_as_large_as_the_tokens_allow(dtype, d):
-    """Values whose number times their size stays below 2^126 do not leave fp32's range in the sums, and neither in the tail."""
-    rng = np.random.default_rng(1)
-    n = 4096 - 10
+@pytest.mark.parametrize("n,T", [(4096 - 10, 1), (64, 1), (64, 64), (4, 2)])
+def test_values_as_large_as_the_tokens_allow(dtype, d, n, T):
+    """Values whose number in the unit times their size stays below 2^126 do not leave fp32's range in the sums, where a
+    row sees all of the tokens, one of them, or only a tail."""
+    rng = np.random.default_rng(n)
     c = Cache(rng, dtype, 1, 4, 1, d, [n], masked=0.0)
-    v = 2.0 ** 113 * rng.uniform(1.0, 1.98, size=(len(c.images), B, d))
+    size = 2.0 ** (125 - np.ceil(np.log2(n)))
+    v = size * rng.uniform(1.0, 1.98, size=(len(c.images), B, d))
     c.images = Q.encode(rng.normal(size=v.shape), v, np.zeros((len(v), B)))
-    c.tv = f64(torch.as_tensor(2.0 ** 113 * rng.uniform(1.0, 1.98, size=c.tv.shape)).to(DT[dtype]))
+    c.tv = f64(torch.as_tensor(size * rng.uniform(1.0, 1.98, size=c.tv.shape)).to(DT[dtype]))
     c.te[:] = 0
     c.upload()
-    q = torch.zeros(1, 1, 4, d, dtype=DT[dtype], device="cuda")
+    q = torch.zeros(1, T, 4, d, dtype=DT[dtype], device="cuda")
     out, lse, status = c.run(q)
     assert status == 0
     c.check(q, out, lse)
